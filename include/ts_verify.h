@@ -388,6 +388,176 @@ TS_API int ts_kv_commit_path(void *k_cache, void *v_cache, int64_t kv_cap, int n
                              void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * 8-bit KV cache.  The context is kept in two parts: rows [0, n_q8) in 8
+ * bits, and the newest n_tail rows, followed by the draft tree's rows, as
+ * bf16 in a tail buffer.  Position j of the context is 8-bit row j for
+ * j < n_q8 and tail row tail_row0 + j - n_q8 after that; tree node a is
+ * tail row tail_row0 + n_tail + a.
+ *
+ * 8-bit rows come in blocks of TS_Q8_BLOCK (64).  A block of one KV head
+ * holds e4m3 codes and, for K and for V, one scale byte b: the rows are
+ * code * 2^(b - 127), and b = 255 makes the whole block NaN.  Attention and
+ * gather take any scale byte and any code but the two that e4m3 reserves
+ * for NaN (0x7F, 0xFF), which ts_kv_quantize_q8 never writes.
+ *
+ * A step: ts_rope_append puts the tree's rows behind the tail's context,
+ * ts_tree_verify_attn_q8 attends, ts_kv_commit_path (on the tail's buffers,
+ * advanced to tail_row0, with n_ctx = n_tail) keeps the accepted path;
+ * once n_tail reaches 64, ts_kv_quantize_q8 turns the tail's first 64 rows
+ * into the next block, and tail_row0 and n_q8 grow by 64.
+ *
+ *  k8, v8            device e4m3 [Hkv, q8_cap, D]; rows at or past n_q8 are
+ *                    not read.  May be NULL when n_q8 is 0.
+ *  k_scale, v_scale  device uint8 [Hkv, q8_cap / 64]; NULL as above.
+ *  q8_cap            rows per KV head, a multiple of 64, >= n_q8.
+ *  k_tail, v_tail    device bf16 [Hkv, tail_cap, D].
+ *  n_q8              a multiple of 64, >= 0.
+ *  n_tail            >= 0; any length, though a long tail is read at twice
+ *                    the bytes.
+ */
+#define TS_Q8_BLOCK 64
+typedef struct ts_q8_cache {
+    const void *k8;
+    const void *v8;
+    const uint8_t *k_scale;
+    const uint8_t *v_scale;
+    int64_t q8_cap;
+    const void *k_tail;
+    const void *v_tail;
+    int64_t tail_cap;
+    int64_t tail_row0;
+    int n_heads_kv;
+    int head_dim; /* 64 or 128 */
+    int n_q8;
+    int n_tail;
+} ts_q8_cache;
+
+/*
+ * Quantises full blocks of bf16 rows: rows [src_row0, src_row0 + n_rows) of
+ * k and v become 8-bit rows [dst_row, dst_row + n_rows).  A block's scale is
+ * 2^e, e the least integer >= -100 with max|x| <= 448 * 2^e; a code is
+ * x * 2^-e rounded to e4m3, nearest, ties to even.  A block that holds an
+ * infinity or a NaN gets scale byte 255 and zero codes.  Other rows and
+ * scales are not touched.
+ *
+ *  k, v              device bf16 [Hkv, src_cap, D].
+ *  n_rows, dst_row, q8_cap  multiples of 64; n_rows 0 does nothing.
+ */
+TS_API int ts_kv_quantize_q8(const void *k, const void *v, int64_t src_cap, int n_heads_kv,
+                             int head_dim, int64_t src_row0, int n_rows, void *k8, void *v8,
+                             uint8_t *k_scale, uint8_t *v_scale, int64_t q8_cap, int64_t dst_row,
+                             void *stream);
+
+/*
+ * ts_tree_verify_attn over an 8-bit cache: the same attention, with the
+ * context and the tree's rows as ts_q8_cache lays them out, and the output
+ * rounded once to bf16.  Optionally also the root node's base-2 scores over
+ * the context, as ts_tree_verify_attn_root_scores leaves them.
+ *
+ *  q            device bf16 [n_tree, Hq, D].
+ *  cache        HOST struct, read before the call returns;
+ *               tail_row0 + n_tail + n_tree <= tail_cap.
+ *  out          device bf16 [n_tree, Hq, D], written entirely.
+ *  root_scores_out  device fp32 [Hq, n_q8 + n_tail], or NULL.
+ *  workspace    device, >= ts_tree_verify_attn_q8_workspace_size(...) bytes.
+ * Other arguments as for ts_tree_verify_attn.  A position that a row does
+ * not see does not affect it, whatever its K and V hold; a row that sees a
+ * key or value row with an infinity or a NaN comes out as NaN.
+ */
+TS_API size_t ts_tree_verify_attn_q8_workspace_size(int n_heads_q, int n_heads_kv, int head_dim,
+                                                    int n_q8, int n_tail, int n_tree);
+TS_API int ts_tree_verify_attn_q8(const ts_q8_cache *cache, const void *q, int n_heads_q,
+                                  int n_tree, const int32_t *parent, float softmax_scale,
+                                  void *out, float *root_scores_out, void *workspace,
+                                  size_t workspace_bytes, void *stream);
+
+/*
+ * Copies selected context rows into a compact bf16 cache: row t of KV head
+ * g of k_partial and v_partial becomes context row idx[g, t], 8-bit rows as
+ * code * scale (exact in bf16 while in its normal range).
+ *
+ *  idx          device int32 [Hkv, n_keep]; an index outside [0, n_q8 +
+ *               n_tail) gives a zero row and TS_ERR_DEVICE_ARG in the
+ *               status word.
+ *  k_partial, v_partial  device bf16 [Hkv, partial_cap, D], rows [0, n_keep)
+ *               written.  n_keep 0 does nothing.
+ *  workspace    device, >= 256 bytes (the status header).
+ */
+TS_API int ts_kv_gather_q8(const ts_q8_cache *cache, const int32_t *idx, int n_keep,
+                           void *k_partial, void *v_partial, int64_t partial_cap,
+                           void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * ts_kv_select_from_scores on an 8-bit cache: the same positions from root
+ * scores over n_ctx = n_q8 + n_tail positions, their rows gathered as by
+ * ts_kv_gather_q8.  Workspace: ts_kv_select_from_scores_workspace_size(Hq,
+ * Hkv, n_ctx).
+ */
+TS_API int ts_kv_select_from_scores_q8(const float *root_scores, const ts_q8_cache *cache,
+                                       int n_heads_q, int n_sink, int budget, float *scores_out,
+                                       int32_t *idx_out, void *k_partial, void *v_partial,
+                                       int64_t partial_cap, void *workspace,
+                                       size_t workspace_bytes, void *stream);
+
+/*
+ * Rotary position embedding of a step's (or a prompt's) queries and keys,
+ * with the append of its K/V rows to a bf16 cache.  Token i has position
+ * pos0 + its depth in the draft tree (parent given) or pos0 + i (parent
+ * NULL: consecutive tokens, any number).  Pair j of a head is turned by
+ * angle = position * inv_freq[j], formed in 64 bits:
+ *   (u, w) -> mscale * (u cos - w sin, w cos + u sin),
+ * rounded once to bf16.  Pairs are elements (j, j + rot_dim / 2), or
+ * (2 j, 2 j + 1) when interleaved; elements at or past rot_dim pass through
+ * (without mscale).  Token i's turned key and its value become rows
+ * row0 + i of the cache; other rows are not touched.
+ *
+ *  q, k, v      device bf16, token rows q_stride, k_stride, v_stride elements
+ *               apart (multiples of 8, at least a row), heads and elements of
+ *               a token contiguous: slices of one projection's output serve.
+ *               n_heads_q 0 with q and q_out NULL appends without queries.
+ *  parent       HOST int32 [n_tok] as for ts_tree_verify_attn (n_tok <=
+ *               TS_MAX_TREE), or NULL.
+ *  pos0         >= 0.
+ *  inv_freq     device fp32 [rot_dim / 2]; may be NULL when rot_dim is 0.
+ *  rot_dim      even, 0 .. head_dim.
+ *  q_out        device bf16 [n_tok, Hq, D]; may be q itself when q is
+ *               contiguous, must not overlap it otherwise.
+ *  k_cache, v_cache  device bf16 [Hkv, kv_cap, D], not overlapping the
+ *               inputs; row0 + n_tok <= kv_cap.  n_tok 0 does nothing.
+ */
+TS_API int ts_rope_append(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                          const void *v, int64_t v_stride, int n_heads_q, int n_heads_kv,
+                          int head_dim, int n_tok, const int32_t *parent, int64_t pos0,
+                          const float *inv_freq, int rot_dim, int interleaved, float mscale,
+                          void *q_out, void *k_cache, void *v_cache, int64_t kv_cap,
+                          int64_t row0, void *stream);
+
+/*
+ * The frequency table of a rotary embedding (HOST code): inv_freq[j], j <
+ * rot_dim / 2, and the factor *mscale for ts_rope_append, computed in 64
+ * bits.  f_j = base^(-2 j / rot_dim), then by kind:
+ *  TS_ROPE_PLAIN       f_j
+ *  TS_ROPE_LINEAR      f_j / factor;                      params {factor}
+ *  TS_ROPE_WAVELENGTH  with t = ctx * f_j / (2 pi) turns over the original
+ *                      context and s = clamp((t - low) / (high - low), 0, 1):
+ *                      f_j (s + (1 - s) / factor);
+ *                      params {factor, low, high, ctx}, high > low
+ *  TS_ROPE_YARN        with r the clamped ramp from floor(i(fast)) to
+ *                      ceil(i(slow)), i(b) = rot_dim ln(ctx / (2 pi b)) /
+ *                      (2 ln base): f_j ((1 - r) + r / factor); *mscale =
+ *                      0.1 ln(factor) + 1 for a factor above 1;
+ *                      params {factor, ctx, fast, slow}
+ * (YaRN: Peng et al., "YaRN: Efficient Context Window Extension of Large
+ * Language Models", section 3.)  All params > 0, base > 1.
+ */
+#define TS_ROPE_PLAIN 0
+#define TS_ROPE_LINEAR 1
+#define TS_ROPE_WAVELENGTH 2
+#define TS_ROPE_YARN 3
+TS_API int ts_rope_inv_freq(float *inv_freq, int rot_dim, double base, int kind,
+                            const double *params, float *mscale);
+
+/*
  * n-gram reuse table.  TokenSwift drafts with the frequencies of the
  * n-grams already generated: phrases that occurred often are retrieved and
  * reused as draft candidates, and the table is updated with the tokens

@@ -29,10 +29,26 @@ EXPORTS = ("ts_status_string", "ts_version", "ts_tree_verify_attn_workspace_size
            "ts_ngram_table_bytes", "ts_ngram_init", "ts_ngram_update", "ts_ngram_topk",
            "ts_ngram_topk_prefix",
            "ts_ngram_count", "ts_ngram_size", "ts_selftest_bounded_wait",
-           "ts_penalize_accept_ex", "ts_penalize_sample_accept", "ts_kv_commit_path")
+           "ts_penalize_accept_ex", "ts_penalize_sample_accept", "ts_kv_commit_path",
+           "ts_kv_quantize_q8", "ts_tree_verify_attn_q8_workspace_size",
+           "ts_tree_verify_attn_q8", "ts_kv_gather_q8", "ts_kv_select_from_scores_q8",
+           "ts_rope_append", "ts_rope_inv_freq")
+
+TS_Q8_BLOCK = 64
+ROPE_KINDS = {"plain": 0, "linear": 1, "wavelength": 2, "yarn": 3}
 
 TS_PENALIZE_PATH_TOKENS = 1
 TS_ACCEPT_RANDOM_TIE = 2
+
+
+class _Q8Cache(ctypes.Structure):
+    """``ts_q8_cache``."""
+    _fields_ = [("k8", ctypes.c_void_p), ("v8", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("q8_cap", ctypes.c_int64),
+                ("k_tail", ctypes.c_void_p), ("v_tail", ctypes.c_void_p),
+                ("tail_cap", ctypes.c_int64), ("tail_row0", ctypes.c_int64),
+                ("n_heads_kv", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("n_q8", ctypes.c_int), ("n_tail", ctypes.c_int)]
 
 
 class TsError(RuntimeError):
@@ -87,6 +103,21 @@ def _lib():
                                                   ctypes.c_uint, ctypes.c_uint64, P, P, P, sz, P]
         lib.ts_kv_commit_path.restype = i32
         lib.ts_kv_commit_path.argtypes = [P, P, i64, i32, i32, i32, i32, P, P, sz, P]
+        lib.ts_kv_quantize_q8.restype = i32
+        lib.ts_kv_quantize_q8.argtypes = [P, P, i64, i32, i32, i64, i32, P, P, P, P, i64, i64, P]
+        lib.ts_tree_verify_attn_q8_workspace_size.restype = sz
+        lib.ts_tree_verify_attn_q8_workspace_size.argtypes = [i32] * 6
+        lib.ts_tree_verify_attn_q8.restype = i32
+        lib.ts_tree_verify_attn_q8.argtypes = [P, P, i32, i32, P, f32, P, P, P, sz, P]
+        lib.ts_kv_gather_q8.restype = i32
+        lib.ts_kv_gather_q8.argtypes = [P, P, i32, P, P, i64, P, sz, P]
+        lib.ts_kv_select_from_scores_q8.restype = i32
+        lib.ts_kv_select_from_scores_q8.argtypes = [P, P, i32, i32, i32, P, P, P, P, i64, P, sz, P]
+        lib.ts_rope_append.restype = i32
+        lib.ts_rope_append.argtypes = [P, i64, P, i64, P, i64, i32, i32, i32, i32, P, i64, P, i32,
+                                       i32, f32, P, P, P, i64, i64, P]
+        lib.ts_rope_inv_freq.restype = i32
+        lib.ts_rope_inv_freq.argtypes = [P, i32, ctypes.c_double, i32, P, P]
         lib.ts_kernel_launch_count.restype = ctypes.c_ulonglong
         lib.ts_kernel_launch_count.argtypes = []
         lib.ts_workspace_status.restype = i32
@@ -435,6 +466,347 @@ def kv_commit_path(k_cache, v_cache, n_ctx: int, n_tree: int, accept, workspace=
                                   _ws_bytes(workspace, dev), _stream(stream))
     _raise(rc, "ts_kv_commit_path")
     return k_cache, v_cache
+
+
+# ------------------------------------------------- rotation and the 8-bit cache
+def rope_inv_freq(rot_dim: int, base: float, kind: str = "plain", *params):
+    """Frequency table of a rotary embedding (``ts_rope_inv_freq``): ``(host
+    fp32 [rot_dim / 2], mscale)``.  kind and params: "plain"; "linear",
+    factor; "wavelength", factor, low, high, ctx; "yarn", factor, ctx, fast,
+    slow."""
+    import numpy as np
+    if kind not in ROPE_KINDS:
+        raise ValueError(f"kind must be one of {sorted(ROPE_KINDS)}")
+    want = (0, 1, 4, 4)[ROPE_KINDS[kind]]
+    if len(params) != want:
+        raise ValueError(f"{kind!r} takes {want} parameters")
+    out = np.zeros(max(int(rot_dim) // 2, 1), dtype=np.float32)
+    par = np.asarray(params + (1.0,), dtype=np.float64)
+    m = ctypes.c_float(0.0)
+    _raise(_lib().ts_rope_inv_freq(out.ctypes.data_as(ctypes.c_void_p), int(rot_dim), float(base),
+                                   ROPE_KINDS[kind], par.ctypes.data_as(ctypes.c_void_p),
+                                   ctypes.byref(m)), "ts_rope_inv_freq")
+    return torch.from_numpy(out[:int(rot_dim) // 2]), float(m.value)
+
+
+def _check_rows(name, t, heads, d, device):
+    """A bf16 [tokens, heads, D] tensor whose tokens may lie apart."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the call's other tensors on {device}")
+    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or t.shape[2] != d:
+        raise ValueError(f"{name} must be [tokens, heads, {d}]")
+    if (t.shape[2] > 1 and t.stride(2) != 1) or (t.shape[1] > 1 and t.stride(1) != d):
+        raise ValueError(f"{name}: the heads and elements of a token must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * d
+
+
+def rope_append(q, k, v, k_cache, v_cache, row0: int, pos0: int, inv_freq, parent=None,
+                interleaved: bool = False, mscale: float = 1.0, q_out=None, stream=None):
+    """Rotary embedding of q and k and the append of k and v to a bf16 cache
+    (``ts_rope_append``).
+
+    q: bf16 [n, Hq, D] or None; k, v: bf16 [n, Hkv, D] (slices of one
+    projection's output serve); k_cache, v_cache: bf16 [Hkv, kv_cap, D], rows
+    ``row0 ..`` written; inv_freq: fp32 [rot / 2] on the device, or None;
+    parent: the draft tree (host int32 [n]; position pos0 + depth) or None
+    (positions pos0 + i).  Returns the turned queries, bf16 [n, Hq, D].
+    """
+    dev = _call_device("k", k)
+    _check_dev("k_cache", k_cache, torch.bfloat16, dev)
+    _check_dev("v_cache", v_cache, torch.bfloat16, dev)
+    if k_cache.dim() != 3 or v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must be [Hkv, kv_cap, D]")
+    hkv, cap, d = k_cache.shape
+    ks, vs = _check_rows("k", k, hkv, d, dev), _check_rows("v", v, hkv, d, dev)
+    n = k.shape[0]
+    hq = qs = 0
+    if q is not None:
+        qs, hq = _check_rows("q", q, None, d, dev), q.shape[1]
+        if q_out is None:
+            q_out = torch.empty((n, hq, d), dtype=torch.bfloat16, device=dev)
+        _check_dev("q_out", q_out, torch.bfloat16, dev)
+        if tuple(q_out.shape) != (n, hq, d):
+            raise ValueError("q_out must have q's shape")
+    if v.shape[0] != n or (q is not None and q.shape[0] != n):
+        raise ValueError("q, k and v must have as many tokens")
+    rot = 0
+    if inv_freq is not None:
+        _check_dev("inv_freq", inv_freq, torch.float32, dev)
+        rot = 2 * inv_freq.numel()
+    par_p = None
+    if parent is not None:
+        par, par_p = _host_i32(parent)
+        if len(par) != n:
+            raise ValueError("parent must have one entry per tree node")
+    _raise(_lib().ts_rope_append(
+        _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, hq, hkv, d, n, par_p, int(pos0),
+        _ptr(inv_freq) if rot else None, rot, int(bool(interleaved)), float(mscale),
+        _ptr(q_out) if hq else None, _ptr(k_cache), _ptr(v_cache), cap, int(row0),
+        _stream(stream)), "ts_rope_append")
+    return q_out
+
+
+def _check_q8(k8, v8, k_scale, v_scale, device):
+    _check_dev("k8", k8, torch.float8_e4m3fn, device)
+    _check_dev("v8", v8, torch.float8_e4m3fn, device)
+    _check_dev("k_scale", k_scale, torch.uint8, device)
+    _check_dev("v_scale", v_scale, torch.uint8, device)
+    if k8.dim() != 3 or v8.shape != k8.shape or k8.shape[1] % TS_Q8_BLOCK:
+        raise ValueError(f"k8 and v8 must be [Hkv, rows, D], rows a multiple of {TS_Q8_BLOCK}")
+    want = (k8.shape[0], k8.shape[1] // TS_Q8_BLOCK)
+    if tuple(k_scale.shape) != want or tuple(v_scale.shape) != want:
+        raise ValueError(f"k_scale and v_scale must be {want}")
+
+
+def kv_quantize_q8(k, v, row0: int, n_rows: int, k8, v8, k_scale, v_scale, dst_row: int,
+                   stream=None):
+    """Rows [row0, row0 + n_rows) of bf16 k and v [Hkv, cap, D] into 8-bit rows
+    [dst_row, dst_row + n_rows) and their blocks' scales
+    (``ts_kv_quantize_q8``); n_rows and dst_row multiples of 64."""
+    _check_dev("k", k, torch.bfloat16)
+    dev = _call_device("k", k)
+    _check_dev("v", v, torch.bfloat16, dev)
+    _check_q8(k8, v8, k_scale, v_scale, dev)
+    if k.dim() != 3 or v.shape != k.shape or k.shape[0] != k8.shape[0] or k.shape[2] != k8.shape[2]:
+        raise ValueError("k / v / k8 / v8 shapes disagree")
+    hkv, cap, d = k.shape
+    _raise(_lib().ts_kv_quantize_q8(_ptr(k), _ptr(v), cap, hkv, d, int(row0), int(n_rows), _ptr(k8),
+                                    _ptr(v8), _ptr(k_scale), _ptr(v_scale), k8.shape[1],
+                                    int(dst_row), _stream(stream)), "ts_kv_quantize_q8")
+    return k8, v8, k_scale, v_scale
+
+
+class KvCacheQ8:
+    """An 8-bit KV cache (``ts_q8_cache``): ``n_q8`` context rows as e4m3
+    blocks of 64, then ``n_tail`` rows (and the draft tree's) as bf16 in a
+    tail that starts at row ``tail_row0`` of its buffer.  The tensors are the
+    caller's, or :meth:`empty`'s.
+
+    A step: :meth:`append` the tree's rows, :func:`tree_verify_attn_q8`,
+    :meth:`commit` the accepted path, :meth:`fold` the blocks that are full.
+    A prompt: :meth:`append` without a tree, then :meth:`fold`.
+    """
+
+    def __init__(self, k8, v8, k_scale, v_scale, k_tail, v_tail, n_q8: int = 0, n_tail: int = 0,
+                 tail_row0: int = 0):
+        dev = _call_device("k_tail", k_tail)
+        _check_q8(k8, v8, k_scale, v_scale, dev)
+        _check_dev("k_tail", k_tail, torch.bfloat16, dev)
+        _check_dev("v_tail", v_tail, torch.bfloat16, dev)
+        if (k_tail.dim() != 3 or v_tail.shape != k_tail.shape or
+                k_tail.shape[0] != k8.shape[0] or k_tail.shape[2] != k8.shape[2]):
+            raise ValueError("k_tail and v_tail must be [Hkv, rows, D] as k8")
+        if not 0 <= n_q8 <= k8.shape[1] or n_q8 % TS_Q8_BLOCK:
+            raise ValueError("n_q8 must be a multiple of 64 within the 8-bit rows")
+        if n_tail < 0 or tail_row0 < 0 or tail_row0 + n_tail > k_tail.shape[1]:
+            raise ValueError("n_tail rows from tail_row0 must lie in the tail")
+        self.k8, self.v8, self.k_scale, self.v_scale = k8, v8, k_scale, v_scale
+        self.k_tail, self.v_tail, self.device = k_tail, v_tail, dev
+        self.n_q8, self.n_tail, self.tail_row0 = int(n_q8), int(n_tail), int(tail_row0)
+
+    @classmethod
+    def empty(cls, n_heads_kv: int, head_dim: int, capacity: int, tail_rows: int = 256,
+              device=None):
+        """An empty cache for ``capacity`` 8-bit rows (rounded up to 64).  The
+        tail takes a step's tree behind up to 63 rows (128 rows), or a
+        prompt's chunk."""
+        device = "cuda" if device is None else device
+        cap = -(-int(capacity) // TS_Q8_BLOCK) * TS_Q8_BLOCK
+
+        def new(rows, dtype):
+            return torch.zeros((n_heads_kv, rows, head_dim), dtype=torch.uint8 if dtype is None
+                               else dtype, device=device)
+
+        scales = [torch.zeros((n_heads_kv, cap // TS_Q8_BLOCK), dtype=torch.uint8, device=device)
+                  for _ in range(2)]
+        return cls(new(cap, None).view(torch.float8_e4m3fn), new(cap, None).view(torch.float8_e4m3fn),
+                   *scales, new(int(tail_rows), torch.bfloat16), new(int(tail_rows), torch.bfloat16))
+
+    @property
+    def n_ctx(self) -> int:
+        return self.n_q8 + self.n_tail
+
+    def struct(self):
+        """The ``ts_q8_cache`` of the cache as it stands."""
+        hkv, cap, d = self.k8.shape
+        return _Q8Cache(self.k8.data_ptr(), self.v8.data_ptr(), self.k_scale.data_ptr(),
+                        self.v_scale.data_ptr(), cap, self.k_tail.data_ptr(),
+                        self.v_tail.data_ptr(), self.k_tail.shape[1], self.tail_row0, hkv, d,
+                        self.n_q8, self.n_tail)
+
+    def append(self, q, k, v, inv_freq, parent=None, stream=None, **kw):
+        """:func:`rope_append` behind the context, at its positions.  With
+        ``parent`` the rows are a draft tree's and wait for :meth:`commit`;
+        without, they are context at once.  Returns the turned queries."""
+        out = rope_append(q, k, v, self.k_tail, self.v_tail, self.tail_row0 + self.n_tail,
+                          self.n_ctx, inv_freq, parent=parent, stream=stream, **kw)
+        if parent is None:
+            self.n_tail += k.shape[0]
+        return out
+
+    def commit(self, accept, n_tree: int, n_accepted: int, workspace=None, stream=None) -> None:
+        """Keeps the root's row and the accepted path's (``ts_kv_commit_path``
+        on the tail).  ``accept``: the device result of
+        :func:`penalize_accept`; ``n_accepted``: its path length, read by the
+        caller."""
+        if not 0 <= int(n_accepted) < int(n_tree):
+            raise ValueError("n_accepted must lie in [0, n_tree)")
+        _check_dev("accept", accept, torch.int32, self.device)
+        dev = _call_device("k_tail", self.k_tail)
+        if workspace is None:
+            workspace = new_workspace(256, dev)
+        hkv, cap, d = self.k_tail.shape
+        if self.tail_row0 + self.n_tail + int(n_tree) > cap:
+            raise ValueError("the tree's rows do not lie in the tail")
+        off = 2 * d * self.tail_row0
+        _raise(_lib().ts_kv_commit_path(
+            ctypes.c_void_p(self.k_tail.data_ptr() + off),
+            ctypes.c_void_p(self.v_tail.data_ptr() + off), cap, hkv, d, self.n_tail, int(n_tree),
+            _ptr(accept), _ptr(workspace), _ws_bytes(workspace, dev), _stream(stream)),
+            "ts_kv_commit_path")
+        self.n_tail += int(n_accepted) + 1
+
+    def fold(self, stream=None) -> int:
+        """Turns the tail's full blocks into 8 bits and, where the tail's end
+        is near, moves the rows that are left to its start.  Returns the rows
+        folded."""
+        rows = self.n_tail // TS_Q8_BLOCK * TS_Q8_BLOCK
+        if rows:
+            kv_quantize_q8(self.k_tail, self.v_tail, self.tail_row0, rows, self.k8, self.v8,
+                           self.k_scale, self.v_scale, self.n_q8, stream=stream)
+            self.n_q8 += rows
+            self.n_tail -= rows
+            self.tail_row0 += rows
+        # fewer than 64 rows are left; those before them are done with
+        if (self.tail_row0 and self.tail_row0 >= self.n_tail and
+                self.k_tail.shape[1] - self.tail_row0 < 3 * TS_Q8_BLOCK):
+            cur = torch.cuda.current_stream() if stream is None else stream
+            with torch.cuda.stream(cur):
+                for t in (self.k_tail, self.v_tail):
+                    t[:, :self.n_tail].copy_(t[:, self.tail_row0:self.tail_row0 + self.n_tail])
+            self.tail_row0 = 0
+        return rows
+
+
+def _call_cache(cache):
+    if not isinstance(cache, KvCacheQ8):
+        raise ValueError("cache must be a KvCacheQ8")
+    return _call_device("cache", cache.k_tail), cache.struct()
+
+
+def tree_verify_attn_q8_workspace_size(n_heads_q, n_heads_kv, head_dim, n_q8, n_tail,
+                                       n_tree) -> int:
+    return int(_lib().ts_tree_verify_attn_q8_workspace_size(n_heads_q, n_heads_kv, head_dim, n_q8,
+                                                            n_tail, n_tree))
+
+
+def tree_verify_attn_q8(q, cache: KvCacheQ8, parent, out=None, workspace=None,
+                        softmax_scale: float | None = None, stream=None, root_scores_out=None):
+    """Tree-masked attention over an 8-bit cache (``ts_tree_verify_attn_q8``);
+    the tree's rows lie in the tail behind the context.  q: bf16 [T, Hq, D];
+    returns bf16 [T, Hq, D].  ``root_scores_out``: fp32 [Hq, n_ctx], as for
+    :func:`tree_verify_attn`."""
+    _check_dev("q", q, torch.bfloat16)
+    dev, st = _call_cache(cache)
+    if q.device != dev:
+        raise ValueError(f"q is on {q.device}, the call's other tensors on {dev}")
+    t, hq, d = q.shape
+    if d != st.head_dim:
+        raise ValueError("q and the cache must have the same head_dim")
+    if out is None:
+        out = torch.empty((t, hq, d), dtype=torch.bfloat16, device=dev)
+    _check_dev("out", out, torch.bfloat16, dev)
+    if tuple(out.shape) != (t, hq, d):
+        raise ValueError("out must have q's shape")
+    if root_scores_out is not None:
+        _check_dev("root_scores_out", root_scores_out, torch.float32, dev)
+        if tuple(root_scores_out.shape) != (hq, cache.n_ctx):
+            raise ValueError("root_scores_out must be [Hq, n_ctx]")
+    if workspace is None:
+        workspace = new_workspace(tree_verify_attn_q8_workspace_size(
+            hq, st.n_heads_kv, d, st.n_q8, st.n_tail, t), dev)
+    par, par_p = _host_i32(parent)
+    if len(par) != t:
+        raise ValueError("parent must have one entry per tree node")
+    scale = float(d) ** -0.5 if softmax_scale is None else float(softmax_scale)
+    rc = _lib().ts_tree_verify_attn_q8(
+        ctypes.byref(st), _ptr(q), hq, t, par_p, scale, _ptr(out), _ptr(root_scores_out),
+        _ptr(workspace), _ws_bytes(workspace, dev), _stream(stream))
+    _raise(rc, "ts_tree_verify_attn_q8")
+    return out
+
+
+def _q8_partials(cache, n_keep, k_partial, v_partial, dev):
+    hkv, _, d = cache.k8.shape
+    if k_partial is None:
+        k_partial = torch.empty((hkv, n_keep, d), dtype=torch.bfloat16, device=dev)
+    if v_partial is None:
+        v_partial = torch.empty_like(k_partial)
+    _check_dev("k_partial", k_partial, torch.bfloat16, dev)
+    _check_dev("v_partial", v_partial, torch.bfloat16, dev)
+    if (k_partial.dim() != 3 or k_partial.shape[0] != hkv or k_partial.shape[2] != d or
+            v_partial.shape != k_partial.shape):
+        raise ValueError("k_partial and v_partial must be [Hkv, rows, D]")
+    return k_partial, v_partial
+
+
+def kv_gather_q8(cache: KvCacheQ8, idx, k_partial=None, v_partial=None, workspace=None,
+                 stream=None):
+    """Context rows ``idx`` (int32 [Hkv, n_keep]) of an 8-bit cache as bf16 rows
+    (``ts_kv_gather_q8``).  Returns ``(k_partial, v_partial)``."""
+    dev, st = _call_cache(cache)
+    _check_dev("idx", idx, torch.int32, dev)
+    if idx.dim() != 2 or idx.shape[0] != st.n_heads_kv:
+        raise ValueError("idx must be [Hkv, n_keep]")
+    k_partial, v_partial = _q8_partials(cache, idx.shape[1], k_partial, v_partial, dev)
+    if workspace is None:
+        workspace = new_workspace(256, dev)
+    _raise(_lib().ts_kv_gather_q8(
+        ctypes.byref(st), _ptr(idx), idx.shape[1], _ptr(k_partial), _ptr(v_partial),
+        k_partial.shape[1], _ptr(workspace), _ws_bytes(workspace, dev), _stream(stream)),
+        "ts_kv_gather_q8")
+    return k_partial, v_partial
+
+
+def kv_select_from_scores_q8(root_scores, cache: KvCacheQ8, n_sink: int, budget: int,
+                             k_partial=None, v_partial=None, idx_out=None, scores_out=None,
+                             workspace=None, stream=None, want_scores: bool = False):
+    """:func:`kv_select_from_scores` on an 8-bit cache
+    (``ts_kv_select_from_scores_q8``).
+
+    Returns ``(idx [Hkv, n_keep] int32, k_partial, v_partial, scores or None)``.
+    """
+    _check_dev("root_scores", root_scores, torch.float32)
+    dev, st = _call_cache(cache)
+    if root_scores.device != dev:
+        raise ValueError(f"root_scores is on {root_scores.device}, the call's tensors on {dev}")
+    hq, n_ctx, hkv = root_scores.shape[0], cache.n_ctx, st.n_heads_kv
+    if root_scores.shape[1] != n_ctx:
+        raise ValueError("root_scores must be [Hq, n_ctx]")
+    n_keep = min(n_ctx, int(n_sink) + int(budget))
+    k_partial, v_partial = _q8_partials(cache, n_keep, k_partial, v_partial, dev)
+    if idx_out is None:
+        idx_out = torch.empty((hkv, n_keep), dtype=torch.int32, device=dev)
+    _check_dev("idx_out", idx_out, torch.int32, dev)
+    if idx_out.numel() != hkv * n_keep:
+        raise ValueError("idx_out must be [Hkv, n_keep]")
+    if want_scores and scores_out is None:
+        scores_out = torch.empty((hkv, n_ctx), dtype=torch.float32, device=dev)
+    if scores_out is not None:
+        _check_dev("scores_out", scores_out, torch.float32, dev)
+        if scores_out.numel() != hkv * n_ctx:
+            raise ValueError("scores_out must be [Hkv, n_ctx]")
+    if workspace is None:
+        workspace = new_workspace(kv_select_from_scores_workspace_size(hq, hkv, n_ctx), dev)
+    _raise(_lib().ts_kv_select_from_scores_q8(
+        _ptr(root_scores), ctypes.byref(st), hq, int(n_sink), int(budget), _ptr(scores_out),
+        _ptr(idx_out), _ptr(k_partial), _ptr(v_partial), k_partial.shape[1], _ptr(workspace),
+        _ws_bytes(workspace, dev), _stream(stream)), "ts_kv_select_from_scores_q8")
+    return idx_out, k_partial, v_partial, scores_out
 
 
 def kernel_launch_count() -> int:

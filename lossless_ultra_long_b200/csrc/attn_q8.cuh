@@ -1,0 +1,80 @@
+// attn_q8.cuh -- the 8-bit KV cache as the kernels see it: blocks of 64
+// rows of e4m3 codes with one power-of-two scale per block and KV head,
+// followed by a bf16 tail that holds the newest context rows and the draft
+// tree's rows.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "ts_internal.cuh"
+
+namespace ts {
+
+constexpr int kQ8Block = TS_Q8_BLOCK;   // rows that share a scale
+// least exponent of a scale: magnitudes below 2^-100 * 2^-10 round to zero
+constexpr int kQ8MinExp = -100;
+
+struct Q8Cache {
+    const uint8_t *k8, *v8;             // [Hkv, q8_cap, D] e4m3
+    const uint8_t *k_scale, *v_scale;   // [Hkv, q8_cap / 64]: 2^(byte - 127), 255: NaN
+    int64_t q8_cap;
+    const __nv_bfloat16 *k_tail, *v_tail;   // [Hkv, tail_cap, D]
+    int64_t tail_cap;
+    int n_q8, n_tail;                   // context rows in 8 bits (a multiple of 64), in the tail
+};
+
+struct QuantArgs {
+    const __nv_bfloat16 *k, *v;   // first row to quantise; src_cap rows per head apart
+    int64_t src_cap;
+    int n_heads_kv, head_dim, n_rows;
+    uint8_t *k8, *v8, *k_scale, *v_scale;
+    int64_t q8_cap, dst_row;
+};
+
+struct GatherQ8Args {
+    Q8Cache c;
+    int n_heads_kv, head_dim;
+    const int32_t *idx;   // [Hkv, n_keep]
+    int n_keep;
+    __nv_bfloat16 *k_partial, *v_partial;
+    int64_t partial_cap;
+    void *workspace;
+};
+
+struct AttnQ8Args {
+    Q8Cache c;
+    const __nv_bfloat16 *q;
+    __nv_bfloat16 *out;
+    float *root_scores;   // fp32 [Hq, n_q8 + n_tail], base 2, or null
+    int n_heads_q, n_heads_kv, head_dim, n_tree;
+    float scale_log2;
+    void *workspace;
+};
+
+cudaError_t kv_quantize_launch(const QuantArgs &a, cudaStream_t stream);
+cudaError_t kv_gather_q8_launch(const GatherQ8Args &a, cudaStream_t stream);
+
+size_t attn_q8_workspace_bytes(int n_heads_q, int n_heads_kv, int head_dim, int n_q8, int n_tail,
+                               int n_tree, int num_sms);
+cudaError_t attn_q8_launch(const AttnQ8Args &a, const TreeMasks &masks, int num_sms,
+                           cudaStream_t stream);
+
+// the factor a scale byte stands for
+__device__ __forceinline__ float q8_factor(uint32_t byte)
+{
+    // byte 0 is 2^-127, a subnormal
+    return byte == 255u ? __uint_as_float(0x7FC00000u)
+                        : __uint_as_float(byte ? byte << 23 : 0x00400000u);
+}
+
+// two codes (low byte first) times f, rounded to bf16 (exactly, for a power
+// of two inside bf16's normal range)
+__device__ __forceinline__ uint32_t q8_pair(uint32_t two, float f)
+{
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(two & 0xFFFFu), __NV_E4M3);
+    const float2 x = __half22float2(__half2(h));
+    const __nv_bfloat162 b = __floats2bfloat162_rn(x.x * f, x.y * f);
+    return *reinterpret_cast<const uint32_t *>(&b);
+}
+
+}  // namespace ts

@@ -946,6 +946,8 @@ sel_gather_kernel(SelectArgs a, SelGeom geo, SelWs ws, int mode, int cand_cap)
     if (tid == kSelThreads - 1)
         n_rows = min(slot, n_keep - ci.x);
     __syncthreads();
+    if (a.k == nullptr)
+        return;   // the positions alone: another kernel copies the rows
     const int rows = n_rows;
     constexpr int LPR = D / 8;   // lanes per row, 16 bytes each
     const __nv_bfloat16 *kh = a.k + (int64_t)g * a.kv_cap * D;

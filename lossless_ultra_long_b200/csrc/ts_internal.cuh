@@ -164,6 +164,25 @@ struct CommitArgs {
 };
 cudaError_t commit_launch(const CommitArgs &a, cudaStream_t stream);
 
+// Rotation of a step's (or a prompt's) queries and keys and the append of
+// its K/V rows.
+struct RopeArgs {
+    const __nv_bfloat16 *q, *k, *v;          // token rows q_stride, ... elements apart
+    int64_t q_stride, k_stride, v_stride;
+    int n_heads_q, n_heads_kv, head_dim;     // n_heads_q 0: keys and values alone
+    int n_tok;
+    bool tree;                               // positions by depth in the draft tree
+    int64_t pos0;
+    const float *inv_freq;                   // [rot_dim / 2]
+    int rot_dim;
+    bool interleaved;
+    float mscale;
+    __nv_bfloat16 *q_out, *k_cache, *v_cache;
+    int64_t kv_cap, row0;
+};
+cudaError_t rope_append_launch(const RopeArgs &a, const int32_t *parent, int num_sms,
+                               cudaStream_t stream);
+
 size_t penalize_workspace_bytes(int n_tree, int vocab);
 // Largest vocabulary one penalty launch covers (its splits times the
 // longest slice a CTA stages); `sample`: with the temperature draw's noise.
