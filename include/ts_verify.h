@@ -396,9 +396,9 @@ TS_API int ts_kv_commit_path(void *k_cache, void *v_cache, int64_t kv_cap, int n
  *
  * 8-bit rows come in blocks of TS_Q8_BLOCK (64).  A block of one KV head
  * holds e4m3 codes and, for K and for V, one scale byte b: the rows are
- * code * 2^(b - 127), and b = 255 makes the whole block NaN.  Attention and
- * gather take any scale byte and any code but the two that e4m3 reserves
- * for NaN (0x7F, 0xFF), which ts_kv_quantize_q8 never writes.
+ * code * 2^(b - 127), and b = 255 makes the whole block NaN.  Bytes below
+ * 27 (2^-100) are read as 27.  The codes 0x7F and 0xFF, which e4m3 reserves
+ * for NaN and ts_kv_quantize_q8 never writes, must not occur below n_q8.
  *
  * A step: ts_rope_append puts the tree's rows behind the tail's context,
  * ts_tree_verify_attn_q8 attends, ts_kv_commit_path (on the tail's buffers,

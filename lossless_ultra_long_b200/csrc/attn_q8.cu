@@ -100,7 +100,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
 attn_q8_kernel(AttnQ8Args a, TreeMasks masks, int tiles_per_split, int n_split)
 {
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ unsigned long long odd_rows;   // tail tile: rows with a value that is no number
+    // tail tile: rows with a value that is no number, and those of K among them
+    __shared__ unsigned long long odd_rows, odd_keys;
     constexpr int TB = Shape<D>::kTileBytes;
     const Q8Cache &kc = a.c;
 
@@ -198,7 +199,7 @@ attn_q8_kernel(AttnQ8Args a, TreeMasks masks, int tiles_per_split, int n_split)
         const bool q8 = tile < n_blocks;
         float sk = 1.f, sv = 1.f;
         uint32_t ks, vs;
-        unsigned long long odd = 0ull;
+        unsigned long long odd = 0ull, odd_k = 0ull;
         if (q8) {
             sk = q8_factor(ksc[tile]);
             sv = q8_factor(vsc[tile]);
@@ -219,17 +220,21 @@ attn_q8_kernel(AttnQ8Args a, TreeMasks masks, int tiles_per_split, int n_split)
         } else {
             // rows with an infinity or a NaN leave the products
             if (threadIdx.x == 0)
-                odd_rows = 0ull;
+                odd_rows = odd_keys = 0ull;
             __syncthreads();
             for (int c = threadIdx.x; c < kTile * D / 4; c += nthreads) {
                 const int which = c / (kTile * D / 8), ch = c % (kTile * D / 8);
                 const int r = ch / (D / 8);
                 const uint4 w = *reinterpret_cast<const uint4 *>(raw + which * TB + 16 * ch);
-                if (odd_pair(w.x) || odd_pair(w.y) || odd_pair(w.z) || odd_pair(w.w))
+                if (odd_pair(w.x) || odd_pair(w.y) || odd_pair(w.z) || odd_pair(w.w)) {
                     atomicOr(&odd_rows, 1ull << r);
+                    if (which == 0)
+                        atomicOr(&odd_keys, 1ull << r);
+                }
             }
             __syncthreads();
             odd = odd_rows;
+            odd_k = odd_keys;
             if (odd) {
                 for (int c = threadIdx.x; c < kTile * D / 4; c += nthreads) {
                     const int which = c / (kTile * D / 8), ch = c % (kTile * D / 8);
@@ -291,7 +296,7 @@ attn_q8_kernel(AttnQ8Args a, TreeMasks masks, int tiles_per_split, int n_split)
                 float x = s[nt][e] * sc;
                 if (a.root_scores && rnode[hi] == 0 && rvalid[hi] && pos0 + p < n_ctx)
                     a.root_scores[(int64_t)rhead[hi] * n_ctx + pos0 + p] =
-                        (odd >> p) & 1ull ? __uint_as_float(0x7FC00000u) : x;
+                        (odd_k >> p) & 1ull ? __uint_as_float(0x7FC00000u) : x;
                 if (!q8 && !((vis[hi] >> p) & 1ull))
                     x = -INFINITY;
                 s[nt][e] = x;
@@ -355,7 +360,7 @@ attn_q8_kernel(AttnQ8Args a, TreeMasks masks, int tiles_per_split, int n_split)
         l_run[hi] += __shfl_xor_sync(0xffffffffu, l_run[hi], 2);
     }
     const int rows_all = a.n_tree * a.n_heads_q;
-    float *ws_o = reinterpret_cast<float *>(reinterpret_cast<char *>(a.workspace) + kHeaderBytes);
+    float *ws_o = reinterpret_cast<float *>(reinterpret_cast<char *>(a.workspace) + kHeaderBytes + kQ8SyncBytes);
     float *ws_ml = ws_o + (size_t)n_split * rows_all * D;
 #pragma unroll
     for (int hi = 0; hi < 2; ++hi) {
@@ -468,7 +473,7 @@ cudaError_t launch_d(const AttnQ8Args &a, const TreeMasks &masks, const SplitPla
         return e;
     const int rows_all = a.n_tree * a.n_heads_q;
     const float *ws_o = reinterpret_cast<const float *>(
-        reinterpret_cast<const char *>(a.workspace) + kHeaderBytes);
+        reinterpret_cast<const char *>(a.workspace) + kHeaderBytes + kQ8SyncBytes);
     const float *ws_ml = ws_o + (size_t)p.n_split * rows_all * D;
     attn_q8_combine_kernel<D><<<(rows_all + 7) / 8, 256, 0, stream>>>(ws_o, ws_ml, a.out, rows_all,
                                                                      p.n_split);
@@ -484,13 +489,22 @@ size_t attn_q8_workspace_bytes(int n_heads_q, int n_heads_kv, int head_dim, int 
                                int n_tree, int num_sms)
 {
     const SplitPlan p = make_plan(n_heads_q, n_heads_kv, n_q8, n_tail, n_tree, num_sms);
-    return kHeaderBytes +
-           align_up((size_t)p.n_split * n_tree * n_heads_q * (head_dim + 2) * sizeof(float), 256);
+    size_t bytes = kHeaderBytes + kQ8SyncBytes +
+                   align_up((size_t)p.n_split * n_tree * n_heads_q * (head_dim + 2) * sizeof(float), 256);
+    // large enough for whichever kernel the launch picks
+    if (attn_q8_t128_eligible(n_heads_q, n_heads_kv, head_dim, n_q8, n_tail, n_tree, num_sms)) {
+        const size_t t = attn_q8_t128_workspace_bytes(n_heads_q, n_heads_kv, n_q8, n_tail, n_tree, num_sms);
+        bytes = t > bytes ? t : bytes;
+    }
+    return bytes;
 }
 
 cudaError_t attn_q8_launch(const AttnQ8Args &a, const TreeMasks &masks, int num_sms,
                            cudaStream_t stream)
 {
+    if (a.scale_log2 > 0.f && attn_q8_t128_eligible(a.n_heads_q, a.n_heads_kv, a.head_dim, a.c.n_q8,
+                                                    a.c.n_tail, a.n_tree, num_sms))
+        return attn_q8_t128_launch(a, masks, num_sms, stream);
     const SplitPlan p = make_plan(a.n_heads_q, a.n_heads_kv, a.c.n_q8, a.c.n_tail, a.n_tree, num_sms);
     return a.head_dim == 128 ? launch_d<128>(a, masks, p, stream)
                              : launch_d<64>(a, masks, p, stream);

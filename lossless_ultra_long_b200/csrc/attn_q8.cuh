@@ -59,12 +59,35 @@ size_t attn_q8_workspace_bytes(int n_heads_q, int n_heads_kv, int head_dim, int 
 cudaError_t attn_q8_launch(const AttnQ8Args &a, const TreeMasks &masks, int num_sms,
                            cudaStream_t stream);
 
-// the factor a scale byte stands for
+// head_dim 128 on the tcgen05 tensor cores (one cooperative launch)
+bool attn_q8_t128_eligible(int n_heads_q, int n_heads_kv, int head_dim, int n_q8, int n_tail,
+                           int n_tree, int num_sms);
+size_t attn_q8_t128_workspace_bytes(int n_heads_q, int n_heads_kv, int n_q8, int n_tail, int n_tree,
+                                    int num_sms);
+cudaError_t attn_q8_t128_launch(const AttnQ8Args &a, const TreeMasks &masks, int num_sms,
+                                cudaStream_t stream);
+
+// Both attention kernels' workspaces: header, this region (the tcgen05
+// kernel's counters, zero between calls, so that one workspace serves calls
+// of any shape), then scratch.
+constexpr size_t kQ8SyncBytes = 4096;
+
+// the factor a scale byte stands for (bytes below the least scale read as
+// it), its exponent, and its inverse; 255 is NaN
 __device__ __forceinline__ float q8_factor(uint32_t byte)
 {
-    // byte 0 is 2^-127, a subnormal
-    return byte == 255u ? __uint_as_float(0x7FC00000u)
-                        : __uint_as_float(byte ? byte << 23 : 0x00400000u);
+    return __uint_as_float(byte == 255u ? 0x7FC00000u : max(byte, (uint32_t)(kQ8MinExp + 127)) << 23);
+}
+__device__ __forceinline__ float q8_log2(uint32_t byte)
+{
+    return byte == 255u ? __uint_as_float(0x7FC00000u) : (float)max((int)byte - 127, kQ8MinExp);
+}
+__device__ __forceinline__ float q8_inverse(uint32_t byte)
+{
+    // 2^-127, the inverse of the largest, is a subnormal
+    return __uint_as_float(byte == 255u   ? 0x7FC00000u
+                           : byte == 254u ? 0x00400000u
+                                          : (254u - max(byte, (uint32_t)(kQ8MinExp + 127))) << 23);
 }
 
 // two codes (low byte first) times f, rounded to bf16 (exactly, for a power

@@ -1,0 +1,1459 @@
+// attn_q8_t128.cu -- tree-verify attention over the 8-bit KV cache on the
+// 5th-generation tensor cores (head_dim 128): split-KV, 128-position tiles.
+//
+// Products, for the R = G*T query rows of a KV head and one tile:
+//   S_b  = Q_b K^T     kind::f8f6f4 on the codes as they lie in HBM.  A bf16
+//                      query is the sum of an e4m3 and an e5m2 number: with
+//                      its row scaled to at most 448, hi = e4m3(q) keeps 4 of
+//                      the 8 significant bits and lo = e5m2(q - hi) holds
+//                      what is left (an integer of 0..8 units of the last
+//                      bit, which 3 bits represent), down to 2^-16 of the
+//                      scaled row.  So S = hi K^T + lo K^T costs what one
+//                      bf16 product costs, and K is never converted.
+//   O^T += V^T P^T     kind::f16 on bf16: V's codes are bf16 numbers; four
+//                      converter warps write them out once per tile.
+// The scales (a power of two per 64 rows) never touch the products' inputs:
+// K's multiplies the score inside the exponent's FMA, V's is added to the
+// exponent, so the weight leaves as p * s_v with its one rounding to bf16,
+// and each block's sum is multiplied back by 1 / s_v.
+//
+// A tail tile (bf16 rows: newest context, tree) goes through the same
+// products: a converter warp scales its keys by block and splits them like
+// the queries into an e4m3 and an e5m2 tile (two K slots, four products),
+// and copies V.  Rows with an infinity or a NaN are zeroed there and noted;
+// a query row that sees one gets a NaN sum.
+//
+// Softmax layout, reference maximum (fixed at a row's first tile), run-time
+// hand-out of tiles from the end of the cache backwards, partials, and the
+// combine by the splits themselves follow the bf16 kernel in attn_t128.cu;
+// a split whose row sum outgrows the reference by 2^63 is recomputed exactly
+// from the owner map.  The result is rounded to bf16, as coarse as the
+// weights' own rounding, so rows that rest on few positions need no second
+// look.
+//
+// CTA = (split, KV head, node group), 20 warps, one CTA per SM:
+//   warp 0      root scores out of S        warp 1  QK issuer, TMEM
+//   warp 2      PV issuer                   warp 3  TMA producer
+//   warps 4-15  softmax                     warps 16-19  converters
+// P^T is double-buffered, and with one query block (R <= 128) S too, so a
+// tile's exponentials overlap the previous tile's PV and the next one's QK.
+// TMEM: O^T in [0, 192), Q_0 (hi, lo) in [192, 256), S in [256, 512).
+//
+// Every wait is bounded (about a second): on expiry the kernel records
+// TS_ERR_TIMEOUT in the workspace status word, all roles leave their loops,
+// and TMEM is freed before the CTA exits.
+#include <math.h>
+
+#include "attn_common.cuh"
+#include "attn_q8.cuh"
+#include "sm100.cuh"
+
+namespace ts {
+
+// from attn_dispatch.cu
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
+
+namespace {
+
+using namespace sm100;
+
+constexpr int kD = 128;
+constexpr int kTileN = 128;                  // KV positions per tile
+constexpr int kBlockM = 128;                 // query rows per QK block (TMEM lanes)
+constexpr int kRawBytes = kTileN * kD;       // codes of K (or V) of a tile: 16 KB
+constexpr int kBoxBytes = kTileN * 64 * 2;   // one 64-column half of a bf16 V tile
+constexpr int kVbBytes = 2 * kBoxBytes;
+constexpr int kThreads = 640;                // 20 warps
+constexpr int kMaxStages = 5;
+constexpr int kMaxRows = 192;
+constexpr int kQCol = 192;                   // Q of block 0: hi 32 columns, lo 32 columns
+constexpr int kSCol = 256;                   // S slots: 128 columns each
+constexpr int kTmemCols = 512;
+constexpr int kQ1Bytes = 2 * kBlockM * kD;   // Q of block 1 in shared memory: hi, lo
+constexpr float kMaxRowSum = 9.223372036854775808e18f;   // 2^63
+constexpr size_t kSmemLimit = 232448;        // dynamic shared memory per CTA
+constexpr int kBarQuery = 1;                 // named barrier: query rows in place
+constexpr int kBarOut = 2;                   // named barrier: O^T staged in shared memory
+constexpr int kTileRing = 16;                // entries of the tile rings (> any role's lead)
+constexpr int kConvWarps = 4;
+// registers per thread: the launch gives 640 * 96; the softmax warpgroups
+// take 128 each, the two others 48: 3 * 128 * 128 + 2 * 128 * 48 = 640 * 96
+constexpr int kRegsLaunch = 96, kRegsSoftmax = 128, kRegsOther = 48;
+static_assert(3 * 128 * kRegsSoftmax + 2 * 128 * kRegsOther <= kThreads * kRegsLaunch, "registers");
+constexpr int kMaxGz = 256;                  // (KV head, node group) pairs: counters in the workspace
+static_assert(kMaxGz * 16 <= (int)kQ8SyncBytes, "counters fit their region");
+
+struct Bars {
+    uint64_t full_k[kMaxStages];
+    uint64_t empty_k[kMaxStages];
+    uint64_t full_v[kMaxStages];    // codes of V landed (or: a tail tile, or the end)
+    uint64_t empty_v[kMaxStages];
+    uint64_t vb_full[2];            // V in bf16 (or the end)
+    uint64_t s_full[2];             // QK landed in an S slot
+    uint64_t s_free[2];             // its readers hold it in registers
+    uint64_t sm_done[2];            // every softmax warp wrote its P^T rows
+    uint64_t pv_done[2];            // PV of a tile of that parity is complete
+    uint64_t o_final;
+    uint64_t drain[2];
+    uint64_t conv;                  // the converter warps meet (tail tiles)
+    // per tile, at [t % kTileRing]: its index (-1 after the last), its scale
+    // bytes (k of its two blocks, v of its two blocks), its first K ring
+    // entry.  Written by the producer (a tail tile's k bytes by a converter)
+    // before the arrival that the readers wait for.
+    volatile int32_t tile_of[kTileRing];
+    volatile uint32_t scale_of[kTileRing];
+    volatile int32_t entry_of[kTileRing];
+    uint32_t bad[4][4];             // tail tile t % 4: rows with a value that is no number
+    uint32_t bad_k[4][4];
+    uint32_t top[4];                // converters: largest key magnitude of each 32 rows
+    uint32_t tmem_base;
+    uint32_t abort;
+    int32_t overflow;
+};
+
+struct Aux {
+    Bars bar;
+    unsigned long long anc[TS_MAX_TREE];
+    float row_scale[2 * kBlockM];   // softmax scale * log2 e * the query row's scale
+};
+constexpr size_t kAuxBytes = (sizeof(Aux) + 1023) / 1024 * 1024;
+
+struct Layout {
+    int r_pad, stages_k, stages_v, stages_vb;
+    size_t q1_off, p_off, vb_off, k_off, v_off, aux_off, smem_bytes;
+};
+
+__host__ __device__ inline int q8_row_of(int n, int R)
+{
+    return R > kBlockM ? (n < kBlockM ? (R - kBlockM) + n : n - kBlockM) : n;
+}
+
+__host__ __device__ inline Layout q8_layout(int rows)
+{
+    Layout L;
+    L.r_pad = (rows + 15) / 16 * 16;
+    L.q1_off = 0;
+    L.p_off = rows > kBlockM ? kQ1Bytes : 0;
+    // two P^T tiles, then 1 KB that rows past the query rows are written to
+    L.vb_off = L.p_off + (size_t)L.r_pad * 512 + 1024;
+    L.stages_vb = rows > kBlockM ? 1 : 2;
+    L.k_off = L.vb_off + (size_t)L.stages_vb * kVbBytes;
+    const size_t fixed = 1024 + L.k_off + kAuxBytes;
+    int stages = (int)((kSmemLimit - fixed) / kRawBytes);
+    stages = stages > 2 * kMaxStages ? 2 * kMaxStages : stages;
+    L.stages_v = stages / 2;
+    L.stages_k = stages - L.stages_v;   // at least 2: a tail tile takes two
+    L.v_off = L.k_off + (size_t)L.stages_k * kRawBytes;
+    L.aux_off = L.v_off + (size_t)L.stages_v * kRawBytes;
+    L.smem_bytes = 1024 + L.aux_off + kAuxBytes;
+    return L;
+}
+
+// Instruction descriptor of kind::f8f6f4, fp32 accumulation, K-major
+// operands; a5 / b5: that operand is e5m2 instead of e4m3.
+constexpr uint32_t idesc_f8(int m, int n, int a5, int b5)
+{
+    return (1u << 4) | ((uint32_t)a5 << 7) | ((uint32_t)b5 << 10) | ((uint32_t)(n >> 3) << 17) |
+           ((uint32_t)(m >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma8_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc)
+{
+    asm volatile(
+        "{\n"
+        " .reg .pred p;\n"
+        " setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n"
+        "}\n" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma8_ts(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc,
+                                        bool acc)
+{
+    asm volatile(
+        "{\n"
+        " .reg .pred p;\n"
+        " setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n"
+        "}\n" ::"r"(d), "r"(a_tmem), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+        : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void regs_inc()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+
+// 16 TMEM lanes x 32 columns, the layout of tmem_ld16x256_x16; waits.
+__device__ __forceinline__ void tmem_ld16x256_x4(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+        "tcgen05.wait::ld.sync.aligned;\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+
+// Four values (times f) as e4m3 codes, and what that leaves as e5m2 codes.
+__device__ __forceinline__ void split_8(float a, float b, float c, float d, float f, uint32_t &hi,
+                                        uint32_t &lo)
+{
+    const float2 x = make_float2(a * f, b * f), y = make_float2(c * f, d * f);
+    const uint32_t h0 = __nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
+    const uint32_t h1 = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
+    const float2 bx = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)h0, __NV_E4M3)));
+    const float2 by = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)h1, __NV_E4M3)));
+    const uint32_t l0 = __nv_cvt_float2_to_fp8x2(make_float2(x.x - bx.x, x.y - bx.y), __NV_SATFINITE, __NV_E5M2);
+    const uint32_t l1 = __nv_cvt_float2_to_fp8x2(make_float2(y.x - by.x, y.y - by.y), __NV_SATFINITE, __NV_E5M2);
+    hi = h0 | (h1 << 16);
+    lo = l0 | (l1 << 16);
+}
+
+// Eight bf16 values (16 bytes) split: two words of hi, two of lo.
+__device__ __forceinline__ void split_16b(const uint4 &u, float f, uint2 &hi, uint2 &lo)
+{
+    const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u.x));
+    const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u.y));
+    const float2 c = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u.z));
+    const float2 d = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u.w));
+    split_8(a.x, a.y, b.x, b.y, f, hi.x, lo.x);
+    split_8(c.x, c.y, d.x, d.y, f, hi.y, lo.y);
+}
+
+// Largest magnitude of a bf16 pair-wise maximum word, as bits.
+__device__ __forceinline__ uint32_t top_of(uint32_t m) { return max(m & 0xFFFFu, m >> 16); }
+__device__ __forceinline__ uint32_t top_word(const uint4 &u)
+{
+    return __vmaxu2(__vmaxu2(u.x & 0x7FFF7FFFu, u.y & 0x7FFF7FFFu),
+                    __vmaxu2(u.z & 0x7FFF7FFFu, u.w & 0x7FFF7FFFu));
+}
+
+// Exponent e of the scale 2^e that brings a largest magnitude (bf16 bits,
+// finite) to at most 448; 0 for an all-zero row.
+__device__ __forceinline__ int split_exp(uint32_t top)
+{
+    const int e = (int)(top >> 7) - 127 - 8 + ((top & 0x7Fu) > 0x60u ? 1 : 0);
+    return top == 0 ? 0 : max(e, kQ8MinExp);
+}
+__device__ __forceinline__ float two_to(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+// Four codes -> two bf16 pairs (low codes first).  The seven low bits of a
+// code, shifted to bf16's exponent and mantissa, are its magnitude times
+// 2^-120 (subnormals included); NaN codes read as 480.
+__device__ __forceinline__ uint2 codes_to_bf16(uint32_t w)
+{
+    const uint32_t lo = __byte_perm(w, 0u, 0x1404), hi = __byte_perm(w, 0u, 0x3424);
+    const uint32_t a = (lo & 0x80008000u) | ((lo & 0x7F007F00u) >> 4);
+    const uint32_t b = (hi & 0x80008000u) | ((hi & 0x7F007F00u) >> 4);
+    const uint32_t f = 0x7B807B80u;   // 2^120
+    const __nv_bfloat162 fb = *reinterpret_cast<const __nv_bfloat162 *>(&f);
+    const __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&a), fb);
+    const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&b), fb);
+    return make_uint2(*reinterpret_cast<const uint32_t *>(&x), *reinterpret_cast<const uint32_t *>(&y));
+}
+
+// The tile's 128 positions that a row sees, as two words: the first d, then
+// the bits of anc (its root path).
+struct Vis {
+    unsigned long long w[2];
+};
+__device__ __forceinline__ Vis row_vis(unsigned long long anc, int d)
+{
+    Vis v;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+        const int n = min(max(d - 64 * w, 0), 64);
+        unsigned long long m = n == 64 ? ~0ull : ((1ull << n) - 1ull);
+        const int sft = 64 * w - d;   // tree bit of the word's bit 0
+        if (sft >= 0)
+            m |= sft < 64 ? anc >> sft : 0ull;
+        else if (-sft < 64)
+            m |= anc << (-sft);
+        v.w[w] = m;
+    }
+    return v;
+}
+
+// bits 8 j + c0 + e (e = 0, 1) of the words -> bit 2 j + e
+__device__ __forceinline__ uint32_t thread_vis(const Vis &v, int c0)
+{
+    uint32_t vis = 0u;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+        unsigned long long x = (v.w[w] >> c0) & 0x0303030303030303ull;
+        x = (x | (x >> 6)) & 0x000F000F000F000Full;
+        x = (x | (x >> 12)) & 0x000000FF000000FFull;
+        x = (x | (x >> 24)) & 0xFFFFull;
+        vis |= (uint32_t)x << (16 * w);
+    }
+    return vis;
+}
+
+// One 64-position block (half H of the tile) of a thread's rows A and, when
+// TWO, B: weights 2^(x * c + n) packed to bf16 pairs; returns the pair sums.
+template <bool TWO, int H>
+__device__ __forceinline__ void exp_half(const uint32_t (&r)[64], float cA, float nA, float cB,
+                                         float nB, uint32_t (&pA)[16], uint32_t (&pB)[16],
+                                         float &sumA, float &sumB)
+{
+    const uint64_t cA2 = pack2(cA, cA), nA2 = pack2(nA, nA);
+    const uint64_t cB2 = pack2(cB, cB), nB2 = pack2(nB, nB);
+    uint64_t sA = 0ull, sB = 0ull;
+#pragma unroll
+    for (int j = 8 * H; j < 8 * H + 8; ++j) {
+#pragma unroll
+        for (int h = 0; h < (TWO ? 2 : 1); ++h) {
+            const uint64_t y = fma2(pack2(__uint_as_float(r[4 * j + 2 * h]),
+                                          __uint_as_float(r[4 * j + 2 * h + 1])),
+                                    h ? cB2 : cA2, h ? nB2 : nA2);
+            float y0, y1;
+            unpack2(y, y0, y1);
+            const float x0 = ex2(y0), x1 = ex2(y1);
+            const __nv_bfloat162 hv = __floats2bfloat162_rn(x0, x1);
+            const uint32_t hb = *reinterpret_cast<const uint32_t *>(&hv);
+            if (h) {
+                pB[j] = hb;
+                sB = add2(sB, pack2(x0, x1));
+            } else {
+                pA[j] = hb;
+                sA = add2(sA, pack2(x0, x1));
+            }
+        }
+    }
+    float a0, a1;
+    unpack2(sA, a0, a1);
+    sumA = a0 + a1;
+    unpack2(sB, a0, a1);
+    sumB = a0 + a1;
+}
+
+// Maximum of the 16 scores of half H that a thread holds of row A (E = 0) or B (E = 2).
+template <int H, int E>
+__device__ __forceinline__ float half_max(const uint32_t (&r)[64])
+{
+    float m = -INFINITY;
+#pragma unroll
+    for (int j = 8 * H; j < 8 * H + 8; ++j)
+        m = max3f(m, __uint_as_float(r[4 * j + E]), __uint_as_float(r[4 * j + E + 1]));
+    return m;
+}
+
+// Eight rows' P (rows nbase + 0..7, of which the first n_valid are query
+// rows) into the K-major, 128-byte-swizzled P^T tile; other rows go to the
+// scratch kilobyte.
+__device__ __forceinline__ void store_p_half(uint32_t p_addr, uint32_t scratch, int nbase,
+                                             int n_valid, int r_pad, int lane,
+                                             const uint32_t (&pk)[16])
+{
+    const int r = lane & 7, n = nbase + r;
+    const bool valid = r < n_valid;
+    const uint32_t row = p_addr + (uint32_t)((n >> 3) * 1024 + (n & 7) * 128);
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+        const int j = 4 * m + (lane >> 3);
+        const uint32_t addr = valid ? row + (uint32_t)((j >> 3) * (r_pad * 128) +
+                                                       (((j & 7) ^ (n & 7)) << 4))
+                                    : scratch + (uint32_t)(lane << 4);
+        stmatrix_x4(addr, pk[4 * m], pk[4 * m + 1], pk[4 * m + 2], pk[4 * m + 3]);
+    }
+}
+
+// The kernel's workspace, after the header and the counters.
+struct Q8Sync {
+    int32_t *sync;    // [Hkv * groups][4]: tile counter, arrivals, finished combines, unused;
+                      // zero when a call starts, and again when it ends
+    float *part;      // acc fp32 [n_split][T*Hq][128], then (m, l) fp32 [n_split][T*Hq][2]
+    int32_t *flags;   // [n_split][Hkv * groups]: some row's sum outgrew its reference
+    uint8_t *owner;   // [Hkv * groups][n_tiles]: the split that streamed each tile
+};
+
+// Adds one tile to a row's running exact partial (m, l, acc): fp32 online
+// softmax on CUDA cores, one warp, lane holding head dims 4 lane .. + 3.
+__device__ void tile_exact(const AttnQ8Args &a, unsigned long long anc, int g, const float (&q4)[4],
+                           int tile, int nq, float &m, float &l, float (&acc)[4])
+{
+    const int lane = threadIdx.x & 31;
+    const Q8Cache &kc = a.c;
+    const bool q8 = tile < nq;
+    const int r0 = q8 ? tile * kTileN : (tile - nq) * kTileN;
+    const int n = min(kTileN, (q8 ? kc.n_q8 : kc.n_tail + a.n_tree) - r0);
+    for (int i = 0; i < n; ++i) {
+        float k[4], v[4];
+        if (q8) {
+            const int64_t row = (int64_t)g * kc.q8_cap + r0 + i;
+            const int64_t blk = (int64_t)g * (kc.q8_cap / kQ8Block) + (r0 + i) / kQ8Block;
+            const float sk = q8_factor(kc.k_scale[blk]), sv = q8_factor(kc.v_scale[blk]);
+            const uint32_t kw = *reinterpret_cast<const uint32_t *>(kc.k8 + row * kD + 4 * lane);
+            const uint32_t vw = *reinterpret_cast<const uint32_t *>(kc.v8 + row * kD + 4 * lane);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float2 x = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(
+                    (__nv_fp8x2_storage_t)((kw >> (16 * h)) & 0xFFFFu), __NV_E4M3)));
+                const float2 y = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(
+                    (__nv_fp8x2_storage_t)((vw >> (16 * h)) & 0xFFFFu), __NV_E4M3)));
+                k[2 * h] = x.x * sk;
+                k[2 * h + 1] = x.y * sk;
+                v[2 * h] = y.x * sv;
+                v[2 * h + 1] = y.y * sv;
+            }
+        } else {
+            const int tp = r0 + i - kc.n_tail;
+            if (tp >= 0 && !((anc >> tp) & 1ull))
+                continue;
+            const int64_t row = (int64_t)g * kc.tail_cap + r0 + i;
+            const uint2 kb = *reinterpret_cast<const uint2 *>(kc.k_tail + row * kD + 4 * lane);
+            const uint2 vb = *reinterpret_cast<const uint2 *>(kc.v_tail + row * kD + 4 * lane);
+            const float2 k0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&kb.x));
+            const float2 k1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&kb.y));
+            const float2 v0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&vb.x));
+            const float2 v1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&vb.y));
+            k[0] = k0.x; k[1] = k0.y; k[2] = k1.x; k[3] = k1.y;
+            v[0] = v0.x; v[1] = v0.y; v[2] = v1.x; v[3] = v1.y;
+        }
+        float s = q4[0] * k[0] + q4[1] * k[1] + q4[2] * k[2] + q4[3] * k[3];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            s += __shfl_xor_sync(0xffffffffu, s, o);
+        s *= a.scale_log2;
+        if (s > m) {
+            const float f = m == -INFINITY ? 0.f : exp2f(m - s);
+            l *= f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                acc[e] *= f;
+            m = s;
+        }
+        const float p = exp2f(s - m);
+        l += p;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            acc[e] += p * v[e];
+    }
+}
+
+// One output row, by one warp: out = sum_s 2^(m_s - M) acc_s / sum_s
+// 2^(m_s - M) l_s over the splits, a flagged split recomputed exactly.
+__device__ __forceinline__ void combine_row(const AttnQ8Args &a, const TreeMasks &masks, int row,
+                                            int g, int gz, int n_gz, int n_split, int nq,
+                                            int n_tiles_all, const Q8Sync &sy)
+{
+    const int rows_all = a.n_tree * a.n_heads_q;
+    const int lane = threadIdx.x & 31;
+    const float *ws_o = sy.part;
+    const float2 *ws_ml = reinterpret_cast<const float2 *>(ws_o + (size_t)n_split * rows_all * kD);
+    auto ml_of = [&](int s) { return __ldcg(ws_ml + (size_t)s * rows_all + row); };
+    auto acc_of = [&](int s) {
+        return __ldcg(reinterpret_cast<const float4 *>(ws_o + ((size_t)s * rows_all + row) * kD) + lane);
+    };
+    // the first kB splits' columns are in flight while M is formed
+    constexpr int kB = 9;
+    float4 x[kB];
+#pragma unroll
+    for (int u = 0; u < kB; ++u)
+        x[u] = u < n_split ? acc_of(u) : make_float4(0.f, 0.f, 0.f, 0.f);
+    bool any = false;
+    float M = -INFINITY;
+    float2 mine = make_float2(-INFINITY, 0.f);
+    for (int s = lane; s < n_split; s += 32) {
+        any |= __ldcg(sy.flags + (size_t)s * n_gz + gz) != 0;
+        const float2 ml = ml_of(s);
+        if (s == lane)
+            mine = ml;
+        M = fmaxf(M, ml.x);
+    }
+    any = __any_sync(0xffffffffu, any);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    float L = 0.f;
+    if (!any) {
+        for (int s0 = 0; s0 < n_split; s0 += kB) {
+            if (s0 > 0) {
+#pragma unroll
+                for (int u = 0; u < kB; ++u)
+                    x[u] = s0 + u < n_split ? acc_of(s0 + u) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+            for (int u = 0; u < kB; ++u) {
+                const int s = s0 + u;
+                if (s >= n_split)
+                    break;
+                float2 ml;
+                if (s < 32) {
+                    ml.x = __shfl_sync(0xffffffffu, mine.x, s);
+                    ml.y = __shfl_sync(0xffffffffu, mine.y, s);
+                } else {
+                    ml = ml_of(s);
+                }
+                // (a NaN reference keeps its NaN)
+                const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
+                L += w * ml.y;
+                acc[0] += w * x[u].x;
+                acc[1] += w * x[u].y;
+                acc[2] += w * x[u].z;
+                acc[3] += w * x[u].w;
+            }
+        }
+    } else {
+        const uint2 qb = *reinterpret_cast<const uint2 *>(a.q + (size_t)row * kD + 4 * lane);
+        const float2 q01 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&qb.x));
+        const float2 q23 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&qb.y));
+        const float q4[4] = {q01.x, q01.y, q23.x, q23.y};
+        const uint8_t *own = sy.owner + (size_t)gz * n_tiles_all;
+        float Mr = -INFINITY;
+        for (int s = 0; s < n_split; ++s) {
+            float ms, ls, as[4];
+            if (__ldcg(sy.flags + (size_t)s * n_gz + gz) != 0) {
+                ms = -INFINITY;
+                ls = as[0] = as[1] = as[2] = as[3] = 0.f;
+                for (int t0 = 0; t0 < n_tiles_all; t0 += 32) {
+                    const int t = t0 + lane;
+                    uint32_t bits = __ballot_sync(0xffffffffu, t < n_tiles_all && __ldcg(own + t) == s);
+                    while (bits) {
+                        const int tt = t0 + __ffs(bits) - 1;
+                        bits &= bits - 1;
+                        tile_exact(a, masks.anc[row / a.n_heads_q], g, q4, tt, nq, ms, ls, as);
+                    }
+                }
+            } else {
+                const float2 ml = ml_of(s);
+                const float4 y = acc_of(s);
+                ms = ml.x;
+                ls = ml.y;
+                as[0] = y.x;
+                as[1] = y.y;
+                as[2] = y.z;
+                as[3] = y.w;
+            }
+            if (ms == -INFINITY) {
+                L += ls;   // nothing seen: 0, or NaN
+                continue;
+            }
+            const float Mn = fmaxf(Mr, ms);
+            const float fa = Mr == -INFINITY ? 1.f : exp2f(Mr - Mn);   // L may hold a NaN
+            const float fb = exp2f(ms - Mn);
+            L = L * fa + ls * fb;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                acc[e] = acc[e] * fa + as[e] * fb;
+            Mr = Mn;
+        }
+    }
+    const float inv = 1.f / L;
+    const __nv_bfloat162 o0 = __floats2bfloat162_rn(acc[0] * inv, acc[1] * inv);
+    const __nv_bfloat162 o1 = __floats2bfloat162_rn(acc[2] * inv, acc[3] * inv);
+    *reinterpret_cast<uint2 *>(a.out + (size_t)row * kD + 4 * lane) = make_uint2(
+        *reinterpret_cast<const uint32_t *>(&o0), *reinterpret_cast<const uint32_t *>(&o1));
+}
+
+// Bounded wait until the int32 at p (written by other CTAs) reaches target.
+__device__ __forceinline__ bool wait_count_bounded(const int32_t *p, int target,
+                                                   volatile uint32_t *abort, WorkspaceHeader *ws)
+{
+    const long long t0 = clock64();
+    for (;;) {
+        int32_t v;
+        asm volatile("ld.acquire.gpu.global.b32 %0, [%1];\n" : "=r"(v) : "l"(p) : "memory");
+        if (v >= target)
+            return true;
+        if (clock64() - t0 > kWaitCycles) {
+            *abort = 1u;
+            record_status(ws, TS_ERR_TIMEOUT);
+            return false;
+        }
+        __nanosleep(64);
+    }
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
+                    const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ AttnQ8Args a,
+                    const __grid_constant__ TreeMasks masks, int n_split, int nodes_per_group,
+                    Q8Sync sy)
+{
+    const Q8Cache &kc = a.c;
+    const int G = a.n_heads_q / a.n_heads_kv;
+    const int node0 = blockIdx.z * nodes_per_group;
+    const int T = min(nodes_per_group, a.n_tree - node0);
+    const int R = G * T;
+    const int NB = R > kBlockM ? 2 : 1;
+    const int R0 = R < kBlockM ? R : kBlockM, R1 = R - R0;
+    const int rq0 = (R0 + 3) / 4, rq1 = (R1 + 3) / 4;  // rows per lane quarter
+    const int u0 = (rq0 + 15) / 16, u1 = (rq1 + 15) / 16;
+    const int U = u0 + u1;  // softmax warps per lane quarter (at most 3)
+    // the root node's rows 0..G-1 sit in the last block's first lanes; with
+    // more than 16 lanes of them, or split over quarters, softmax rows store
+    // the scores themselves (rs_rows)
+    const int rqL = NB == 2 ? rq1 : rq0;
+    const bool want_rs = a.root_scores != nullptr && node0 == 0;
+    const bool rs_warp0 = want_rs && G <= 8 && G <= rqL;
+    const bool rs_rows = want_rs && !rs_warp0;
+    const Layout lay = q8_layout(R);
+    const int SK = lay.stages_k, SV = lay.stages_v, SVB = lay.stages_vb, r_pad = lay.r_pad;
+
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *base = reinterpret_cast<unsigned char *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    unsigned char *sQ1 = base + lay.q1_off;
+    unsigned char *sP = base + lay.p_off;
+    unsigned char *sVb = base + lay.vb_off;
+    unsigned char *sK = base + lay.k_off;
+    unsigned char *sV = base + lay.v_off;
+    Aux *aux = reinterpret_cast<Aux *>(base + lay.aux_off);
+    Bars *bar = &aux->bar;
+    WorkspaceHeader *hdr = reinterpret_cast<WorkspaceHeader *>(a.workspace);
+    volatile uint32_t *abort = &bar->abort;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int split = blockIdx.x, g = blockIdx.y;
+    const int n_ctx = kc.n_q8 + kc.n_tail;
+    const int tail_rows = kc.n_tail + a.n_tree;
+    const int nq = (kc.n_q8 + kTileN - 1) / kTileN;
+    const int n_tiles_all = nq + (tail_rows + kTileN - 1) / kTileN;
+    const int gz = g * gridDim.z + blockIdx.z;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < SK; ++s) {
+            mbar_init(smem_addr(&bar->full_k[s]), 1);
+            mbar_init(smem_addr(&bar->empty_k[s]), 1);
+        }
+        for (int s = 0; s < SV; ++s) {
+            mbar_init(smem_addr(&bar->full_v[s]), 1);
+            mbar_init(smem_addr(&bar->empty_v[s]), kConvWarps);
+        }
+        const int rs = rs_warp0 ? 1 : 0;
+        mbar_init(smem_addr(&bar->s_free[0]), 4 * u0 + (NB == 1 ? rs : 0));
+        mbar_init(smem_addr(&bar->s_free[1]), (NB == 1 ? 4 * u0 : 4 * u1) + rs);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_addr(&bar->vb_full[i]), kConvWarps);
+            mbar_init(smem_addr(&bar->s_full[i]), 1);
+            mbar_init(smem_addr(&bar->sm_done[i]), 4 * U);
+            mbar_init(smem_addr(&bar->pv_done[i]), 1);
+            mbar_init(smem_addr(&bar->drain[i]), 1);
+        }
+        mbar_init(smem_addr(&bar->o_final), 1);
+        mbar_init(smem_addr(&bar->conv), kConvWarps);
+        bar->abort = 0u;
+        bar->overflow = 0;
+        fence_mbar_init();
+        launch_dependents();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_addr(&bar->tmem_base), kTmemCols);
+        tmem_relinquish();
+    }
+    if (warp == 3 && lane == 0 && nq > 0) {
+        prefetch_tmap(&tmap_k);
+        prefetch_tmap(&tmap_v);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    // a programmatic dependent: what follows reads the previous kernel's results
+    grid_dependency_wait();
+    const uint32_t tmem = bar->tmem_base;
+
+    auto q_row = [&](int n) {
+        return reinterpret_cast<const uint4 *>(
+            a.q + ((int64_t)(node0 + n / G) * a.n_heads_q + g * G + n % G) * kD);
+    };
+
+    if (warp < 4) {
+        regs_dec<kRegsOther>();
+        if (warp == 0)
+            for (int i = lane; i < a.n_tree; i += 32)
+                aux->anc[i] = masks.anc[i];
+        if (warp != 3) {
+            tc_fence_before();
+            named_bar_sync(kBarQuery, kThreads - 32 * (1 + kConvWarps));
+            tc_fence_after();
+        }
+        if (warp == 3) {
+            // ------------------------------------------------ TMA producer
+            if (lane == 0) {
+                auto tile_at = [&](int k) { return n_tiles_all - 1 - k; };
+                int32_t *ctr = sy.sync + 4 * gz;
+                const uint8_t *ksc = kc.k_scale + (int64_t)g * (kc.q8_cap / kQ8Block);
+                const uint8_t *vsc = kc.v_scale + (int64_t)g * (kc.q8_cap / kQ8Block);
+                const int n_blk = kc.n_q8 / kQ8Block;
+                // scale bytes of a tile's two blocks (127, a factor of one,
+                // past the last block and on a tail tile)
+                auto scales = [&](int tile, uint32_t (&b)[4]) {
+                    const int b0 = 2 * tile;
+                    const bool h0 = tile >= 0 && b0 < n_blk, h1 = tile >= 0 && b0 + 1 < n_blk;
+                    b[0] = h0 ? __ldg(ksc + b0) : 127u;
+                    b[1] = h1 ? __ldg(ksc + b0 + 1) : 127u;
+                    b[2] = h0 ? __ldg(vsc + b0) : 127u;
+                    b[3] = h1 ? __ldg(vsc + b0 + 1) : 127u;
+                };
+                // tile i is issued while the scales of tile i + 1 and the
+                // hand-out of tile i + 2 are on their way
+                uint32_t sc_cur[4], sc_nxt[4];
+                int cur = tile_at(split);
+                scales(cur, sc_cur);
+                int nxt = tile_at(n_split + atomicAdd(&ctr[0], 1));
+                scales(nxt, sc_nxt);
+                int k_nn = atomicAdd(&ctr[0], 1);
+                uint8_t *owner = sy.owner + (size_t)gz * n_tiles_all;
+                const uint64_t pol = l2_evict_first_policy();
+                int ke = 0;             // K ring entries used
+                int vn = 0;             // V ring entries used
+                int k_tma = -1, v_tma = -1;   // last entries that were TMA loads
+                bool ok = true;
+                auto issue_v = [&](int t) {
+                    const int s = t % SV;
+                    if (t >= SV && !wait_bounded(smem_addr(&bar->empty_v[s]), ((t / SV) & 1) ^ 1,
+                                                 abort, hdr))
+                        return false;
+                    const uint32_t fb = smem_addr(&bar->full_v[s]);
+                    const int tile = bar->tile_of[t % kTileRing];
+                    if (tile < 0 || tile >= nq) {
+                        mbar_arrive(fb);   // the end, or a tail tile: the converters take it
+                    } else {
+                        mbar_arrive_expect_tx(fb, kRawBytes);
+                        tma_load_3d_hint(smem_addr(sV + s * kRawBytes), &tmap_v, 0, tile * kTileN,
+                                         g, fb, pol);
+                        v_tma = t;
+                    }
+                    return true;
+                };
+                for (int i = 0; ok; ++i) {
+                    const int tile = cur < 0 ? -1 : cur;
+                    const bool tail = tile >= nq;
+                    bar->tile_of[i % kTileRing] = tile;
+                    bar->scale_of[i % kTileRing] =
+                        sc_cur[0] | (sc_cur[1] << 8) | (sc_cur[2] << 16) | (sc_cur[3] << 24);
+                    bar->entry_of[i % kTileRing] = ke;
+                    if (tile >= 0)
+                        owner[tile] = (uint8_t)split;
+                    for (int part = 0; part < (tail ? 2 : 1) && ok; ++part, ++ke) {
+                        const int s = ke % SK;
+                        if (ke >= SK && !wait_bounded(smem_addr(&bar->empty_k[s]),
+                                                      ((ke / SK) & 1) ^ 1, abort, hdr)) {
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t fb = smem_addr(&bar->full_k[s]);
+                        if (tile < 0) {
+                            mbar_arrive(fb);   // no tile left: the QK issuer passes it on
+                        } else if (!tail) {
+                            mbar_arrive_expect_tx(fb, kRawBytes);
+                            tma_load_3d_hint(smem_addr(sK + s * kRawBytes), &tmap_k, 0,
+                                             tile * kTileN, g, fb, pol);
+                            k_tma = ke;
+                        }   // a tail tile's slots are filled by the converters
+                    }
+                    if (!ok)
+                        break;
+                    cur = nxt;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        sc_cur[e] = sc_nxt[e];
+                    nxt = tile_at(n_split + k_nn);
+                    scales(nxt, sc_nxt);
+                    if (nxt >= 0)
+                        k_nn = atomicAdd(&ctr[0], 1);
+                    // V one tile behind K; a tail tile's (and the end) at once
+                    while (ok && (vn < i || (vn == i && (tail || tile < 0))))
+                        ok = issue_v(vn++);
+                    if (tile < 0)
+                        break;
+                }
+                if (*abort) {
+                    // our own copies land before the CTA exits
+                    for (int t = max(0, k_tma - SK + 1); t <= k_tma; ++t)
+                        wait_drain(smem_addr(&bar->full_k[t % SK]), (t / SK) & 1);
+                    for (int t = max(0, v_tma - SV + 1); t <= v_tma; ++t)
+                        wait_drain(smem_addr(&bar->full_v[t % SV]), (t / SV) & 1);
+                }
+            }
+        } else if (warp == 0) {
+            // ------------------------------------ root node's scores out of S
+            if (rs_warp0) {
+                const int r = lane >> 2;
+                const bool mine = r < G;
+                const int c0 = 2 * (lane & 3);
+                const float rsc = aux->row_scale[NB == 2 ? kBlockM + (mine ? r : 0) : (mine ? r : 0)];
+                float *dst_row = a.root_scores + (size_t)(g * G + (mine ? r : 0)) * n_ctx;
+                const bool vec = ((reinterpret_cast<uintptr_t>(a.root_scores) | (uintptr_t)n_ctx * 4) & 7) == 0;
+                for (int t = 0;; ++t) {
+                    const int slot = NB == 2 ? 1 : (t & 1), ph = NB == 2 ? (t & 1) : ((t >> 1) & 1);
+                    if (!warp_wait_bounded(smem_addr(&bar->s_full[slot]), ph, abort, hdr))
+                        break;
+                    const int tile = bar->tile_of[t % kTileRing];
+                    if (tile < 0)
+                        break;
+                    tc_fence_after();
+                    const uint32_t sc = bar->scale_of[t % kTileRing];
+                    const bool q8 = tile < nq;
+                    const int r0 = (q8 ? tile : tile - nq) * kTileN;
+                    const int left = (q8 ? kc.n_q8 : kc.n_tail) - r0;   // context positions here
+                    const int pos0 = q8 ? r0 : kc.n_q8 + r0;
+#pragma unroll
+                    for (int qd = 0; qd < 4; ++qd) {
+                        if (32 * qd >= left)
+                            break;   // uniform: nothing of the context from here on
+                        uint32_t rr[16];
+                        tmem_ld16x256_x4(tmem + kSCol + 128 * slot + 32 * qd, rr);
+                        if (mine) {
+                            const float f = rsc * q8_factor((sc >> (qd < 2 ? 0 : 8)) & 0xFFu);
+#pragma unroll
+                            for (int jj = 0; jj < 4; ++jj) {
+                                const int p = 32 * qd + 8 * jj + c0;
+                                float x0 = __uint_as_float(rr[4 * jj]) * f;
+                                float x1 = __uint_as_float(rr[4 * jj + 1]) * f;
+                                if (!q8) {
+                                    const uint32_t bk = bar->bad_k[t & 3][qd] >> (8 * jj + c0);
+                                    x0 = bk & 1u ? __uint_as_float(0x7FC00000u) : x0;
+                                    x1 = bk & 2u ? __uint_as_float(0x7FC00000u) : x1;
+                                }
+                                float *dst = dst_row + pos0 + p;
+                                if (vec && p + 1 < left) {
+                                    *reinterpret_cast<float2 *>(dst) = make_float2(x0, x1);
+                                } else {
+                                    if (p < left)
+                                        dst[0] = x0;
+                                    if (p + 1 < left)
+                                        dst[1] = x1;
+                                }
+                            }
+                        }
+                        __syncwarp();   // the next TMEM load is the whole warp's
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(smem_addr(&bar->s_free[slot]));
+                }
+            }
+        } else if (lane == 0 && warp == 1) {
+            // ------------------------------------------------ QK issuer
+            constexpr uint32_t id[4] = {idesc_f8(kBlockM, kTileN, 0, 0), idesc_f8(kBlockM, kTileN, 1, 0),
+                                        idesc_f8(kBlockM, kTileN, 0, 1), idesc_f8(kBlockM, kTileN, 1, 1)};
+            const uint64_t kd0 = sdesc_sw128(smem_addr(sK), 16, 1024);
+            const uint64_t qd0 = sdesc_sw128(smem_addr(sQ1), 16, 1024);
+            int ke = 0;
+            for (int t = 0;; ++t) {
+                if (!wait_bounded(smem_addr(&bar->full_k[ke % SK]), (ke / SK) & 1, abort, hdr))
+                    break;
+                const int tile = bar->tile_of[t % kTileRing];
+                const int parts = tile >= nq ? 2 : 1;
+                bool ok = parts == 1 || wait_bounded(smem_addr(&bar->full_k[(ke + 1) % SK]),
+                                                     ((ke + 1) / SK) & 1, abort, hdr);
+                for (int b = 0; b < NB && ok; ++b) {
+                    const int slot = NB == 2 ? b : (t & 1);
+                    const int used = NB == 2 ? t : (t >> 1);   // earlier tiles in this slot
+                    if (used > 0 && !wait_bounded(smem_addr(&bar->s_free[slot]), (used - 1) & 1,
+                                                  abort, hdr)) {
+                        ok = false;
+                        break;
+                    }
+                    if (tile < 0) {
+                        mbar_arrive(smem_addr(&bar->s_full[slot]));   // the end
+                        continue;
+                    }
+                    tc_fence_after();
+                    const uint32_t d = tmem + kSCol + 128 * slot;
+                    for (int part = 0; part < parts; ++part) {
+                        const uint64_t kd = kd0 + (uint64_t)((ke + part) % SK) * (kRawBytes >> 4);
+#pragma unroll
+                        for (int lo = 0; lo < 2; ++lo)
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk) {
+                                const bool acc = part + lo + kk > 0;
+                                const uint32_t idesc = part ? id[2 + lo] : id[lo];
+                                if (b == 0)
+                                    mma8_ts(d, tmem + kQCol + 32 * lo + 8 * kk, kd + 2 * kk, idesc, acc);
+                                else
+                                    mma8_ss(d, qd0 + lo * ((kBlockM * kD) >> 4) + 2 * kk, kd + 2 * kk,
+                                            idesc, acc);
+                            }
+                    }
+                    mma_commit(smem_addr(&bar->s_full[slot]));
+                }
+                if (!ok || tile < 0)
+                    break;
+                for (int part = 0; part < parts; ++part)
+                    mma_commit(smem_addr(&bar->empty_k[(ke + part) % SK]));
+                ke += parts;
+            }
+            mma_commit(smem_addr(&bar->drain[0]));
+            wait_drain(smem_addr(&bar->drain[0]), 0);
+        } else if (lane == 0) {
+            // ------------------------------------------------ PV issuer
+            const uint32_t idesc = idesc_bf16(kD, r_pad, 1, 0);
+            const uint64_t vd0 = sdesc_sw128(smem_addr(sVb), kBoxBytes, 1024);
+            const uint64_t pd0 = sdesc_sw128(smem_addr(sP), 16, 1024);
+            const uint32_t p_half = (uint32_t)r_pad * 128;
+            for (int t = 0;; ++t) {
+                const int s = t % SVB;
+                if (!wait_bounded(smem_addr(&bar->vb_full[s]), (t / SVB) & 1, abort, hdr))
+                    break;
+                if (bar->tile_of[t % kTileRing] < 0) {
+                    mma_commit(smem_addr(&bar->o_final));   // after the last PV
+                    break;
+                }
+                if (!wait_bounded(smem_addr(&bar->sm_done[t & 1]), (t >> 1) & 1, abort, hdr))
+                    break;
+                tc_fence_after();
+                const uint64_t vd = vd0 + (uint64_t)s * (kVbBytes >> 4);
+                const uint64_t pd = pd0 + (uint64_t)(t & 1) * ((uint64_t)(r_pad * 256) >> 4);
+                if (t == 0)
+                    mma_ss_c<0>(tmem, vd, pd, idesc);
+                else
+                    mma_ss_c<1>(tmem, vd, pd, idesc);
+#pragma unroll
+                for (int kk = 1; kk < kTileN / 16; ++kk)
+                    mma_ss_c<1>(tmem, vd + ((kk * 2048) >> 4),
+                                pd + (((kk >> 2) * p_half + (kk & 3) * 32) >> 4), idesc);
+                mma_commit(smem_addr(&bar->pv_done[t & 1]));
+            }
+            mma_commit(smem_addr(&bar->drain[1]));
+            wait_drain(smem_addr(&bar->drain[1]), 0);
+        }
+        __syncwarp();
+        regs_inc<kRegsLaunch>();
+    } else if (warp >= 16) {
+        // ------------------------------------------------ converters
+        regs_dec<kRegsOther>();
+        const int tid = threadIdx.x - 512;   // 0..127
+        int met = 0;                         // meetings of the converter warps so far
+        for (int t = 0;; ++t) {
+            const int s = t % SV;
+            if (!warp_wait_bounded(smem_addr(&bar->full_v[s]), (t / SV) & 1, abort, hdr))
+                break;
+            const int tile = bar->tile_of[t % kTileRing];
+            if (tile < 0) {
+                // the PV issuer's end, once it is past the slot's last tile (two
+                // phases at once would pass it by)
+                if (t >= SVB && !warp_wait_bounded(smem_addr(&bar->pv_done[(t - SVB) & 1]),
+                                                   ((t - SVB) >> 1) & 1, abort, hdr))
+                    break;
+                if (lane == 0)
+                    mbar_arrive(smem_addr(&bar->vb_full[t % SVB]));
+                break;
+            }
+            unsigned char *vb = sVb + (t % SVB) * kVbBytes;
+            const __nv_bfloat16 *vrow = nullptr;
+            if (tile >= nq) {
+                // a tail tile, one row per thread: keys into two K slots
+                const int row = (tile - nq) * kTileN + tid;
+                const int64_t at = ((int64_t)g * kc.tail_cap + row) * kD;
+                const bool have = row < tail_rows;
+                const uint4 *kr = reinterpret_cast<const uint4 *>(kc.k_tail + at);
+                const uint4 *vr = reinterpret_cast<const uint4 *>(kc.v_tail + at);
+                uint32_t tk = 0, tv = 0;
+                if (have) {
+#pragma unroll 4
+                    for (int c = 0; c < kD / 8; ++c) {
+                        tk = __vmaxu2(tk, top_word(__ldg(kr + c)));
+                        tv = __vmaxu2(tv, top_word(__ldg(vr + c)));
+                    }
+                }
+                tk = top_of(tk);
+                tv = top_of(tv);
+                const bool bad_k = tk >= 0x7F80u, bad = bad_k || tv >= 0x7F80u;
+                const uint32_t wk = __ballot_sync(0xffffffffu, bad_k), wb = __ballot_sync(0xffffffffu, bad);
+                const uint32_t wtop = __reduce_max_sync(0xffffffffu, bad ? 0u : tk);
+                if (lane == 0) {
+                    bar->bad_k[t & 3][warp - 16] = wk;
+                    bar->bad[t & 3][warp - 16] = wb;
+                    bar->top[warp - 16] = wtop;
+                    mbar_arrive(smem_addr(&bar->conv));
+                }
+                if (!warp_wait_bounded(smem_addr(&bar->conv), met++ & 1, abort, hdr))
+                    break;
+                // a block's two warps share its scale
+                const int w2 = (warp - 16) & 2;
+                const uint32_t top = max(*(volatile uint32_t *)&bar->top[w2],
+                                         *(volatile uint32_t *)&bar->top[w2 + 1]);
+                const int e = split_exp(top);
+                if (tid == 0) {
+                    const int e1 = split_exp(max(*(volatile uint32_t *)&bar->top[2],
+                                                 *(volatile uint32_t *)&bar->top[3]));
+                    bar->scale_of[t % kTileRing] =
+                        (uint32_t)(e + 127) | ((uint32_t)(e1 + 127) << 8) | (127u << 16) | (127u << 24);
+                }
+                const int e0 = bar->entry_of[t % kTileRing];
+                unsigned char *khi = sK + (e0 % SK) * kRawBytes, *klo = sK + ((e0 + 1) % SK) * kRawBytes;
+                const float f = two_to(-e);
+#pragma unroll 2
+                for (int c = 0; c < kD / 16; ++c) {   // 16 codes a step
+                    uint4 hi = make_uint4(0u, 0u, 0u, 0u), lo = hi;
+                    if (have && !bad) {
+                        uint2 h0, l0, h1, l1;
+                        split_16b(__ldg(kr + 2 * c), f, h0, l0);
+                        split_16b(__ldg(kr + 2 * c + 1), f, h1, l1);
+                        hi = make_uint4(h0.x, h0.y, h1.x, h1.y);
+                        lo = make_uint4(l0.x, l0.y, l1.x, l1.y);
+                    }
+                    const int off = tid * 128 + ((c ^ (tid & 7)) << 4);
+                    *reinterpret_cast<uint4 *>(khi + off) = hi;
+                    *reinterpret_cast<uint4 *>(klo + off) = lo;
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_addr(&bar->conv));
+                if (!warp_wait_bounded(smem_addr(&bar->conv), met++ & 1, abort, hdr))
+                    break;
+                if (tid == 0) {
+                    mbar_arrive(smem_addr(&bar->full_k[e0 % SK]));
+                    mbar_arrive(smem_addr(&bar->full_k[(e0 + 1) % SK]));
+                }
+                vrow = have && !bad ? kc.v_tail + at : nullptr;
+            }
+            // the bf16 slot is free once PV of the tile before it in it is done
+            if (t >= SVB && !warp_wait_bounded(smem_addr(&bar->pv_done[(t - SVB) & 1]),
+                                               ((t - SVB) >> 1) & 1, abort, hdr))
+                break;
+            if (tile < nq) {
+                // 16 codes per thread and step: a warp reads 512 consecutive
+                // bytes; halves 0 and 1 of V's columns write their two chunks in
+                // opposite order, so that eight lanes' stores hit eight banks
+                const unsigned char *raw = sV + s * kRawBytes;
+#pragma unroll
+                for (int i = 0; i < kRawBytes / (16 * 32 * kConvWarps); ++i) {
+                    const int u = tid + i * 32 * kConvWarps;   // 16-byte unit of the tile
+                    const int p = u >> 3, c16 = u & 7;
+                    const uint4 w = *reinterpret_cast<const uint4 *>(raw + 16 * u);
+                    const uint2 x0 = codes_to_bf16(w.x), x1 = codes_to_bf16(w.y);
+                    const uint2 x2 = codes_to_bf16(w.z), x3 = codes_to_bf16(w.w);
+                    const uint4 first = make_uint4(x0.x, x0.y, x1.x, x1.y);
+                    const uint4 second = make_uint4(x2.x, x2.y, x3.x, x3.y);
+                    const int half = c16 >> 2, ch = 2 * (c16 & 3);
+                    unsigned char *dst = vb + half * kBoxBytes + p * 128;
+                    const int a0 = ((ch + half) ^ (p & 7)) << 4, a1 = ((ch + 1 - half) ^ (p & 7)) << 4;
+                    *reinterpret_cast<uint4 *>(dst + a0) = half ? second : first;
+                    *reinterpret_cast<uint4 *>(dst + a1) = half ? first : second;
+                }
+            } else {
+#pragma unroll 4
+                for (int c = 0; c < kD / 8; ++c)
+                    *reinterpret_cast<uint4 *>(vb + (c >> 3) * kBoxBytes + tid * 128 +
+                                               (((c & 7) ^ (tid & 7)) << 4)) =
+                        vrow ? __ldg(reinterpret_cast<const uint4 *>(vrow) + c)
+                             : make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(smem_addr(&bar->vb_full[t % SVB]));
+                mbar_arrive(smem_addr(&bar->empty_v[s]));
+            }
+        }
+        __syncwarp();
+        regs_inc<kRegsLaunch>();
+    } else {
+        regs_inc<kRegsSoftmax>();
+        // ---- query rows of this KV head: row n = node * G + (head - g*G),
+        // block 0 into TMEM lanes (warps 4-7), block 1 into the shared-memory
+        // A tile (warps 8-11), each split into hi and lo codes
+        if (warp < 8 || (NB == 2 && warp < 12)) {
+            const int b = warp < 8 ? 0 : 1, q = warp & 3;
+            const int rqb = b ? rq1 : rq0, Rb = b ? R1 : R0;
+            const int n = kBlockM * b + q * rqb + lane;
+            const bool valid = lane < rqb && q * rqb + lane < Rb;
+            uint32_t hi[32], lo[32];
+            uint32_t top = 0;
+            uint4 u[16];
+            const uint4 *src = valid ? q_row(q8_row_of(n, R)) : nullptr;
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+                u[c] = valid ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+                top = __vmaxu2(top, top_word(u[c]));
+            }
+            top = top_of(top);
+            const bool bad = top >= 0x7F80u;
+            const int e = bad ? 0 : split_exp(top);
+            const float f = two_to(-e);
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+                uint2 h, l;
+                split_16b(u[c], f, h, l);
+                hi[2 * c] = h.x;
+                hi[2 * c + 1] = h.y;
+                lo[2 * c] = l.x;
+                lo[2 * c + 1] = l.y;
+            }
+            if (valid)
+                aux->row_scale[n] = bad ? __uint_as_float(0x7FC00000u) : a.scale_log2 * two_to(e);
+            if (b == 0) {
+                const uint32_t qa = tmem + ((uint32_t)(q * 32) << 16) + kQCol;
+                tmem_st32(qa, hi);
+                tmem_st32(qa + 32, lo);
+                tmem_st_wait();
+            } else {
+                const int m = q * 32 + lane;   // A-tile row = TMEM lane of S_1
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const int off = m * 128 + ((c ^ (m & 7)) << 4);
+                    *reinterpret_cast<uint4 *>(sQ1 + off) =
+                        make_uint4(hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
+                    *reinterpret_cast<uint4 *>(sQ1 + kBlockM * kD + off) =
+                        make_uint4(lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
+                }
+                fence_proxy_async_smem();
+            }
+        }
+        tc_fence_before();
+        named_bar_sync(kBarQuery, kThreads - 32 * (1 + kConvWarps));
+        tc_fence_after();
+        if ((warp - 4) / 4 < U) {
+            // ------------------------------------------------ softmax
+            const int q = warp & 3, j = (warp - 4) >> 2;
+            const int b = j < u0 ? 0 : 1;
+            const int lb = 16 * (b == 0 ? j : j - u0);  // unit's first lane in the quarter
+            const int Rb = b == 0 ? R0 : R1, rqb = b == 0 ? rq0 : rq1;
+            const int iA = lb + (lane >> 2), iB = iA + 8;
+            const bool vA = iA < rqb && q * rqb + iA < Rb;
+            const bool vB = iB < rqb && q * rqb + iB < Rb;
+            const bool hasA = __any_sync(0xffffffffu, vA), hasB = __any_sync(0xffffffffu, vB);
+            const int nA = kBlockM * b + q * rqb + iA, nB = nA + 8;
+            const uint32_t s_addr = tmem + ((uint32_t)(32 * q + lb) << 16) + kSCol;
+            const int c0 = 2 * (lane & 3);
+            const int nbase = kBlockM * b + q * rqb + lb;
+            const int nvA = max(0, min(8, min(rqb - lb, Rb - q * rqb - lb)));
+            const int nvB = max(0, min(8, min(rqb - lb - 8, Rb - q * rqb - lb - 8)));
+            const uint32_t p_addr = smem_addr(sP);
+            const uint32_t p_scratch = p_addr + (uint32_t)r_pad * 512;
+            const float rsA = vA ? aux->row_scale[nA] : 1.f, rsB = vB ? aux->row_scale[nB] : 1.f;
+            float mA = -INFINITY, mB = -INFINITY, lA = 0.f, lB = 0.f;
+            bool ok = true;
+            for (int t = 0;; ++t) {
+                const int slot = NB == 2 ? b : (t & 1), ph = NB == 2 ? (t & 1) : ((t >> 1) & 1);
+                if (!warp_wait_bounded(smem_addr(&bar->s_full[slot]), ph, abort, hdr)) {
+                    ok = false;
+                    break;
+                }
+                const int tile = bar->tile_of[t % kTileRing];
+                if (tile < 0)
+                    break;
+                const uint32_t sc = bar->scale_of[t % kTileRing];
+                tc_fence_after();
+                uint32_t r[64];
+                tmem_ld16x256_x16(s_addr + 128 * slot, r);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_addr(&bar->s_free[slot]));
+                // factors of the tile's two blocks: scores (never zero: a
+                // masked score is -inf), and the exponent V's scale adds
+                const float k0 = q8_factor(sc & 0xFFu), k1 = q8_factor((sc >> 8) & 0xFFu);
+                constexpr float kTiny = 1.17549435e-38f;
+                const float cA0 = rsA * k0 < kTiny ? kTiny : rsA * k0;
+                const float cA1 = rsA * k1 < kTiny ? kTiny : rsA * k1;
+                const float cB0 = rsB * k0 < kTiny ? kTiny : rsB * k0;
+                const float cB1 = rsB * k1 < kTiny ? kTiny : rsB * k1;
+                const bool tail = tile >= nq;
+                const int r0 = (tail ? tile - nq : tile) * kTileN;
+                const int left = (tail ? kc.n_tail : kc.n_q8) - r0;   // context positions here
+                if (left < kTileN) {
+                    const unsigned long long ancA = tail ? aux->anc[node0 + (vA ? q8_row_of(nA, R) / G : 0)] : 0ull;
+                    const unsigned long long ancB = tail ? aux->anc[node0 + (vB ? q8_row_of(nB, R) / G : 0)] : 0ull;
+                    const Vis wA = row_vis(ancA, left), wB = row_vis(ancB, left);
+                    const uint32_t visA = thread_vis(wA, c0), visB = thread_vis(wB, c0);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        if (!((visA >> k) & 1u))
+                            r[4 * (k >> 1) + (k & 1)] = __float_as_uint(-INFINITY);
+                        if (!((visB >> k) & 1u))
+                            r[4 * (k >> 1) + 2 + (k & 1)] = __float_as_uint(-INFINITY);
+                    }
+                }
+                if (tail) {
+                    const uint32_t *bw = bar->bad[t & 3];
+                    const unsigned long long b0 = bw[0] | ((unsigned long long)bw[1] << 32);
+                    const unsigned long long b1 = bw[2] | ((unsigned long long)bw[3] << 32);
+                    if (b0 | b1) {
+                        const Vis wA = row_vis(aux->anc[node0 + (vA ? q8_row_of(nA, R) / G : 0)], left);
+                        const Vis wB = row_vis(aux->anc[node0 + (vB ? q8_row_of(nB, R) / G : 0)], left);
+                        if ((wA.w[0] & b0) | (wA.w[1] & b1))
+                            lA = __uint_as_float(0x7FC00000u);
+                        if ((wB.w[0] & b0) | (wB.w[1] & b1))
+                            lB = __uint_as_float(0x7FC00000u);
+                    }
+                }
+                if (rs_rows) {
+                    // the root node's rows store their own scores
+                    const int pos0 = tail ? kc.n_q8 + r0 : r0;
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        const int p = 8 * (k >> 1) + c0 + (k & 1);
+                        const bool bk = tail && ((bar->bad_k[t & 3][p >> 5] >> (p & 31)) & 1u);
+                        if (p < left) {
+                            const int hA = q8_row_of(nA, R), hB = q8_row_of(nB, R);
+                            if (vA && hA < G)
+                                a.root_scores[(size_t)(g * G + hA) * n_ctx + pos0 + p] =
+                                    bk ? __uint_as_float(0x7FC00000u)
+                                       : __uint_as_float(r[4 * (k >> 1) + (k & 1)]) * (rsA * (k < 16 ? k0 : k1));
+                            if (vB && hB < G)
+                                a.root_scores[(size_t)(g * G + hB) * n_ctx + pos0 + p] =
+                                    bk ? __uint_as_float(0x7FC00000u)
+                                       : __uint_as_float(r[4 * (k >> 1) + 2 + (k & 1)]) * (rsB * (k < 16 ? k0 : k1));
+                        }
+                    }
+                }
+                // a row that has seen nothing yet takes this tile's max,
+                // rounded up to an integer, as its reference
+                if (__any_sync(0xffffffffu, mA == -INFINITY || mB == -INFINITY)) {
+                    float yA = fmaxf(half_max<0, 0>(r) * cA0, half_max<1, 0>(r) * cA1);
+                    float yB = fmaxf(half_max<0, 2>(r) * cB0, half_max<1, 2>(r) * cB1);
+                    yA = fmaxf(yA, __shfl_xor_sync(0xffffffffu, yA, 1));
+                    yB = fmaxf(yB, __shfl_xor_sync(0xffffffffu, yB, 1));
+                    yA = fmaxf(yA, __shfl_xor_sync(0xffffffffu, yA, 2));
+                    yB = fmaxf(yB, __shfl_xor_sync(0xffffffffu, yB, 2));
+                    if (mA == -INFINITY)
+                        mA = ceilf(yA);
+                    if (mB == -INFINITY)
+                        mB = ceilf(yB);
+                }
+                uint32_t pA[16], pB[16];
+                {
+                    const float v0 = q8_log2((sc >> 16) & 0xFFu), v1 = q8_log2(sc >> 24);
+                    const float i0 = q8_inverse((sc >> 16) & 0xFFu), i1 = q8_inverse(sc >> 24);
+                    const float nmA = mA == -INFINITY ? 0.f : -mA;
+                    const float nmB = mB == -INFINITY ? 0.f : -mB;
+                    float sA, sB;
+                    if (hasB) {
+                        exp_half<true, 0>(r, cA0, nmA + v0, cB0, nmB + v0, pA, pB, sA, sB);
+                        lA += sA * i0;
+                        lB += sB * i0;
+                        exp_half<true, 1>(r, cA1, nmA + v1, cB1, nmB + v1, pA, pB, sA, sB);
+                        lA += sA * i1;
+                        lB += sB * i1;
+                    } else if (hasA) {
+                        exp_half<false, 0>(r, cA0, nmA + v0, cB0, nmB + v0, pA, pB, sA, sB);
+                        lA += sA * i0;
+                        exp_half<false, 1>(r, cA1, nmA + v1, cB1, nmB + v1, pA, pB, sA, sB);
+                        lA += sA * i1;
+                    }
+                }
+                // this P^T tile is free once PV(t - 2) is done
+                if (t >= 2 && !warp_wait_bounded(smem_addr(&bar->pv_done[t & 1]),
+                                                 ((t - 2) >> 1) & 1, abort, hdr)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t p_tile = p_addr + (uint32_t)(t & 1) * (uint32_t)r_pad * 256;
+                if (hasA)
+                    store_p_half(p_tile, p_scratch, nbase, nvA, r_pad, lane, pA);
+                if (hasB)
+                    store_p_half(p_tile, p_scratch, nbase + 8, nvB, r_pad, lane, pB);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_addr(&bar->sm_done[t & 1]));
+            }
+            // ---- (m, l) of each row (four threads' partial sums), then O^T
+#pragma unroll
+            for (int o = 1; o <= 2; o <<= 1) {
+                lA += __shfl_xor_sync(0xffffffffu, lA, o);
+                lB += __shfl_xor_sync(0xffffffffu, lB, o);
+            }
+            // a sum past 2^63 flags the split for the exact recompute (NaN
+            // stays NaN)
+            const bool over = (vA && lA > kMaxRowSum) || (vB && lB > kMaxRowSum);
+            if (__any_sync(0xffffffffu, over) && lane == 0)
+                bar->overflow = 1;
+            const int rows_all = a.n_tree * a.n_heads_q;
+            float *ws_o = sy.part;
+            float2 *ws_ml = reinterpret_cast<float2 *>(ws_o + (size_t)n_split * rows_all * kD);
+            auto orow_of = [&](int n) {
+                const int m = q8_row_of(n, R);
+                return (node0 + m / G) * a.n_heads_q + g * G + m % G;
+            };
+            if (ok && (lane & 3) == 0) {
+                if (vA)
+                    ws_ml[(size_t)split * rows_all + orow_of(nA)] = make_float2(mA, lA);
+                if (vB)
+                    ws_ml[(size_t)split * rows_all + orow_of(nB)] = make_float2(mB, lB);
+            }
+            // O^T out of TMEM into the P^T tiles (free after the last PV, and
+            // just as large) in output order, then one bulk copy per node
+            const bool have_o = ok && warp_wait_bounded(smem_addr(&bar->o_final), 0, abort, hdr);
+            if (have_o) {
+                tc_fence_after();
+                for (int c = 32 * j; c < r_pad; c += 32 * U) {
+                    uint32_t o[32];
+                    tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + c, o);
+                    const int nv = min(32, R - c);
+                    float *dst = reinterpret_cast<float *>(sP) + (size_t)q8_row_of(c, R) * kD + 32 * q + lane;
+#pragma unroll
+                    for (int jj = 0; jj < 32; ++jj)
+                        if (jj < nv)
+                            dst[jj * kD] = __uint_as_float(o[jj]);
+                }
+            }
+            fence_proxy_async_smem();
+            named_bar_sync(kBarOut, 128 * U);   // every softmax warp, whatever its path
+            if (!*abort && lane == 0) {
+                const int sw = warp - 4;   // 0 .. 4U-1
+                for (int node = sw; node < T; node += 4 * U)
+                    bulk_store(ws_o + ((size_t)split * rows_all + (size_t)(node0 + node) * a.n_heads_q + g * G) * kD,
+                               smem_addr(sP) + (uint32_t)(node * G * kD * 4), (uint32_t)(G * kD * 4));
+                bulk_commit();
+                bulk_wait_all();
+                fence_proxy_async_global();
+            }
+        }
+        __syncwarp();
+        regs_dec<kRegsLaunch>();
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+
+    // ---- combine: once every split of this (head, group) has arrived, each
+    // folds rows split, split + n_split, ... (one warp each)
+    const int n_gz = a.n_heads_kv * gridDim.z;
+    int32_t *ctr = sy.sync + 4 * gz;
+    if (threadIdx.x == 0) {
+        sy.flags[(size_t)split * n_gz + gz] = bar->overflow;
+        __threadfence();   // partials, flag and owner entries before the arrival
+        atomicAdd(&ctr[1], 1);
+        wait_count_bounded(&ctr[1], n_split, abort, hdr);
+    }
+    __syncthreads();
+    if (!*abort) {
+        for (int m = split + warp * n_split; m < R; m += (kThreads / 32) * n_split)
+            combine_row(a, masks, (node0 + m / G) * a.n_heads_q + g * G + m % G, g, gz, n_gz,
+                        n_split, nq, n_tiles_all, sy);
+    }
+    __syncthreads();
+    if (threadIdx.x == 0 && atomicAdd(&ctr[2], 1) == n_split - 1) {
+        atomicExch(&ctr[0], 0);
+        atomicExch(&ctr[1], 0);
+        atomicExch(&ctr[2], 0);
+    }
+}
+
+struct T128Plan {
+    int n_split, node_groups, nodes_per_group;
+    size_t part, flags, owner, total;
+};
+
+T128Plan q8_plan(int n_heads_q, int n_heads_kv, int n_q8, int n_tail, int n_tree, int num_sms)
+{
+    T128Plan p;
+    const int G = n_heads_q / n_heads_kv, rows = G * n_tree;
+    p.node_groups = rows <= kMaxRows ? 1 : (rows + kBlockM - 1) / kBlockM;
+    p.nodes_per_group = (n_tree + p.node_groups - 1) / p.node_groups;
+    // whole nodes per CTA: a group's rows must fit one block
+    if (p.node_groups > 1 && p.nodes_per_group * G > kBlockM)
+        p.nodes_per_group = kBlockM / G;
+    p.node_groups = (n_tree + p.nodes_per_group - 1) / p.nodes_per_group;
+    const int n_tiles = (n_q8 + kTileN - 1) / kTileN + (n_tail + n_tree + kTileN - 1) / kTileN;
+    int want = num_sms / (n_heads_kv * p.node_groups);
+    want = want < 1 ? 1 : want;
+    want = want > n_tiles ? n_tiles : want;
+    p.n_split = want > 255 ? 255 : want;
+    const size_t n_gz = (size_t)n_heads_kv * p.node_groups;
+    p.part = kHeaderBytes + kQ8SyncBytes;
+    p.flags = p.part + align_up((size_t)p.n_split * n_tree * n_heads_q * (kD + 2) * sizeof(float), 256);
+    p.owner = p.flags + align_up((size_t)p.n_split * n_gz * sizeof(int32_t), 256);
+    p.total = p.owner + align_up(n_gz * n_tiles, 256);
+    return p;
+}
+
+bool encode_codes_map(CUtensorMap *m, const void *ptr, int rows, int64_t cap, int n_heads_kv,
+                      bool swizzled)
+{
+    auto enc = tensor_map_encoder();
+    if (!enc)
+        return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)kD, (cuuint64_t)rows, (cuuint64_t)n_heads_kv};
+    const cuuint64_t strides[2] = {(cuuint64_t)kD, (cuuint64_t)cap * kD};
+    const cuuint32_t box[3] = {kD, kTileN, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(ptr), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE,
+               swizzled ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+bool attn_q8_t128_eligible(int n_heads_q, int n_heads_kv, int head_dim, int n_q8, int n_tail,
+                           int n_tree, int num_sms)
+{
+    // a CTA takes whole tree nodes: one node's G rows must fit one block;
+    // one CTA per SM, all resident
+    if (head_dim != kD || n_heads_q / n_heads_kv > kBlockM)
+        return false;
+    const T128Plan p = q8_plan(n_heads_q, n_heads_kv, n_q8, n_tail, n_tree, num_sms);
+    const long long gz = (long long)n_heads_kv * p.node_groups;
+    return gz <= kMaxGz && gz * p.n_split <= num_sms;
+}
+
+size_t attn_q8_t128_workspace_bytes(int n_heads_q, int n_heads_kv, int n_q8, int n_tail, int n_tree,
+                                    int num_sms)
+{
+    return q8_plan(n_heads_q, n_heads_kv, n_q8, n_tail, n_tree, num_sms).total;
+}
+
+cudaError_t attn_q8_t128_launch(const AttnQ8Args &a, const TreeMasks &masks, int num_sms,
+                                cudaStream_t stream)
+{
+    const T128Plan p = q8_plan(a.n_heads_q, a.n_heads_kv, a.c.n_q8, a.c.n_tail, a.n_tree, num_sms);
+    CUtensorMap mk = {}, mv = {};
+    if (a.c.n_q8 > 0 &&
+        (!encode_codes_map(&mk, a.c.k8, a.c.n_q8, a.c.q8_cap, a.n_heads_kv, true) ||
+         !encode_codes_map(&mv, a.c.v8, a.c.n_q8, a.c.q8_cap, a.n_heads_kv, false)))
+        return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(attn_q8_t128_kernel,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemLimit);
+    if (e != cudaSuccess)
+        return e;
+    // the softmax warps' larger share comes out of the launch's registers: a
+    // build that gave the kernel fewer would wait for them for good
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, attn_q8_t128_kernel);
+    if (e != cudaSuccess)
+        return e;
+    if (fa.numRegs < kRegsLaunch)
+        return cudaErrorInvalidConfiguration;
+    char *ws = reinterpret_cast<char *>(a.workspace);
+    Q8Sync sy;
+    sy.sync = reinterpret_cast<int32_t *>(ws + kHeaderBytes);
+    sy.part = reinterpret_cast<float *>(ws + p.part);
+    sy.flags = reinterpret_cast<int32_t *>(ws + p.flags);
+    sy.owner = reinterpret_cast<uint8_t *>(ws + p.owner);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.n_split, a.n_heads_kv, p.node_groups);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemLimit;   // each group lays out its own rows' share
+    cfg.stream = stream;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeCooperative;
+    at[0].val.cooperative = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    e = cudaLaunchKernelEx(&cfg, attn_q8_t128_kernel, mk, mv, a, masks, p.n_split, p.nodes_per_group,
+                           sy);
+    if (e == cudaSuccess)
+        e = cudaGetLastError();
+    if (e == cudaSuccess)
+        count_launches(1);
+    return e;
+}
+
+}  // namespace ts
