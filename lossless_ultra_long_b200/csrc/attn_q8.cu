@@ -502,7 +502,10 @@ size_t attn_q8_workspace_bytes(int n_heads_q, int n_heads_kv, int head_dim, int 
 cudaError_t attn_q8_launch(const AttnQ8Args &a, const TreeMasks &masks, int num_sms,
                            cudaStream_t stream)
 {
-    if (a.scale_log2 > 0.f && attn_q8_t128_eligible(a.n_heads_q, a.n_heads_kv, a.head_dim, a.c.n_q8,
+    // the tcgen05 kernel needs scores that grow with the products, and leaves
+    // root scores for groups of up to 8 heads
+    if (a.scale_log2 > 0.f && (!a.root_scores || a.n_heads_q / a.n_heads_kv <= 8) &&
+        attn_q8_t128_eligible(a.n_heads_q, a.n_heads_kv, a.head_dim, a.c.n_q8,
                                                     a.c.n_tail, a.n_tree, num_sms))
         return attn_q8_t128_launch(a, masks, num_sms, stream);
     const SplitPlan p = make_plan(a.n_heads_q, a.n_heads_kv, a.c.n_q8, a.c.n_tail, a.n_tree, num_sms);

@@ -76,10 +76,8 @@ constexpr int kBarQuery = 1;                 // named barrier: query rows in pla
 constexpr int kBarOut = 2;                   // named barrier: O^T staged in shared memory
 constexpr int kTileRing = 16;                // entries of the tile rings (> any role's lead)
 constexpr int kConvWarps = 4;
-// registers per thread: the launch gives 640 * 96; the softmax warpgroups
-// take 128 each, the two others 48: 3 * 128 * 128 + 2 * 128 * 48 = 640 * 96
-constexpr int kRegsLaunch = 96, kRegsSoftmax = 128, kRegsOther = 48;
-static_assert(3 * 128 * kRegsSoftmax + 2 * 128 * kRegsOther <= kThreads * kRegsLaunch, "registers");
+constexpr int kBarQLoads = 3;                // named barrier: the query rows are read
+constexpr int kQLoadThreads = 32 * 9;        // warps 4-11 arrive, the producer warp waits
 constexpr int kMaxGz = 256;                  // (KV head, node group) pairs: counters in the workspace
 static_assert(kMaxGz * 16 <= (int)kQ8SyncBytes, "counters fit their region");
 
@@ -180,28 +178,32 @@ __device__ __forceinline__ void mma8_ts(uint32_t d, uint32_t a_tmem, uint64_t b,
         : "memory");
 }
 
-template <int N>
-__device__ __forceinline__ void regs_inc()
-{
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_dec()
-{
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
-}
-
-// 16 TMEM lanes x 32 columns, the layout of tmem_ld16x256_x16; waits.
-__device__ __forceinline__ void tmem_ld16x256_x4(uint32_t taddr, uint32_t (&r)[16])
+// 16 TMEM lanes x 64 columns, the layout of tmem_ld16x256_x16; waits.
+__device__ __forceinline__ void tmem_ld16x256_x8(uint32_t taddr, uint32_t (&r)[32])
 {
     asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
         "tcgen05.wait::ld.sync.aligned;\n"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
           "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-          "=r"(r[14]), "=r"(r[15])
+          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(taddr)
+        : "memory");
+}
+
+// 16 consecutive 32-bit TMEM columns of this thread's lane; not waited.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+        "r"(r[15])
         : "memory");
 }
 
@@ -263,110 +265,67 @@ __device__ __forceinline__ uint2 codes_to_bf16(uint32_t w)
     return make_uint2(*reinterpret_cast<const uint32_t *>(&x), *reinterpret_cast<const uint32_t *>(&y));
 }
 
-// The tile's 128 positions that a row sees, as two words: the first d, then
-// the bits of anc (its root path).
-struct Vis {
-    unsigned long long w[2];
-};
-__device__ __forceinline__ Vis row_vis(unsigned long long anc, int d)
+// A half tile's 64 positions that a row sees: the first d, then the bits of
+// anc (its root path).
+__device__ __forceinline__ unsigned long long row_vis(unsigned long long anc, int d)
 {
-    Vis v;
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-        const int n = min(max(d - 64 * w, 0), 64);
-        unsigned long long m = n == 64 ? ~0ull : ((1ull << n) - 1ull);
-        const int sft = 64 * w - d;   // tree bit of the word's bit 0
-        if (sft >= 0)
-            m |= sft < 64 ? anc >> sft : 0ull;
-        else if (-sft < 64)
-            m |= anc << (-sft);
-        v.w[w] = m;
-    }
-    return v;
+    if (d >= 64)
+        return ~0ull;
+    return d > 0 ? ((1ull << d) - 1ull) | (anc << d) : (d > -64 ? anc >> -d : 0ull);
 }
 
-// bits 8 j + c0 + e (e = 0, 1) of the words -> bit 2 j + e
-__device__ __forceinline__ uint32_t thread_vis(const Vis &v, int c0)
+// bits 8 j + c0 + e (e = 0, 1) -> bit 2 j + e
+__device__ __forceinline__ uint32_t thread_vis(unsigned long long w, int c0)
 {
-    uint32_t vis = 0u;
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-        unsigned long long x = (v.w[w] >> c0) & 0x0303030303030303ull;
-        x = (x | (x >> 6)) & 0x000F000F000F000Full;
-        x = (x | (x >> 12)) & 0x000000FF000000FFull;
-        x = (x | (x >> 24)) & 0xFFFFull;
-        vis |= (uint32_t)x << (16 * w);
-    }
-    return vis;
+    unsigned long long x = (w >> c0) & 0x0303030303030303ull;
+    x = (x | (x >> 6)) & 0x000F000F000F000Full;
+    x = (x | (x >> 12)) & 0x000000FF000000FFull;
+    return (uint32_t)(x | (x >> 24)) & 0xFFFFu;
 }
 
-// One 64-position block (half H of the tile) of a thread's rows A and, when
-// TWO, B: weights 2^(x * c + n) packed to bf16 pairs; returns the pair sums.
-template <bool TWO, int H>
-__device__ __forceinline__ void exp_half(const uint32_t (&r)[64], float cA, float nA, float cB,
-                                         float nB, uint32_t (&pA)[16], uint32_t (&pB)[16],
-                                         float &sumA, float &sumB)
+// Weights 2^(x * c + n) of the 16 scores a thread holds of row E / 2 (E = 0:
+// row A, E = 2: row B) of a half tile, packed to bf16 pairs; returns their sum.
+template <int E>
+__device__ __forceinline__ float exp_row(const uint32_t (&r)[32], float c, float n, uint32_t (&p)[8])
 {
-    const uint64_t cA2 = pack2(cA, cA), nA2 = pack2(nA, nA);
-    const uint64_t cB2 = pack2(cB, cB), nB2 = pack2(nB, nB);
-    uint64_t sA = 0ull, sB = 0ull;
+    const uint64_t c2 = pack2(c, c), n2 = pack2(n, n);
+    uint64_t sum = 0ull;
 #pragma unroll
-    for (int j = 8 * H; j < 8 * H + 8; ++j) {
-#pragma unroll
-        for (int h = 0; h < (TWO ? 2 : 1); ++h) {
-            const uint64_t y = fma2(pack2(__uint_as_float(r[4 * j + 2 * h]),
-                                          __uint_as_float(r[4 * j + 2 * h + 1])),
-                                    h ? cB2 : cA2, h ? nB2 : nA2);
-            float y0, y1;
-            unpack2(y, y0, y1);
-            const float x0 = ex2(y0), x1 = ex2(y1);
-            const __nv_bfloat162 hv = __floats2bfloat162_rn(x0, x1);
-            const uint32_t hb = *reinterpret_cast<const uint32_t *>(&hv);
-            if (h) {
-                pB[j] = hb;
-                sB = add2(sB, pack2(x0, x1));
-            } else {
-                pA[j] = hb;
-                sA = add2(sA, pack2(x0, x1));
-            }
-        }
+    for (int j = 0; j < 8; ++j) {
+        const uint64_t y = fma2(pack2(__uint_as_float(r[4 * j + E]), __uint_as_float(r[4 * j + E + 1])),
+                                c2, n2);
+        float y0, y1;
+        unpack2(y, y0, y1);
+        const float x0 = ex2(y0), x1 = ex2(y1);
+        const __nv_bfloat162 hv = __floats2bfloat162_rn(x0, x1);
+        p[j] = *reinterpret_cast<const uint32_t *>(&hv);
+        sum = add2(sum, pack2(x0, x1));
     }
     float a0, a1;
-    unpack2(sA, a0, a1);
-    sumA = a0 + a1;
-    unpack2(sB, a0, a1);
-    sumB = a0 + a1;
+    unpack2(sum, a0, a1);
+    return a0 + a1;
 }
 
-// Maximum of the 16 scores of half H that a thread holds of row A (E = 0) or B (E = 2).
-template <int H, int E>
-__device__ __forceinline__ float half_max(const uint32_t (&r)[64])
+// Maximum of the 16 scores that a thread holds of row A (E = 0) or B (E = 2).
+template <int E>
+__device__ __forceinline__ float half_max(const uint32_t (&r)[32])
 {
     float m = -INFINITY;
 #pragma unroll
-    for (int j = 8 * H; j < 8 * H + 8; ++j)
+    for (int j = 0; j < 8; ++j)
         m = max3f(m, __uint_as_float(r[4 * j + E]), __uint_as_float(r[4 * j + E + 1]));
     return m;
 }
 
-// Eight rows' P (rows nbase + 0..7, of which the first n_valid are query
-// rows) into the K-major, 128-byte-swizzled P^T tile; other rows go to the
-// scratch kilobyte.
-__device__ __forceinline__ void store_p_half(uint32_t p_addr, uint32_t scratch, int nbase,
-                                             int n_valid, int r_pad, int lane,
-                                             const uint32_t (&pk)[16])
+// Eight rows' P of one half tile (64 positions: a 128-byte row of the K-major,
+// 128-byte-swizzled P^T tile): `row` is this lane's row address, rx its row
+// index mod 8.
+__device__ __forceinline__ void store_p(uint32_t row, int rx, int lane, const uint32_t (&pk)[8])
 {
-    const int r = lane & 7, n = nbase + r;
-    const bool valid = r < n_valid;
-    const uint32_t row = p_addr + (uint32_t)((n >> 3) * 1024 + (n & 7) * 128);
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
-        const int j = 4 * m + (lane >> 3);
-        const uint32_t addr = valid ? row + (uint32_t)((j >> 3) * (r_pad * 128) +
-                                                       (((j & 7) ^ (n & 7)) << 4))
-                                    : scratch + (uint32_t)(lane << 4);
-        stmatrix_x4(addr, pk[4 * m], pk[4 * m + 1], pk[4 * m + 2], pk[4 * m + 3]);
-    }
+    for (int m = 0; m < 2; ++m)
+        stmatrix_x4(row + (uint32_t)(((4 * m + (lane >> 3)) ^ rx) << 4), pk[4 * m], pk[4 * m + 1],
+                    pk[4 * m + 2], pk[4 * m + 3]);
 }
 
 // The kernel's workspace, after the header and the counters.
@@ -590,16 +549,13 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
     const int R = G * T;
     const int NB = R > kBlockM ? 2 : 1;
     const int R0 = R < kBlockM ? R : kBlockM, R1 = R - R0;
-    const int rq0 = (R0 + 3) / 4, rq1 = (R1 + 3) / 4;  // rows per lane quarter
+    // rows per lane quarter: a quarter of the block's, but at least 8 while
+    // that needs no more warps (a warp takes 8 rows as fast as one), so that
+    // the root node's rows 0..G-1, G <= 8, are the last block's first lanes
+    const int rq0 = max((R0 + 3) / 4, min(R0, 8)), rq1 = max((R1 + 3) / 4, min(R1, 8));
     const int u0 = (rq0 + 15) / 16, u1 = (rq1 + 15) / 16;
     const int U = u0 + u1;  // softmax warps per lane quarter (at most 3)
-    // the root node's rows 0..G-1 sit in the last block's first lanes; with
-    // more than 16 lanes of them, or split over quarters, softmax rows store
-    // the scores themselves (rs_rows)
-    const int rqL = NB == 2 ? rq1 : rq0;
-    const bool want_rs = a.root_scores != nullptr && node0 == 0;
-    const bool rs_warp0 = want_rs && G <= 8 && G <= rqL;
-    const bool rs_rows = want_rs && !rs_warp0;
+    const bool rs_warp0 = a.root_scores != nullptr && node0 == 0;
     const Layout lay = q8_layout(R);
     const int SK = lay.stages_k, SV = lay.stages_v, SVB = lay.stages_vb, r_pad = lay.r_pad;
 
@@ -671,7 +627,6 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
     };
 
     if (warp < 4) {
-        regs_dec<kRegsOther>();
         if (warp == 0)
             for (int i = lane; i < a.n_tree; i += 32)
                 aux->anc[i] = masks.anc[i];
@@ -682,6 +637,8 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
         }
         if (warp == 3) {
             // ------------------------------------------------ TMA producer
+            // (the query rows first: not behind every CTA's first ring of tiles)
+            named_bar_sync(kBarQLoads, kQLoadThreads);
             if (lane == 0) {
                 auto tile_at = [&](int k) { return n_tiles_all - 1 - k; };
                 int32_t *ctr = sy.sync + 4 * gz;
@@ -801,32 +758,34 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     const int r0 = (q8 ? tile : tile - nq) * kTileN;
                     const int left = (q8 ? kc.n_q8 : kc.n_tail) - r0;   // context positions here
                     const int pos0 = q8 ? r0 : kc.n_q8 + r0;
-#pragma unroll
-                    for (int qd = 0; qd < 4; ++qd) {
-                        if (32 * qd >= left)
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) {
+                        const int lh = left - 64 * h;
+                        if (lh <= 0)
                             break;   // uniform: nothing of the context from here on
-                        uint32_t rr[16];
-                        tmem_ld16x256_x4(tmem + kSCol + 128 * slot + 32 * qd, rr);
+                        uint32_t rr[32];
+                        tmem_ld16x256_x8(tmem + kSCol + 128 * slot + 64 * h, rr);
                         if (mine) {
-                            const float f = rsc * q8_factor((sc >> (qd < 2 ? 0 : 8)) & 0xFFu);
+                            const float f = rsc * q8_factor((sc >> (8 * h)) & 0xFFu);
+                            float *dst = dst_row + pos0 + 64 * h + c0;
+                            unsigned long long nan = 0ull;
+                            if (!q8)
+                                nan = bar->bad_k[t & 3][2 * h] |
+                                      ((unsigned long long)bar->bad_k[t & 3][2 * h + 1] << 32);
+                            if (vec && lh >= 64 && nan == 0ull) {
 #pragma unroll
-                            for (int jj = 0; jj < 4; ++jj) {
-                                const int p = 32 * qd + 8 * jj + c0;
-                                float x0 = __uint_as_float(rr[4 * jj]) * f;
-                                float x1 = __uint_as_float(rr[4 * jj + 1]) * f;
-                                if (!q8) {
-                                    const uint32_t bk = bar->bad_k[t & 3][qd] >> (8 * jj + c0);
-                                    x0 = bk & 1u ? __uint_as_float(0x7FC00000u) : x0;
-                                    x1 = bk & 2u ? __uint_as_float(0x7FC00000u) : x1;
-                                }
-                                float *dst = dst_row + pos0 + p;
-                                if (vec && p + 1 < left) {
-                                    *reinterpret_cast<float2 *>(dst) = make_float2(x0, x1);
-                                } else {
-                                    if (p < left)
-                                        dst[0] = x0;
-                                    if (p + 1 < left)
-                                        dst[1] = x1;
+                                for (int j = 0; j < 8; ++j)
+                                    *reinterpret_cast<float2 *>(dst + 8 * j) =
+                                        make_float2(__uint_as_float(rr[4 * j]) * f,
+                                                    __uint_as_float(rr[4 * j + 1]) * f);
+                            } else {
+#pragma unroll
+                                for (int k = 0; k < 16; ++k) {
+                                    const int p = 8 * (k >> 1) + c0 + (k & 1);
+                                    if (p < lh)
+                                        dst[8 * (k >> 1) + (k & 1)] =
+                                            (nan >> p) & 1ull ? __uint_as_float(0x7FC00000u)
+                                                              : __uint_as_float(rr[4 * (k >> 1) + (k & 1)]) * f;
                                 }
                             }
                         }
@@ -840,8 +799,6 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
             }
         } else if (lane == 0 && warp == 1) {
             // ------------------------------------------------ QK issuer
-            constexpr uint32_t id[4] = {idesc_f8(kBlockM, kTileN, 0, 0), idesc_f8(kBlockM, kTileN, 1, 0),
-                                        idesc_f8(kBlockM, kTileN, 0, 1), idesc_f8(kBlockM, kTileN, 1, 1)};
             const uint64_t kd0 = sdesc_sw128(smem_addr(sK), 16, 1024);
             const uint64_t qd0 = sdesc_sw128(smem_addr(sQ1), 16, 1024);
             int ke = 0;
@@ -866,20 +823,24 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     }
                     tc_fence_after();
                     const uint32_t d = tmem + kSCol + 128 * slot;
-                    for (int part = 0; part < parts; ++part) {
+                    // parts: K's codes (hi, lo on a tail tile), each times Q's hi
+                    // and lo
+#pragma unroll 1
+                    for (int i = 0; i < 2 * parts; ++i) {
+                        const int lo = i & 1, part = i >> 1;
                         const uint64_t kd = kd0 + (uint64_t)((ke + part) % SK) * (kRawBytes >> 4);
+                        const uint32_t idesc = idesc_f8(kBlockM, kTileN, 0, 0) | ((uint32_t)lo << 7) |
+                                               ((uint32_t)part << 10);
+                        if (b == 0) {
 #pragma unroll
-                        for (int lo = 0; lo < 2; ++lo)
+                            for (int kk = 0; kk < 4; ++kk)
+                                mma8_ts(d, tmem + kQCol + 32 * lo + 8 * kk, kd + 2 * kk, idesc, i + kk > 0);
+                        } else {
+                            const uint64_t qd = qd0 + lo * ((kBlockM * kD) >> 4);
 #pragma unroll
-                            for (int kk = 0; kk < 4; ++kk) {
-                                const bool acc = part + lo + kk > 0;
-                                const uint32_t idesc = part ? id[2 + lo] : id[lo];
-                                if (b == 0)
-                                    mma8_ts(d, tmem + kQCol + 32 * lo + 8 * kk, kd + 2 * kk, idesc, acc);
-                                else
-                                    mma8_ss(d, qd0 + lo * ((kBlockM * kD) >> 4) + 2 * kk, kd + 2 * kk,
-                                            idesc, acc);
-                            }
+                            for (int kk = 0; kk < 4; ++kk)
+                                mma8_ss(d, qd + 2 * kk, kd + 2 * kk, idesc, i + kk > 0);
+                        }
                     }
                     mma_commit(smem_addr(&bar->s_full[slot]));
                 }
@@ -923,11 +884,8 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
             mma_commit(smem_addr(&bar->drain[1]));
             wait_drain(smem_addr(&bar->drain[1]), 0);
         }
-        __syncwarp();
-        regs_inc<kRegsLaunch>();
     } else if (warp >= 16) {
         // ------------------------------------------------ converters
-        regs_dec<kRegsOther>();
         const int tid = threadIdx.x - 512;   // 0..127
         int met = 0;                         // meetings of the converter warps so far
         for (int t = 0;; ++t) {
@@ -1024,7 +982,7 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 // bytes; halves 0 and 1 of V's columns write their two chunks in
                 // opposite order, so that eight lanes' stores hit eight banks
                 const unsigned char *raw = sV + s * kRawBytes;
-#pragma unroll
+#pragma unroll 2
                 for (int i = 0; i < kRawBytes / (16 * 32 * kConvWarps); ++i) {
                     const int u = tid + i * 32 * kConvWarps;   // 16-byte unit of the tile
                     const int p = u >> 3, c16 = u & 7;
@@ -1054,10 +1012,7 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 mbar_arrive(smem_addr(&bar->empty_v[s]));
             }
         }
-        __syncwarp();
-        regs_inc<kRegsLaunch>();
     } else {
-        regs_inc<kRegsSoftmax>();
         // ---- query rows of this KV head: row n = node * G + (head - g*G),
         // block 0 into TMEM lanes (warps 4-7), block 1 into the shared-memory
         // A tile (warps 8-11), each split into hi and lo codes
@@ -1066,47 +1021,53 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
             const int rqb = b ? rq1 : rq0, Rb = b ? R1 : R0;
             const int n = kBlockM * b + q * rqb + lane;
             const bool valid = lane < rqb && q * rqb + lane < Rb;
-            uint32_t hi[32], lo[32];
-            uint32_t top = 0;
-            uint4 u[16];
             const uint4 *src = valid ? q_row(q8_row_of(n, R)) : nullptr;
+            uint32_t top = 0;
 #pragma unroll
-            for (int c = 0; c < 16; ++c) {
-                u[c] = valid ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-                top = __vmaxu2(top, top_word(u[c]));
-            }
+            for (int c = 0; c < 16; ++c)
+                top = __vmaxu2(top, valid ? top_word(__ldg(src + c)) : 0u);
+            named_bar_arrive(kBarQLoads, kQLoadThreads);
             top = top_of(top);
             const bool bad = top >= 0x7F80u;
             const int e = bad ? 0 : split_exp(top);
             const float f = two_to(-e);
-#pragma unroll
-            for (int c = 0; c < 16; ++c) {
-                uint2 h, l;
-                split_16b(u[c], f, h, l);
-                hi[2 * c] = h.x;
-                hi[2 * c + 1] = h.y;
-                lo[2 * c] = l.x;
-                lo[2 * c + 1] = l.y;
-            }
             if (valid)
                 aux->row_scale[n] = bad ? __uint_as_float(0x7FC00000u) : a.scale_log2 * two_to(e);
-            if (b == 0) {
-                const uint32_t qa = tmem + ((uint32_t)(q * 32) << 16) + kQCol;
-                tmem_st32(qa, hi);
-                tmem_st32(qa + 32, lo);
-                tmem_st_wait();
-            } else {
-                const int m = q * 32 + lane;   // A-tile row = TMEM lane of S_1
+            const int m = q * 32 + lane;   // A-tile row = TMEM lane of S
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {   // 64 dims at a time
+                uint32_t hi[16], lo[16];
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
-                    const int off = m * 128 + ((c ^ (m & 7)) << 4);
-                    *reinterpret_cast<uint4 *>(sQ1 + off) =
-                        make_uint4(hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
-                    *reinterpret_cast<uint4 *>(sQ1 + kBlockM * kD + off) =
-                        make_uint4(lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
+                    uint2 x, y;
+                    split_16b(valid ? __ldg(src + 8 * h + c) : make_uint4(0u, 0u, 0u, 0u), f, x, y);
+                    hi[2 * c] = x.x;
+                    hi[2 * c + 1] = x.y;
+                    lo[2 * c] = y.x;
+                    lo[2 * c + 1] = y.y;
                 }
-                fence_proxy_async_smem();
+                if (b == 0) {
+                    const uint32_t qa = tmem + ((uint32_t)(q * 32) << 16) + kQCol + 16 * h;
+                    __syncwarp();
+                    tmem_st16(qa, hi);
+                    tmem_st16(qa + 32, lo);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const int off = m * 128 + (((4 * h + c) ^ (m & 7)) << 4);
+                        *reinterpret_cast<uint4 *>(sQ1 + off) =
+                            make_uint4(hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
+                        *reinterpret_cast<uint4 *>(sQ1 + kBlockM * kD + off) =
+                            make_uint4(lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
+                    }
+                }
             }
+            if (b == 0)
+                tmem_st_wait();
+            else
+                fence_proxy_async_smem();
+        } else if (warp < 12) {
+            named_bar_arrive(kBarQLoads, kQLoadThreads);   // one block: no rows to load
         }
         tc_fence_before();
         named_bar_sync(kBarQuery, kThreads - 32 * (1 + kConvWarps));
@@ -1127,9 +1088,19 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
             const int nbase = kBlockM * b + q * rqb + lb;
             const int nvA = max(0, min(8, min(rqb - lb, Rb - q * rqb - lb)));
             const int nvB = max(0, min(8, min(rqb - lb - 8, Rb - q * rqb - lb - 8)));
+            // this lane's P^T rows of the unit's halves A and B (stmatrix: lane
+            // l gives the address of row l % 8); rows that are none go to the
+            // scratch kilobyte
             const uint32_t p_addr = smem_addr(sP);
             const uint32_t p_scratch = p_addr + (uint32_t)r_pad * 512;
+            const int rl = lane & 7, pnA = nbase + rl, pnB = pnA + 8;
+            const bool okA = rl < nvA, okB = rl < nvB;
+            const uint32_t p_rowA = okA ? p_addr + (uint32_t)((pnA >> 3) * 1024 + (pnA & 7) * 128) : p_scratch;
+            const uint32_t p_rowB = okB ? p_addr + (uint32_t)((pnB >> 3) * 1024 + (pnB & 7) * 128) : p_scratch;
+            const uint32_t p_half = (uint32_t)r_pad * 128;
             const float rsA = vA ? aux->row_scale[nA] : 1.f, rsB = vB ? aux->row_scale[nB] : 1.f;
+            const unsigned long long ancA = aux->anc[node0 + (vA ? q8_row_of(nA, R) / G : 0)];
+            const unsigned long long ancB = aux->anc[node0 + (vB ? q8_row_of(nB, R) / G : 0)];
             float mA = -INFINITY, mB = -INFINITY, lA = 0.f, lB = 0.f;
             bool ok = true;
             for (int t = 0;; ++t) {
@@ -1141,117 +1112,84 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 const int tile = bar->tile_of[t % kTileRing];
                 if (tile < 0)
                     break;
-                const uint32_t sc = bar->scale_of[t % kTileRing];
-                tc_fence_after();
-                uint32_t r[64];
-                tmem_ld16x256_x16(s_addr + 128 * slot, r);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(smem_addr(&bar->s_free[slot]));
-                // factors of the tile's two blocks: scores (never zero: a
-                // masked score is -inf), and the exponent V's scale adds
-                const float k0 = q8_factor(sc & 0xFFu), k1 = q8_factor((sc >> 8) & 0xFFu);
-                constexpr float kTiny = 1.17549435e-38f;
-                const float cA0 = rsA * k0 < kTiny ? kTiny : rsA * k0;
-                const float cA1 = rsA * k1 < kTiny ? kTiny : rsA * k1;
-                const float cB0 = rsB * k0 < kTiny ? kTiny : rsB * k0;
-                const float cB1 = rsB * k1 < kTiny ? kTiny : rsB * k1;
+                uint32_t sc = bar->scale_of[t % kTileRing];
                 const bool tail = tile >= nq;
-                const int r0 = (tail ? tile - nq : tile) * kTileN;
-                const int left = (tail ? kc.n_tail : kc.n_q8) - r0;   // context positions here
-                if (left < kTileN) {
-                    const unsigned long long ancA = tail ? aux->anc[node0 + (vA ? q8_row_of(nA, R) / G : 0)] : 0ull;
-                    const unsigned long long ancB = tail ? aux->anc[node0 + (vB ? q8_row_of(nB, R) / G : 0)] : 0ull;
-                    const Vis wA = row_vis(ancA, left), wB = row_vis(ancB, left);
-                    const uint32_t visA = thread_vis(wA, c0), visB = thread_vis(wB, c0);
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        if (!((visA >> k) & 1u))
-                            r[4 * (k >> 1) + (k & 1)] = __float_as_uint(-INFINITY);
-                        if (!((visB >> k) & 1u))
-                            r[4 * (k >> 1) + 2 + (k & 1)] = __float_as_uint(-INFINITY);
+                // context positions from the half tile's first on
+                int left = tail ? kc.n_tail - (tile - nq) * kTileN : kc.n_q8 - tile * kTileN;
+                // the halves are the tile's two scale blocks; one copy of the code
+                // serves both (the loop must stay inside the instruction cache)
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h, left -= 64, sc >>= 8) {
+                    tc_fence_after();
+                    uint32_t r[32];
+                    tmem_ld16x256_x8(s_addr + 128 * slot + 64 * h, r);
+                    if (h == 1) {
+                        // S is in registers: QK of a later tile may overwrite it
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(smem_addr(&bar->s_free[slot]));
                     }
-                }
-                if (tail) {
-                    const uint32_t *bw = bar->bad[t & 3];
-                    const unsigned long long b0 = bw[0] | ((unsigned long long)bw[1] << 32);
-                    const unsigned long long b1 = bw[2] | ((unsigned long long)bw[3] << 32);
-                    if (b0 | b1) {
-                        const Vis wA = row_vis(aux->anc[node0 + (vA ? q8_row_of(nA, R) / G : 0)], left);
-                        const Vis wB = row_vis(aux->anc[node0 + (vB ? q8_row_of(nB, R) / G : 0)], left);
-                        if ((wA.w[0] & b0) | (wA.w[1] & b1))
-                            lA = __uint_as_float(0x7FC00000u);
-                        if ((wB.w[0] & b0) | (wB.w[1] & b1))
-                            lB = __uint_as_float(0x7FC00000u);
-                    }
-                }
-                if (rs_rows) {
-                    // the root node's rows store their own scores
-                    const int pos0 = tail ? kc.n_q8 + r0 : r0;
+                    // factor of the scores: never zero, as a masked score is -inf
+                    const float kf = q8_factor(sc & 0xFFu);
+                    constexpr float kTiny = 1.17549435e-38f;
+                    const float cA = rsA * kf < kTiny ? kTiny : rsA * kf;
+                    const float cB = rsB * kf < kTiny ? kTiny : rsB * kf;
+                    if (left < 64) {
+                        const unsigned long long wA = row_vis(tail ? ancA : 0ull, left);
+                        const unsigned long long wB = row_vis(tail ? ancB : 0ull, left);
+                        const uint32_t visA = thread_vis(wA, c0), visB = thread_vis(wB, c0);
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        const int p = 8 * (k >> 1) + c0 + (k & 1);
-                        const bool bk = tail && ((bar->bad_k[t & 3][p >> 5] >> (p & 31)) & 1u);
-                        if (p < left) {
-                            const int hA = q8_row_of(nA, R), hB = q8_row_of(nB, R);
-                            if (vA && hA < G)
-                                a.root_scores[(size_t)(g * G + hA) * n_ctx + pos0 + p] =
-                                    bk ? __uint_as_float(0x7FC00000u)
-                                       : __uint_as_float(r[4 * (k >> 1) + (k & 1)]) * (rsA * (k < 16 ? k0 : k1));
-                            if (vB && hB < G)
-                                a.root_scores[(size_t)(g * G + hB) * n_ctx + pos0 + p] =
-                                    bk ? __uint_as_float(0x7FC00000u)
-                                       : __uint_as_float(r[4 * (k >> 1) + 2 + (k & 1)]) * (rsB * (k < 16 ? k0 : k1));
+                        for (int k = 0; k < 16; ++k) {
+                            if (!((visA >> k) & 1u))
+                                r[4 * (k >> 1) + (k & 1)] = __float_as_uint(-INFINITY);
+                            if (!((visB >> k) & 1u))
+                                r[4 * (k >> 1) + 2 + (k & 1)] = __float_as_uint(-INFINITY);
                         }
                     }
-                }
-                // a row that has seen nothing yet takes this tile's max,
-                // rounded up to an integer, as its reference
-                if (__any_sync(0xffffffffu, mA == -INFINITY || mB == -INFINITY)) {
-                    float yA = fmaxf(half_max<0, 0>(r) * cA0, half_max<1, 0>(r) * cA1);
-                    float yB = fmaxf(half_max<0, 2>(r) * cB0, half_max<1, 2>(r) * cB1);
-                    yA = fmaxf(yA, __shfl_xor_sync(0xffffffffu, yA, 1));
-                    yB = fmaxf(yB, __shfl_xor_sync(0xffffffffu, yB, 1));
-                    yA = fmaxf(yA, __shfl_xor_sync(0xffffffffu, yA, 2));
-                    yB = fmaxf(yB, __shfl_xor_sync(0xffffffffu, yB, 2));
-                    if (mA == -INFINITY)
-                        mA = ceilf(yA);
-                    if (mB == -INFINITY)
-                        mB = ceilf(yB);
-                }
-                uint32_t pA[16], pB[16];
-                {
-                    const float v0 = q8_log2((sc >> 16) & 0xFFu), v1 = q8_log2(sc >> 24);
-                    const float i0 = q8_inverse((sc >> 16) & 0xFFu), i1 = q8_inverse(sc >> 24);
-                    const float nmA = mA == -INFINITY ? 0.f : -mA;
-                    const float nmB = mB == -INFINITY ? 0.f : -mB;
-                    float sA, sB;
-                    if (hasB) {
-                        exp_half<true, 0>(r, cA0, nmA + v0, cB0, nmB + v0, pA, pB, sA, sB);
-                        lA += sA * i0;
-                        lB += sB * i0;
-                        exp_half<true, 1>(r, cA1, nmA + v1, cB1, nmB + v1, pA, pB, sA, sB);
-                        lA += sA * i1;
-                        lB += sB * i1;
-                    } else if (hasA) {
-                        exp_half<false, 0>(r, cA0, nmA + v0, cB0, nmB + v0, pA, pB, sA, sB);
-                        lA += sA * i0;
-                        exp_half<false, 1>(r, cA1, nmA + v1, cB1, nmB + v1, pA, pB, sA, sB);
-                        lA += sA * i1;
+                    if (tail) {
+                        // a row that sees a value that is no number
+                        const unsigned long long bw =
+                            bar->bad[t & 3][2 * h] | ((unsigned long long)bar->bad[t & 3][2 * h + 1] << 32);
+                        if (row_vis(ancA, left) & bw)
+                            lA = __uint_as_float(0x7FC00000u);
+                        if (row_vis(ancB, left) & bw)
+                            lB = __uint_as_float(0x7FC00000u);
                     }
+                    // a row that has seen nothing yet takes this half's max,
+                    // rounded up to an integer, as its reference
+                    if (__any_sync(0xffffffffu, mA == -INFINITY || mB == -INFINITY)) {
+                        float yA = half_max<0>(r) * cA, yB = half_max<2>(r) * cB;
+                        yA = fmaxf(yA, __shfl_xor_sync(0xffffffffu, yA, 1));
+                        yB = fmaxf(yB, __shfl_xor_sync(0xffffffffu, yB, 1));
+                        yA = fmaxf(yA, __shfl_xor_sync(0xffffffffu, yA, 2));
+                        yB = fmaxf(yB, __shfl_xor_sync(0xffffffffu, yB, 2));
+                        if (mA == -INFINITY)
+                            mA = ceilf(yA);
+                        if (mB == -INFINITY)
+                            mB = ceilf(yB);
+                    }
+                    const uint32_t vbyte = (sc >> 16) & 0xFFu;
+                    const float ve = q8_log2(vbyte), vi = q8_inverse(vbyte);
+                    uint32_t pA[8], pB[8];
+                    if (hasA)
+                        lA += exp_row<0>(r, cA, (mA == -INFINITY ? 0.f : -mA) + ve, pA) * vi;
+                    if (hasB)
+                        lB += exp_row<2>(r, cB, (mB == -INFINITY ? 0.f : -mB) + ve, pB) * vi;
+                    // this P^T tile is free once PV(t - 2) is done
+                    if (h == 0 && t >= 2 &&
+                        !warp_wait_bounded(smem_addr(&bar->pv_done[t & 1]), ((t - 2) >> 1) & 1, abort, hdr)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t at = (uint32_t)(t & 1) * 2 * p_half + h * p_half;
+                    if (hasA)
+                        store_p(okA ? p_rowA + at : p_rowA, okA ? pnA & 7 : 0, lane, pA);
+                    if (hasB)
+                        store_p(okB ? p_rowB + at : p_rowB, okB ? pnB & 7 : 0, lane, pB);
                 }
-                // this P^T tile is free once PV(t - 2) is done
-                if (t >= 2 && !warp_wait_bounded(smem_addr(&bar->pv_done[t & 1]),
-                                                 ((t - 2) >> 1) & 1, abort, hdr)) {
-                    ok = false;
+                if (!ok)
                     break;
-                }
-                const uint32_t p_tile = p_addr + (uint32_t)(t & 1) * (uint32_t)r_pad * 256;
-                if (hasA)
-                    store_p_half(p_tile, p_scratch, nbase, nvA, r_pad, lane, pA);
-                if (hasB)
-                    store_p_half(p_tile, p_scratch, nbase + 8, nvB, r_pad, lane, pB);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0)
@@ -1309,8 +1247,6 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 fence_proxy_async_global();
             }
         }
-        __syncwarp();
-        regs_dec<kRegsLaunch>();
     }
 
     tc_fence_before();
@@ -1421,14 +1357,6 @@ cudaError_t attn_q8_t128_launch(const AttnQ8Args &a, const TreeMasks &masks, int
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemLimit);
     if (e != cudaSuccess)
         return e;
-    // the softmax warps' larger share comes out of the launch's registers: a
-    // build that gave the kernel fewer would wait for them for good
-    cudaFuncAttributes fa;
-    e = cudaFuncGetAttributes(&fa, attn_q8_t128_kernel);
-    if (e != cudaSuccess)
-        return e;
-    if (fa.numRegs < kRegsLaunch)
-        return cudaErrorInvalidConfiguration;
     char *ws = reinterpret_cast<char *>(a.workspace);
     Q8Sync sy;
     sy.sync = reinterpret_cast<int32_t *>(ws + kHeaderBytes);
