@@ -37,6 +37,10 @@
 //   warps 4-15  softmax                     warps 16-19  converters
 // P^T is double-buffered, and with one query block (R <= 128) S too, so a
 // tile's exponentials overlap the previous tile's PV and the next one's QK.
+// With at most 64 query rows one warpgroup is enough for a tile, but its chain
+// of waits and loads is longer than the tile's stream from HBM: the three
+// softmax warpgroups then take tiles in turn, each with its own reference,
+// O^T and P^T, and leave three partials per split.
 // TMEM: O^T in [0, 192), Q_0 (hi, lo) in [192, 256), S in [256, 512).
 //
 // Every wait is bounded (about a second): on expiry the kernel records
@@ -87,19 +91,17 @@ struct Bars {
     uint64_t full_v[kMaxStages];    // codes of V landed (or: a tail tile, or the end)
     uint64_t empty_v[kMaxStages];
     uint64_t vb_full[2];            // V in bf16 (or the end)
-    uint64_t s_full[2];             // QK landed in an S slot
-    uint64_t s_free[2];             // its readers hold it in registers
-    uint64_t sm_done[2];            // every softmax warp wrote its P^T rows
-    uint64_t pv_done[2];            // PV of a tile of that parity is complete
+    uint64_t s_full[3];             // QK landed: by block, or (one block) by tile in turn
+    uint64_t s_free[3];             // its readers hold S in registers
+    uint64_t sm_done[3];            // per P^T slot: every softmax warp wrote its rows
+    uint64_t pv_done[3];            // per P^T slot: PV is complete
     uint64_t o_final;
     uint64_t drain[2];
     uint64_t conv;                  // the converter warps meet (tail tiles)
-    // per tile, at [t % kTileRing]: its index (-1 after the last), its scale
-    // bytes (k of its two blocks, v of its two blocks), its first K ring
-    // entry.  Written by the producer (a tail tile's k bytes by a converter)
-    // before the arrival that the readers wait for.
+    // per tile, at [t % kTileRing]: its index (-1 after the last) and its
+    // first K ring entry.  Written by the producer before the arrival that
+    // the readers wait for.
     volatile int32_t tile_of[kTileRing];
-    volatile uint32_t scale_of[kTileRing];
     volatile int32_t entry_of[kTileRing];
     uint32_t bad[4][4];             // tail tile t % 4: rows with a value that is no number
     uint32_t bad_k[4][4];
@@ -111,13 +113,17 @@ struct Bars {
 
 struct Aux {
     Bars bar;
+    // per tile and half, written like tile_of (a tail tile's k by a converter):
+    // K's scale, V's as an exponent, V's inverse.  A block that is NaN, in K
+    // or V, has a NaN exponent and inverse: its weights and sums are NaN.
+    float4 scale_of[kTileRing][2];
     unsigned long long anc[TS_MAX_TREE];
     float row_scale[2 * kBlockM];   // softmax scale * log2 e * the query row's scale
 };
 constexpr size_t kAuxBytes = (sizeof(Aux) + 1023) / 1024 * 1024;
 
 struct Layout {
-    int r_pad, stages_k, stages_v, stages_vb;
+    int r_pad, p_slots, stages_k, stages_v, stages_vb;
     size_t q1_off, p_off, vb_off, k_off, v_off, aux_off, smem_bytes;
 };
 
@@ -126,14 +132,18 @@ __host__ __device__ inline int q8_row_of(int n, int R)
     return R > kBlockM ? (n < kBlockM ? (R - kBlockM) + n : n - kBlockM) : n;
 }
 
-__host__ __device__ inline Layout q8_layout(int rows)
+// Softmax warpgroups that take tiles in turn (one partial each per split).
+__host__ __device__ inline int q8_groups(int rows) { return rows <= 64 ? 3 : 1; }
+
+__host__ __device__ inline Layout q8_layout(int rows, int groups)
 {
     Layout L;
     L.r_pad = (rows + 15) / 16 * 16;
+    L.p_slots = groups == 3 ? 3 : 2;
     L.q1_off = 0;
     L.p_off = rows > kBlockM ? kQ1Bytes : 0;
-    // two P^T tiles, then 1 KB that rows past the query rows are written to
-    L.vb_off = L.p_off + (size_t)L.r_pad * 512 + 1024;
+    // the P^T tiles, then 1 KB that rows past the query rows are written to
+    L.vb_off = L.p_off + (size_t)L.r_pad * 256 * L.p_slots + 1024;
     L.stages_vb = rows > kBlockM ? 1 : 2;
     L.k_off = L.vb_off + (size_t)L.stages_vb * kVbBytes;
     const size_t fixed = 1024 + L.k_off + kAuxBytes;
@@ -162,6 +172,17 @@ __device__ __forceinline__ void mma8_ss(uint32_t d, uint64_t a, uint64_t b, uint
         " .reg .pred p;\n"
         " setp.ne.b32 p, %4, 0;\n"
         " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n"
+        "}\n" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc)
+{
+    asm volatile(
+        "{\n"
+        " .reg .pred p;\n"
+        " setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
         "}\n" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
         : "memory");
 }
@@ -332,7 +353,8 @@ __device__ __forceinline__ void store_p(uint32_t row, int rx, int lane, const ui
 struct Q8Sync {
     int32_t *sync;    // [Hkv * groups][4]: tile counter, arrivals, finished combines, unused;
                       // zero when a call starts, and again when it ends
-    float *part;      // acc fp32 [n_split][T*Hq][128], then (m, l) fp32 [n_split][T*Hq][2]
+    float *part;      // acc fp32 [n_split * groups][T*Hq][128], then (m, l) fp32
+                      // [n_split * groups][T*Hq][2]
     int32_t *flags;   // [n_split][Hkv * groups]: some row's sum outgrew its reference
     uint8_t *owner;   // [Hkv * groups][n_tiles]: the split that streamed each tile
 };
@@ -401,33 +423,35 @@ __device__ void tile_exact(const AttnQ8Args &a, unsigned long long anc, int g, c
     }
 }
 
-// One output row, by one warp: out = sum_s 2^(m_s - M) acc_s / sum_s
-// 2^(m_s - M) l_s over the splits, a flagged split recomputed exactly.
+// One output row, by one warp: out = sum 2^(m - M) acc / sum 2^(m - M) l over
+// the n_split * ng partials, a flagged split recomputed exactly.
 __device__ __forceinline__ void combine_row(const AttnQ8Args &a, const TreeMasks &masks, int row,
-                                            int g, int gz, int n_gz, int n_split, int nq,
+                                            int g, int gz, int n_gz, int n_split, int ng, int nq,
                                             int n_tiles_all, const Q8Sync &sy)
 {
     const int rows_all = a.n_tree * a.n_heads_q;
     const int lane = threadIdx.x & 31;
+    const int n_part = n_split * ng;
     const float *ws_o = sy.part;
-    const float2 *ws_ml = reinterpret_cast<const float2 *>(ws_o + (size_t)n_split * rows_all * kD);
-    auto ml_of = [&](int s) { return __ldcg(ws_ml + (size_t)s * rows_all + row); };
-    auto acc_of = [&](int s) {
-        return __ldcg(reinterpret_cast<const float4 *>(ws_o + ((size_t)s * rows_all + row) * kD) + lane);
+    const float2 *ws_ml = reinterpret_cast<const float2 *>(ws_o + (size_t)n_part * rows_all * kD);
+    auto ml_of = [&](int p) { return __ldcg(ws_ml + (size_t)p * rows_all + row); };
+    auto acc_of = [&](int p) {
+        return __ldcg(reinterpret_cast<const float4 *>(ws_o + ((size_t)p * rows_all + row) * kD) + lane);
     };
-    // the first kB splits' columns are in flight while M is formed
+    // the first kB partials' columns are in flight while M is formed
     constexpr int kB = 9;
     float4 x[kB];
 #pragma unroll
     for (int u = 0; u < kB; ++u)
-        x[u] = u < n_split ? acc_of(u) : make_float4(0.f, 0.f, 0.f, 0.f);
+        x[u] = u < n_part ? acc_of(u) : make_float4(0.f, 0.f, 0.f, 0.f);
     bool any = false;
     float M = -INFINITY;
     float2 mine = make_float2(-INFINITY, 0.f);
-    for (int s = lane; s < n_split; s += 32) {
+    for (int s = lane; s < n_split; s += 32)
         any |= __ldcg(sy.flags + (size_t)s * n_gz + gz) != 0;
-        const float2 ml = ml_of(s);
-        if (s == lane)
+    for (int p = lane; p < n_part; p += 32) {
+        const float2 ml = ml_of(p);
+        if (p == lane)
             mine = ml;
         M = fmaxf(M, ml.x);
     }
@@ -438,31 +462,34 @@ __device__ __forceinline__ void combine_row(const AttnQ8Args &a, const TreeMasks
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
     float L = 0.f;
     if (!any) {
-        for (int s0 = 0; s0 < n_split; s0 += kB) {
-            if (s0 > 0) {
+        for (int p0 = 0; p0 < n_part; p0 += kB) {
+            if (p0 > 0) {
 #pragma unroll
                 for (int u = 0; u < kB; ++u)
-                    x[u] = s0 + u < n_split ? acc_of(s0 + u) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    x[u] = p0 + u < n_part ? acc_of(p0 + u) : make_float4(0.f, 0.f, 0.f, 0.f);
             }
 #pragma unroll
             for (int u = 0; u < kB; ++u) {
-                const int s = s0 + u;
-                if (s >= n_split)
+                const int p = p0 + u;
+                if (p >= n_part)
                     break;
                 float2 ml;
-                if (s < 32) {
-                    ml.x = __shfl_sync(0xffffffffu, mine.x, s);
-                    ml.y = __shfl_sync(0xffffffffu, mine.y, s);
+                if (p < 32) {
+                    ml.x = __shfl_sync(0xffffffffu, mine.x, p);
+                    ml.y = __shfl_sync(0xffffffffu, mine.y, p);
                 } else {
-                    ml = ml_of(s);
+                    ml = ml_of(p);
                 }
-                // (a NaN reference keeps its NaN)
+                // a partial that saw nothing (m = -inf) has l = 0, or NaN, and
+                // its acc may be anything; a NaN reference keeps its NaN
                 const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
                 L += w * ml.y;
-                acc[0] += w * x[u].x;
-                acc[1] += w * x[u].y;
-                acc[2] += w * x[u].z;
-                acc[3] += w * x[u].w;
+                if (w != 0.f) {
+                    acc[0] += w * x[u].x;
+                    acc[1] += w * x[u].y;
+                    acc[2] += w * x[u].z;
+                    acc[3] += w * x[u].w;
+                }
             }
         }
     } else {
@@ -472,9 +499,12 @@ __device__ __forceinline__ void combine_row(const AttnQ8Args &a, const TreeMasks
         const float q4[4] = {q01.x, q01.y, q23.x, q23.y};
         const uint8_t *own = sy.owner + (size_t)gz * n_tiles_all;
         float Mr = -INFINITY;
-        for (int s = 0; s < n_split; ++s) {
+        for (int p = 0; p < n_part; ++p) {
+            const int s = p / ng;
             float ms, ls, as[4];
             if (__ldcg(sy.flags + (size_t)s * n_gz + gz) != 0) {
+                if (p % ng != 0)
+                    continue;   // the split as a whole, once
                 ms = -INFINITY;
                 ls = as[0] = as[1] = as[2] = as[3] = 0.f;
                 for (int t0 = 0; t0 < n_tiles_all; t0 += 32) {
@@ -487,8 +517,8 @@ __device__ __forceinline__ void combine_row(const AttnQ8Args &a, const TreeMasks
                     }
                 }
             } else {
-                const float2 ml = ml_of(s);
-                const float4 y = acc_of(s);
+                const float2 ml = ml_of(p);
+                const float4 y = acc_of(p);
                 ms = ml.x;
                 ls = ml.y;
                 as[0] = y.x;
@@ -536,11 +566,21 @@ __device__ __forceinline__ bool wait_count_bounded(const int32_t *p, int target,
     }
 }
 
+// (lane quarter, unit of 16 lanes) pairs that hold query rows of a block of
+// `rows` rows in runs of rq per quarter.
+__device__ __forceinline__ int active_units(int rows, int rq)
+{
+    int n = 0;
+    for (int q = 0; q < 4; ++q)
+        n += (max(0, min(rq, rows - q * rq)) + 15) / 16;
+    return n;
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
 attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ AttnQ8Args a,
-                    const __grid_constant__ TreeMasks masks, int n_split, int nodes_per_group,
-                    Q8Sync sy)
+                    const __grid_constant__ TreeMasks masks, int n_split, int NG,
+                    int nodes_per_group, Q8Sync sy)
 {
     const Q8Cache &kc = a.c;
     const int G = a.n_heads_q / a.n_heads_kv;
@@ -554,10 +594,14 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
     // the root node's rows 0..G-1, G <= 8, are the last block's first lanes
     const int rq0 = max((R0 + 3) / 4, min(R0, 8)), rq1 = max((R1 + 3) / 4, min(R1, 8));
     const int u0 = (rq0 + 15) / 16, u1 = (rq1 + 15) / 16;
-    const int U = u0 + u1;  // softmax warps per lane quarter (at most 3)
+    const int U = u0 + u1;  // softmax warps per lane quarter and group
+    // (quarter, unit) pairs with query rows: their warps arrive on the barriers
+    const int act0 = active_units(R0, rq0), act1 = active_units(R1, rq1);
     const bool rs_warp0 = a.root_scores != nullptr && node0 == 0;
-    const Layout lay = q8_layout(R);
+    const Layout lay = q8_layout(R, NG);
     const int SK = lay.stages_k, SV = lay.stages_v, SVB = lay.stages_vb, r_pad = lay.r_pad;
+    const int NP = lay.p_slots;
+    const int SI = NB == 2 ? 1 : NP;   // one block: S barriers of tile t are [t % SI], its slot t & 1
 
     extern __shared__ unsigned char smem_raw[];
     unsigned char *base = reinterpret_cast<unsigned char *>(
@@ -590,14 +634,15 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
             mbar_init(smem_addr(&bar->empty_v[s]), kConvWarps);
         }
         const int rs = rs_warp0 ? 1 : 0;
-        mbar_init(smem_addr(&bar->s_free[0]), 4 * u0 + (NB == 1 ? rs : 0));
-        mbar_init(smem_addr(&bar->s_free[1]), (NB == 1 ? 4 * u0 : 4 * u1) + rs);
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&bar->vb_full[i]), kConvWarps);
-            mbar_init(smem_addr(&bar->s_full[i]), 1);
-            mbar_init(smem_addr(&bar->sm_done[i]), 4 * U);
-            mbar_init(smem_addr(&bar->pv_done[i]), 1);
             mbar_init(smem_addr(&bar->drain[i]), 1);
+        }
+        for (int i = 0; i < 3; ++i) {
+            mbar_init(smem_addr(&bar->s_full[i]), 1);
+            mbar_init(smem_addr(&bar->s_free[i]), NB == 1 ? act0 + rs : (i == 0 ? act0 : act1 + rs));
+            mbar_init(smem_addr(&bar->sm_done[i]), act0 + act1);
+            mbar_init(smem_addr(&bar->pv_done[i]), 1);
         }
         mbar_init(smem_addr(&bar->o_final), 1);
         mbar_init(smem_addr(&bar->conv), kConvWarps);
@@ -690,8 +735,14 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     const int tile = cur < 0 ? -1 : cur;
                     const bool tail = tile >= nq;
                     bar->tile_of[i % kTileRing] = tile;
-                    bar->scale_of[i % kTileRing] =
-                        sc_cur[0] | (sc_cur[1] << 8) | (sc_cur[2] << 16) | (sc_cur[3] << 24);
+                    if (tile < 0)   // every group's end
+                        bar->tile_of[(i + 1) % kTileRing] = bar->tile_of[(i + 2) % kTileRing] = -1;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float kf = q8_factor(sc_cur[h]);
+                        const uint32_t vb = sc_cur[h] == 255u ? 255u : sc_cur[2 + h];
+                        aux->scale_of[i % kTileRing][h] = make_float4(kf, q8_log2(vb), q8_inverse(vb), 0.f);
+                    }
                     bar->entry_of[i % kTileRing] = ke;
                     if (tile >= 0)
                         owner[tile] = (uint8_t)split;
@@ -746,14 +797,13 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 float *dst_row = a.root_scores + (size_t)(g * G + (mine ? r : 0)) * n_ctx;
                 const bool vec = ((reinterpret_cast<uintptr_t>(a.root_scores) | (uintptr_t)n_ctx * 4) & 7) == 0;
                 for (int t = 0;; ++t) {
-                    const int slot = NB == 2 ? 1 : (t & 1), ph = NB == 2 ? (t & 1) : ((t >> 1) & 1);
-                    if (!warp_wait_bounded(smem_addr(&bar->s_full[slot]), ph, abort, hdr))
+                    const int slot = NB == 2 ? 1 : (t & 1), sb = NB == 2 ? 1 : t % SI;
+                    if (!warp_wait_bounded(smem_addr(&bar->s_full[sb]), (t / SI) & 1, abort, hdr))
                         break;
                     const int tile = bar->tile_of[t % kTileRing];
                     if (tile < 0)
                         break;
                     tc_fence_after();
-                    const uint32_t sc = bar->scale_of[t % kTileRing];
                     const bool q8 = tile < nq;
                     const int r0 = (q8 ? tile : tile - nq) * kTileN;
                     const int left = (q8 ? kc.n_q8 : kc.n_tail) - r0;   // context positions here
@@ -766,7 +816,7 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                         uint32_t rr[32];
                         tmem_ld16x256_x8(tmem + kSCol + 128 * slot + 64 * h, rr);
                         if (mine) {
-                            const float f = rsc * q8_factor((sc >> (8 * h)) & 0xFFu);
+                            const float f = rsc * aux->scale_of[t % kTileRing][h].x;
                             float *dst = dst_row + pos0 + 64 * h + c0;
                             unsigned long long nan = 0ull;
                             if (!q8)
@@ -794,7 +844,7 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0)
-                        mbar_arrive(smem_addr(&bar->s_free[slot]));
+                        mbar_arrive(smem_addr(&bar->s_free[sb]));
                 }
             }
         } else if (lane == 0 && warp == 1) {
@@ -809,17 +859,26 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 const int parts = tile >= nq ? 2 : 1;
                 bool ok = parts == 1 || wait_bounded(smem_addr(&bar->full_k[(ke + 1) % SK]),
                                                      ((ke + 1) / SK) & 1, abort, hdr);
+                if (tile < 0) {
+                    // the end, to each block or each group, once its readers are
+                    // past the barrier's last phase
+                    for (int i = 0; i < (NB == 2 ? 2 : NG); ++i) {
+                        const int sb = NB == 2 ? i : (t + i) % SI, before = NB == 2 ? t - 1 : t + i - SI;
+                        if (before >= 0 && !wait_bounded(smem_addr(&bar->s_free[sb]), (before / SI) & 1,
+                                                         abort, hdr))
+                            break;
+                        mbar_arrive(smem_addr(&bar->s_full[sb]));
+                    }
+                    break;
+                }
                 for (int b = 0; b < NB && ok; ++b) {
-                    const int slot = NB == 2 ? b : (t & 1);
-                    const int used = NB == 2 ? t : (t >> 1);   // earlier tiles in this slot
-                    if (used > 0 && !wait_bounded(smem_addr(&bar->s_free[slot]), (used - 1) & 1,
-                                                  abort, hdr)) {
+                    const int slot = NB == 2 ? b : (t & 1), sb = NB == 2 ? b : t % SI;
+                    // the tile before it in this slot is in its readers' registers
+                    const int before = NB == 2 ? t - 1 : t - 2;
+                    if (before >= 0 && !wait_bounded(smem_addr(&bar->s_free[NB == 2 ? b : before % SI]),
+                                                     (before / SI) & 1, abort, hdr)) {
                         ok = false;
                         break;
-                    }
-                    if (tile < 0) {
-                        mbar_arrive(smem_addr(&bar->s_full[slot]));   // the end
-                        continue;
                     }
                     tc_fence_after();
                     const uint32_t d = tmem + kSCol + 128 * slot;
@@ -842,9 +901,9 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                                 mma8_ss(d, qd + 2 * kk, kd + 2 * kk, idesc, i + kk > 0);
                         }
                     }
-                    mma_commit(smem_addr(&bar->s_full[slot]));
+                    mma_commit(smem_addr(&bar->s_full[sb]));
                 }
-                if (!ok || tile < 0)
+                if (!ok)
                     break;
                 for (int part = 0; part < parts; ++part)
                     mma_commit(smem_addr(&bar->empty_k[(ke + part) % SK]));
@@ -866,20 +925,23 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     mma_commit(smem_addr(&bar->o_final));   // after the last PV
                     break;
                 }
-                if (!wait_bounded(smem_addr(&bar->sm_done[t & 1]), (t >> 1) & 1, abort, hdr))
+                const int ps = t % NP, ph = (t / NP) & 1;
+                if (!wait_bounded(smem_addr(&bar->sm_done[ps]), ph, abort, hdr))
                     break;
                 tc_fence_after();
-                const uint64_t vd = vd0 + (uint64_t)s * (kVbBytes >> 4);
-                const uint64_t pd = pd0 + (uint64_t)(t & 1) * ((uint64_t)(r_pad * 256) >> 4);
-                if (t == 0)
-                    mma_ss_c<0>(tmem, vd, pd, idesc);
-                else
-                    mma_ss_c<1>(tmem, vd, pd, idesc);
+                uint64_t vd = vd0 + (uint64_t)s * (kVbBytes >> 4);
+                uint64_t pd = pd0 + (uint64_t)ps * ((uint64_t)(r_pad * 256) >> 4);
+                const uint32_t d = tmem + (NG == 3 ? 64 * ps : 0);
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
 #pragma unroll
-                for (int kk = 1; kk < kTileN / 16; ++kk)
-                    mma_ss_c<1>(tmem, vd + ((kk * 2048) >> 4),
-                                pd + (((kk >> 2) * p_half + (kk & 3) * 32) >> 4), idesc);
-                mma_commit(smem_addr(&bar->pv_done[t & 1]));
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma16_ss(d, vd + ((kk * 2048) >> 4), pd + ((kk * 32) >> 4), idesc,
+                                 t >= NG || h + kk > 0);
+                    vd += (4 * 2048) >> 4;
+                    pd += p_half >> 4;
+                }
+                mma_commit(smem_addr(&bar->pv_done[ps]));
             }
             mma_commit(smem_addr(&bar->drain[1]));
             wait_drain(smem_addr(&bar->drain[1]), 0);
@@ -896,8 +958,8 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
             if (tile < 0) {
                 // the PV issuer's end, once it is past the slot's last tile (two
                 // phases at once would pass it by)
-                if (t >= SVB && !warp_wait_bounded(smem_addr(&bar->pv_done[(t - SVB) & 1]),
-                                                   ((t - SVB) >> 1) & 1, abort, hdr))
+                if (t >= SVB && !warp_wait_bounded(smem_addr(&bar->pv_done[(t - SVB) % NP]),
+                                                   ((t - SVB) / NP) & 1, abort, hdr))
                     break;
                 if (lane == 0)
                     mbar_arrive(smem_addr(&bar->vb_full[t % SVB]));
@@ -941,8 +1003,8 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 if (tid == 0) {
                     const int e1 = split_exp(max(*(volatile uint32_t *)&bar->top[2],
                                                  *(volatile uint32_t *)&bar->top[3]));
-                    bar->scale_of[t % kTileRing] =
-                        (uint32_t)(e + 127) | ((uint32_t)(e1 + 127) << 8) | (127u << 16) | (127u << 24);
+                    aux->scale_of[t % kTileRing][0].x = two_to(e);
+                    aux->scale_of[t % kTileRing][1].x = two_to(e1);
                 }
                 const int e0 = bar->entry_of[t % kTileRing];
                 unsigned char *khi = sK + (e0 % SK) * kRawBytes, *klo = sK + ((e0 + 1) % SK) * kRawBytes;
@@ -974,28 +1036,20 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 vrow = have && !bad ? kc.v_tail + at : nullptr;
             }
             // the bf16 slot is free once PV of the tile before it in it is done
-            if (t >= SVB && !warp_wait_bounded(smem_addr(&bar->pv_done[(t - SVB) & 1]),
-                                               ((t - SVB) >> 1) & 1, abort, hdr))
+            if (t >= SVB && !warp_wait_bounded(smem_addr(&bar->pv_done[(t - SVB) % NP]),
+                                               ((t - SVB) / NP) & 1, abort, hdr))
                 break;
             if (tile < nq) {
-                // 16 codes per thread and step: a warp reads 512 consecutive
-                // bytes; halves 0 and 1 of V's columns write their two chunks in
-                // opposite order, so that eight lanes' stores hit eight banks
-                const unsigned char *raw = sV + s * kRawBytes;
-#pragma unroll 2
-                for (int i = 0; i < kRawBytes / (16 * 32 * kConvWarps); ++i) {
-                    const int u = tid + i * 32 * kConvWarps;   // 16-byte unit of the tile
-                    const int p = u >> 3, c16 = u & 7;
-                    const uint4 w = *reinterpret_cast<const uint4 *>(raw + 16 * u);
-                    const uint2 x0 = codes_to_bf16(w.x), x1 = codes_to_bf16(w.y);
-                    const uint2 x2 = codes_to_bf16(w.z), x3 = codes_to_bf16(w.w);
-                    const uint4 first = make_uint4(x0.x, x0.y, x1.x, x1.y);
-                    const uint4 second = make_uint4(x2.x, x2.y, x3.x, x3.y);
-                    const int half = c16 >> 2, ch = 2 * (c16 & 3);
-                    unsigned char *dst = vb + half * kBoxBytes + p * 128;
-                    const int a0 = ((ch + half) ^ (p & 7)) << 4, a1 = ((ch + 1 - half) ^ (p & 7)) << 4;
-                    *reinterpret_cast<uint4 *>(dst + a0) = half ? second : first;
-                    *reinterpret_cast<uint4 *>(dst + a1) = half ? first : second;
+                // 8 codes per thread and step: a thread keeps its column chunk
+                // and its row mod 8, so every address is an offset of two bases
+                const int ch = tid & 15, r8 = tid >> 4;
+                const unsigned char *src = sV + s * kRawBytes + 8 * tid;
+                unsigned char *dst = vb + (ch >> 3) * kBoxBytes + r8 * 128 + (((ch & 7) ^ r8) << 4);
+#pragma unroll 4
+                for (int i = 0; i < kTileN / 8; ++i) {
+                    const uint2 w = *reinterpret_cast<const uint2 *>(src + i * 8 * kD);
+                    const uint2 x = codes_to_bf16(w.x), y = codes_to_bf16(w.y);
+                    *reinterpret_cast<uint4 *>(dst + i * 1024) = make_uint4(x.x, x.y, y.x, y.y);
                 }
             } else {
 #pragma unroll 4
@@ -1072,9 +1126,10 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
         tc_fence_before();
         named_bar_sync(kBarQuery, kThreads - 32 * (1 + kConvWarps));
         tc_fence_after();
-        if ((warp - 4) / 4 < U) {
+        if ((warp - 4) / 4 < U * NG) {
             // ------------------------------------------------ softmax
-            const int q = warp & 3, j = (warp - 4) >> 2;
+            const int q = warp & 3, j = NG == 3 ? 0 : (warp - 4) >> 2;
+            const int grp = NG == 3 ? (warp - 4) >> 2 : 0;
             const int b = j < u0 ? 0 : 1;
             const int lb = 16 * (b == 0 ? j : j - u0);  // unit's first lane in the quarter
             const int Rb = b == 0 ? R0 : R1, rqb = b == 0 ? rq0 : rq1;
@@ -1092,34 +1147,42 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
             // l gives the address of row l % 8); rows that are none go to the
             // scratch kilobyte
             const uint32_t p_addr = smem_addr(sP);
-            const uint32_t p_scratch = p_addr + (uint32_t)r_pad * 512;
+            const uint32_t p_scratch = p_addr + (uint32_t)r_pad * 256 * NP;
             const int rl = lane & 7, pnA = nbase + rl, pnB = pnA + 8;
             const bool okA = rl < nvA, okB = rl < nvB;
             const uint32_t p_rowA = okA ? p_addr + (uint32_t)((pnA >> 3) * 1024 + (pnA & 7) * 128) : p_scratch;
             const uint32_t p_rowB = okB ? p_addr + (uint32_t)((pnB >> 3) * 1024 + (pnB & 7) * 128) : p_scratch;
             const uint32_t p_half = (uint32_t)r_pad * 128;
+            const uint32_t p_stepA = okA ? p_half : 0u, p_stepB = okB ? p_half : 0u;
+            const int rxA = okA ? pnA & 7 : 0, rxB = okB ? pnB & 7 : 0;
             const float rsA = vA ? aux->row_scale[nA] : 1.f, rsB = vB ? aux->row_scale[nB] : 1.f;
             const unsigned long long ancA = aux->anc[node0 + (vA ? q8_row_of(nA, R) / G : 0)];
             const unsigned long long ancB = aux->anc[node0 + (vB ? q8_row_of(nB, R) / G : 0)];
-            float mA = -INFINITY, mB = -INFINITY, lA = 0.f, lB = 0.f;
+            // references, negated (2^(x + n)); sums, NaN from the start for a
+            // query row that is none (its scale is NaN)
+            float mA = -INFINITY, mB = -INFINITY, nmA = 0.f, nmB = 0.f;
+            float lA = rsA == rsA ? 0.f : rsA, lB = rsB == rsB ? 0.f : rsB;
+            bool fresh = true;   // some row has no reference yet (uniform)
             bool ok = true;
-            for (int t = 0;; ++t) {
-                const int slot = NB == 2 ? b : (t & 1), ph = NB == 2 ? (t & 1) : ((t >> 1) & 1);
-                if (!warp_wait_bounded(smem_addr(&bar->s_full[slot]), ph, abort, hdr)) {
+            for (int t = grp; hasA; t += NG) {
+                const int slot = NB == 2 ? b : (t & 1), sb = NB == 2 ? b : t % SI;
+                if (!warp_wait_bounded(smem_addr(&bar->s_full[sb]), (t / SI) & 1, abort, hdr)) {
                     ok = false;
                     break;
                 }
                 const int tile = bar->tile_of[t % kTileRing];
                 if (tile < 0)
                     break;
-                uint32_t sc = bar->scale_of[t % kTileRing];
                 const bool tail = tile >= nq;
                 // context positions from the half tile's first on
                 int left = tail ? kc.n_tail - (tile - nq) * kTileN : kc.n_q8 - tile * kTileN;
+                const float4 *scl = aux->scale_of[t % kTileRing];
+                const int ps = t % NP;
+                uint32_t atA = p_rowA + 2 * ps * p_stepA, atB = p_rowB + 2 * ps * p_stepB;
                 // the halves are the tile's two scale blocks; one copy of the code
                 // serves both (the loop must stay inside the instruction cache)
 #pragma unroll 1
-                for (int h = 0; h < 2; ++h, left -= 64, sc >>= 8) {
+                for (int h = 0; h < 2; ++h, left -= 64) {
                     tc_fence_after();
                     uint32_t r[32];
                     tmem_ld16x256_x8(s_addr + 128 * slot + 64 * h, r);
@@ -1128,13 +1191,12 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0)
-                            mbar_arrive(smem_addr(&bar->s_free[slot]));
+                            mbar_arrive(smem_addr(&bar->s_free[sb]));
                     }
+                    const float4 sc = scl[h];
                     // factor of the scores: never zero, as a masked score is -inf
-                    const float kf = q8_factor(sc & 0xFFu);
                     constexpr float kTiny = 1.17549435e-38f;
-                    const float cA = rsA * kf < kTiny ? kTiny : rsA * kf;
-                    const float cB = rsB * kf < kTiny ? kTiny : rsB * kf;
+                    const float cA = fmaxf(rsA * sc.x, kTiny), cB = fmaxf(rsB * sc.x, kTiny);
                     if (left < 64) {
                         const unsigned long long wA = row_vis(tail ? ancA : 0ull, left);
                         const unsigned long long wB = row_vis(tail ? ancB : 0ull, left);
@@ -1158,7 +1220,7 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     }
                     // a row that has seen nothing yet takes this half's max,
                     // rounded up to an integer, as its reference
-                    if (__any_sync(0xffffffffu, mA == -INFINITY || mB == -INFINITY)) {
+                    if (fresh) {
                         float yA = half_max<0>(r) * cA, yB = half_max<2>(r) * cB;
                         yA = fmaxf(yA, __shfl_xor_sync(0xffffffffu, yA, 1));
                         yB = fmaxf(yB, __shfl_xor_sync(0xffffffffu, yB, 1));
@@ -1168,32 +1230,32 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                             mA = ceilf(yA);
                         if (mB == -INFINITY)
                             mB = ceilf(yB);
+                        nmA = mA == -INFINITY ? 0.f : -mA;
+                        nmB = mB == -INFINITY ? 0.f : -mB;
+                        fresh = __any_sync(0xffffffffu, (vA && mA == -INFINITY) || (vB && mB == -INFINITY));
                     }
-                    const uint32_t vbyte = (sc >> 16) & 0xFFu;
-                    const float ve = q8_log2(vbyte), vi = q8_inverse(vbyte);
                     uint32_t pA[8], pB[8];
-                    if (hasA)
-                        lA += exp_row<0>(r, cA, (mA == -INFINITY ? 0.f : -mA) + ve, pA) * vi;
+                    lA += exp_row<0>(r, cA, nmA + sc.y, pA) * sc.z;
                     if (hasB)
-                        lB += exp_row<2>(r, cB, (mB == -INFINITY ? 0.f : -mB) + ve, pB) * vi;
-                    // this P^T tile is free once PV(t - 2) is done
-                    if (h == 0 && t >= 2 &&
-                        !warp_wait_bounded(smem_addr(&bar->pv_done[t & 1]), ((t - 2) >> 1) & 1, abort, hdr)) {
+                        lB += exp_row<2>(r, cB, nmB + sc.y, pB) * sc.z;
+                    // this P^T tile is free once PV(t - NP) is done
+                    if (h == 0 && t >= NP &&
+                        !warp_wait_bounded(smem_addr(&bar->pv_done[ps]), (t / NP - 1) & 1, abort, hdr)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t at = (uint32_t)(t & 1) * 2 * p_half + h * p_half;
-                    if (hasA)
-                        store_p(okA ? p_rowA + at : p_rowA, okA ? pnA & 7 : 0, lane, pA);
+                    store_p(atA, rxA, lane, pA);
                     if (hasB)
-                        store_p(okB ? p_rowB + at : p_rowB, okB ? pnB & 7 : 0, lane, pB);
+                        store_p(atB, rxB, lane, pB);
+                    atA += p_stepA;
+                    atB += p_stepB;
                 }
                 if (!ok)
                     break;
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(smem_addr(&bar->sm_done[t & 1]));
+                    mbar_arrive(smem_addr(&bar->sm_done[ps]));
             }
             // ---- (m, l) of each row (four threads' partial sums), then O^T
 #pragma unroll
@@ -1208,27 +1270,30 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 bar->overflow = 1;
             const int rows_all = a.n_tree * a.n_heads_q;
             float *ws_o = sy.part;
-            float2 *ws_ml = reinterpret_cast<float2 *>(ws_o + (size_t)n_split * rows_all * kD);
+            float2 *ws_ml = reinterpret_cast<float2 *>(ws_o + (size_t)n_split * NG * rows_all * kD);
+            const size_t part_row = ((size_t)split * NG + grp) * rows_all;
             auto orow_of = [&](int n) {
                 const int m = q8_row_of(n, R);
                 return (node0 + m / G) * a.n_heads_q + g * G + m % G;
             };
             if (ok && (lane & 3) == 0) {
                 if (vA)
-                    ws_ml[(size_t)split * rows_all + orow_of(nA)] = make_float2(mA, lA);
+                    ws_ml[part_row + orow_of(nA)] = make_float2(mA, lA);
                 if (vB)
-                    ws_ml[(size_t)split * rows_all + orow_of(nB)] = make_float2(mB, lB);
+                    ws_ml[part_row + orow_of(nB)] = make_float2(mB, lB);
             }
-            // O^T out of TMEM into the P^T tiles (free after the last PV, and
-            // just as large) in output order, then one bulk copy per node
+            // O^T out of TMEM into shared memory in output order, from the P^T
+            // tiles on (all of it is free after the last PV; one group's rows
+            // are as large as two P^T tiles), then one bulk copy per node
+            unsigned char *stage = sP + (size_t)grp * R * kD * 4;
             const bool have_o = ok && warp_wait_bounded(smem_addr(&bar->o_final), 0, abort, hdr);
             if (have_o) {
                 tc_fence_after();
                 for (int c = 32 * j; c < r_pad; c += 32 * U) {
                     uint32_t o[32];
-                    tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + c, o);
+                    tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + 64 * grp + c, o);
                     const int nv = min(32, R - c);
-                    float *dst = reinterpret_cast<float *>(sP) + (size_t)q8_row_of(c, R) * kD + 32 * q + lane;
+                    float *dst = reinterpret_cast<float *>(stage) + (size_t)q8_row_of(c, R) * kD + 32 * q + lane;
 #pragma unroll
                     for (int jj = 0; jj < 32; ++jj)
                         if (jj < nv)
@@ -1236,12 +1301,12 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 }
             }
             fence_proxy_async_smem();
-            named_bar_sync(kBarOut, 128 * U);   // every softmax warp, whatever its path
+            named_bar_sync(kBarOut, 128 * U * NG);   // every softmax warp, whatever its path
             if (!*abort && lane == 0) {
-                const int sw = warp - 4;   // 0 .. 4U-1
+                const int sw = 4 * j + q;   // 0 .. 4U-1
                 for (int node = sw; node < T; node += 4 * U)
-                    bulk_store(ws_o + ((size_t)split * rows_all + (size_t)(node0 + node) * a.n_heads_q + g * G) * kD,
-                               smem_addr(sP) + (uint32_t)(node * G * kD * 4), (uint32_t)(G * kD * 4));
+                    bulk_store(ws_o + (part_row + (size_t)(node0 + node) * a.n_heads_q + g * G) * kD,
+                               smem_addr(stage) + (uint32_t)(node * G * kD * 4), (uint32_t)(G * kD * 4));
                 bulk_commit();
                 bulk_wait_all();
                 fence_proxy_async_global();
@@ -1270,7 +1335,7 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
     if (!*abort) {
         for (int m = split + warp * n_split; m < R; m += (kThreads / 32) * n_split)
             combine_row(a, masks, (node0 + m / G) * a.n_heads_q + g * G + m % G, g, gz, n_gz,
-                        n_split, nq, n_tiles_all, sy);
+                        n_split, NG, nq, n_tiles_all, sy);
     }
     __syncthreads();
     if (threadIdx.x == 0 && atomicAdd(&ctr[2], 1) == n_split - 1) {
@@ -1281,7 +1346,7 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
 }
 
 struct T128Plan {
-    int n_split, node_groups, nodes_per_group;
+    int n_split, node_groups, nodes_per_group, groups;
     size_t part, flags, owner, total;
 };
 
@@ -1302,7 +1367,8 @@ T128Plan q8_plan(int n_heads_q, int n_heads_kv, int n_q8, int n_tail, int n_tree
     p.n_split = want > 255 ? 255 : want;
     const size_t n_gz = (size_t)n_heads_kv * p.node_groups;
     p.part = kHeaderBytes + kQ8SyncBytes;
-    p.flags = p.part + align_up((size_t)p.n_split * n_tree * n_heads_q * (kD + 2) * sizeof(float), 256);
+    p.groups = q8_groups(p.nodes_per_group * G);
+    p.flags = p.part + align_up((size_t)p.n_split * p.groups * n_tree * n_heads_q * (kD + 2) * sizeof(float), 256);
     p.owner = p.flags + align_up((size_t)p.n_split * n_gz * sizeof(int32_t), 256);
     p.total = p.owner + align_up(n_gz * n_tiles, 256);
     return p;
@@ -1375,8 +1441,8 @@ cudaError_t attn_q8_t128_launch(const AttnQ8Args &a, const TreeMasks &masks, int
     at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, attn_q8_t128_kernel, mk, mv, a, masks, p.n_split, p.nodes_per_group,
-                           sy);
+    e = cudaLaunchKernelEx(&cfg, attn_q8_t128_kernel, mk, mv, a, masks, p.n_split, p.groups,
+                           p.nodes_per_group, sy);
     if (e == cudaSuccess)
         e = cudaGetLastError();
     if (e == cudaSuccess)
