@@ -10,15 +10,15 @@
 //                      bit, which 3 bits represent), down to 2^-16 of the
 //                      scaled row.  So S = hi K^T + lo K^T costs what one
 //                      bf16 product costs, and K is never converted.
-//   O^T += V^T P^T     kind::f16 on bf16: V's codes are bf16 numbers; four
-//                      converter warps write them out once per tile.
+//   O^T += V^T P^T     kind::f16 on bf16: V's codes are bf16 numbers; the
+//                      softmax warps write them out once per tile.
 // The scales (a power of two per 64 rows) never touch the products' inputs:
 // K's multiplies the score inside the exponent's FMA, V's is added to the
 // exponent, so the weight leaves as p * s_v with its one rounding to bf16,
 // and each block's sum is multiplied back by 1 / s_v.
 //
 // A tail tile (bf16 rows: newest context, tree) goes through the same
-// products: a converter warp scales its keys by block and splits them like
+// products: a softmax warpgroup scales its keys by block and splits them like
 // the queries into an e4m3 and an e5m2 tile (two K slots, four products),
 // and copies V.  Rows with an infinity or a NaN are zeroed there and noted;
 // a query row that sees one gets a NaN sum.
@@ -31,16 +31,18 @@
 // weights' own rounding, so rows that rest on few positions need no second
 // look.
 //
-// CTA = (split, KV head, node group), 20 warps, one CTA per SM:
+// CTA = (split, KV head, node group), 16 warps, one CTA per SM:
 //   warp 0      root scores out of S        warp 1  QK issuer, TMEM
 //   warp 2      PV issuer                   warp 3  TMA producer
-//   warps 4-15  softmax                     warps 16-19  converters
+//   warps 4-15  softmax, and V's codes to bf16
+// (Separate converter warps were slower: every sub-partition then ran three
+// unlike loops at once and waited for instructions.)
 // P^T is double-buffered, and with one query block (R <= 128) S too, so a
 // tile's exponentials overlap the previous tile's PV and the next one's QK.
 // With at most 64 query rows one warpgroup is enough for a tile, but its chain
 // of waits and loads is longer than the tile's stream from HBM: the three
 // softmax warpgroups then take tiles in turn, each with its own reference,
-// O^T and P^T, and leave three partials per split.
+// O^T, P^T and V, and their partials are merged before they leave.
 // TMEM: O^T in [0, 192), Q_0 (hi, lo) in [192, 256), S in [256, 512).
 //
 // Every wait is bounded (about a second): on expiry the kernel records
@@ -67,7 +69,7 @@ constexpr int kBlockM = 128;                 // query rows per QK block (TMEM la
 constexpr int kRawBytes = kTileN * kD;       // codes of K (or V) of a tile: 16 KB
 constexpr int kBoxBytes = kTileN * 64 * 2;   // one 64-column half of a bf16 V tile
 constexpr int kVbBytes = 2 * kBoxBytes;
-constexpr int kThreads = 640;                // 20 warps
+constexpr int kThreads = 512;                // 16 warps
 constexpr int kMaxStages = 5;
 constexpr int kMaxRows = 192;
 constexpr int kQCol = 192;                   // Q of block 0: hi 32 columns, lo 32 columns
@@ -77,9 +79,8 @@ constexpr int kQ1Bytes = 2 * kBlockM * kD;   // Q of block 1 in shared memory: h
 constexpr float kMaxRowSum = 9.223372036854775808e18f;   // 2^63
 constexpr size_t kSmemLimit = 232448;        // dynamic shared memory per CTA
 constexpr int kBarQuery = 1;                 // named barrier: query rows in place
-constexpr int kBarOut = 2;                   // named barrier: O^T staged in shared memory
+constexpr int kBarOut = 2;                   // named barrier: O^T staged, or merged, in shared memory
 constexpr int kTileRing = 16;                // entries of the tile rings (> any role's lead)
-constexpr int kConvWarps = 4;
 constexpr int kBarQLoads = 3;                // named barrier: the query rows are read
 constexpr int kQLoadThreads = 32 * 9;        // warps 4-11 arrive, the producer warp waits
 constexpr int kMaxGz = 256;                  // (KV head, node group) pairs: counters in the workspace
@@ -88,16 +89,16 @@ static_assert(kMaxGz * 16 <= (int)kQ8SyncBytes, "counters fit their region");
 struct Bars {
     uint64_t full_k[kMaxStages];
     uint64_t empty_k[kMaxStages];
-    uint64_t full_v[kMaxStages];    // codes of V landed (or: a tail tile, or the end)
+    uint64_t full_v[kMaxStages];    // codes of V landed (or: a tail tile)
     uint64_t empty_v[kMaxStages];
-    uint64_t vb_full[2];            // V in bf16 (or the end)
     uint64_t s_full[3];             // QK landed: by block, or (one block) by tile in turn
     uint64_t s_free[3];             // its readers hold S in registers
-    uint64_t sm_done[3];            // per P^T slot: every softmax warp wrote its rows
+    uint64_t sm_done[3];            // per P^T slot: P^T and V are written
     uint64_t pv_done[3];            // per P^T slot: PV is complete
     uint64_t o_final;
     uint64_t drain[2];
-    uint64_t conv;                  // the converter warps meet (tail tiles)
+    uint64_t conv[3];               // a warpgroup that turns a tail tile meets
+    uint64_t info[kTileRing];       // tile_of, scale_of of that tile are written
     // per tile, at [t % kTileRing]: its index (-1 after the last) and its
     // first K ring entry.  Written by the producer before the arrival that
     // the readers wait for.
@@ -105,7 +106,7 @@ struct Bars {
     volatile int32_t entry_of[kTileRing];
     uint32_t bad[4][4];             // tail tile t % 4: rows with a value that is no number
     uint32_t bad_k[4][4];
-    uint32_t top[4];                // converters: largest key magnitude of each 32 rows
+    uint32_t top[3][4];             // tail tile: largest key magnitude of each 32 rows
     uint32_t tmem_base;
     uint32_t abort;
     int32_t overflow;
@@ -113,11 +114,12 @@ struct Bars {
 
 struct Aux {
     Bars bar;
-    // per tile and half, written like tile_of (a tail tile's k by a converter):
+    // per tile and half, written like tile_of (a tail tile's k by the warps that turn it):
     // K's scale, V's as an exponent, V's inverse.  A block that is NaN, in K
     // or V, has a NaN exponent and inverse: its weights and sums are NaN.
     float4 scale_of[kTileRing][2];
     unsigned long long anc[TS_MAX_TREE];
+    float2 ml[3][64];               // (m, l) of each group's rows, to be merged
     float row_scale[2 * kBlockM];   // softmax scale * log2 e * the query row's scale
 };
 constexpr size_t kAuxBytes = (sizeof(Aux) + 1023) / 1024 * 1024;
@@ -144,7 +146,7 @@ __host__ __device__ inline Layout q8_layout(int rows, int groups)
     L.p_off = rows > kBlockM ? kQ1Bytes : 0;
     // the P^T tiles, then 1 KB that rows past the query rows are written to
     L.vb_off = L.p_off + (size_t)L.r_pad * 256 * L.p_slots + 1024;
-    L.stages_vb = rows > kBlockM ? 1 : 2;
+    L.stages_vb = rows > kBlockM ? 1 : L.p_slots;
     L.k_off = L.vb_off + (size_t)L.stages_vb * kVbBytes;
     const size_t fixed = 1024 + L.k_off + kAuxBytes;
     int stages = (int)((kSmemLimit - fixed) / kRawBytes);
@@ -353,8 +355,7 @@ __device__ __forceinline__ void store_p(uint32_t row, int rx, int lane, const ui
 struct Q8Sync {
     int32_t *sync;    // [Hkv * groups][4]: tile counter, arrivals, finished combines, unused;
                       // zero when a call starts, and again when it ends
-    float *part;      // acc fp32 [n_split * groups][T*Hq][128], then (m, l) fp32
-                      // [n_split * groups][T*Hq][2]
+    float *part;      // acc fp32 [n_split][T*Hq][128], then (m, l) fp32 [n_split][T*Hq][2]
     int32_t *flags;   // [n_split][Hkv * groups]: some row's sum outgrew its reference
     uint8_t *owner;   // [Hkv * groups][n_tiles]: the split that streamed each tile
 };
@@ -424,16 +425,15 @@ __device__ void tile_exact(const AttnQ8Args &a, unsigned long long anc, int g, c
 }
 
 // One output row, by one warp: out = sum 2^(m - M) acc / sum 2^(m - M) l over
-// the n_split * ng partials, a flagged split recomputed exactly.
+// the splits, a flagged split recomputed exactly.
 __device__ __forceinline__ void combine_row(const AttnQ8Args &a, const TreeMasks &masks, int row,
-                                            int g, int gz, int n_gz, int n_split, int ng, int nq,
+                                            int g, int gz, int n_gz, int n_split, int nq,
                                             int n_tiles_all, const Q8Sync &sy)
 {
     const int rows_all = a.n_tree * a.n_heads_q;
     const int lane = threadIdx.x & 31;
-    const int n_part = n_split * ng;
     const float *ws_o = sy.part;
-    const float2 *ws_ml = reinterpret_cast<const float2 *>(ws_o + (size_t)n_part * rows_all * kD);
+    const float2 *ws_ml = reinterpret_cast<const float2 *>(ws_o + (size_t)n_split * rows_all * kD);
     auto ml_of = [&](int p) { return __ldcg(ws_ml + (size_t)p * rows_all + row); };
     auto acc_of = [&](int p) {
         return __ldcg(reinterpret_cast<const float4 *>(ws_o + ((size_t)p * rows_all + row) * kD) + lane);
@@ -443,13 +443,13 @@ __device__ __forceinline__ void combine_row(const AttnQ8Args &a, const TreeMasks
     float4 x[kB];
 #pragma unroll
     for (int u = 0; u < kB; ++u)
-        x[u] = u < n_part ? acc_of(u) : make_float4(0.f, 0.f, 0.f, 0.f);
+        x[u] = u < n_split ? acc_of(u) : make_float4(0.f, 0.f, 0.f, 0.f);
     bool any = false;
     float M = -INFINITY;
     float2 mine = make_float2(-INFINITY, 0.f);
     for (int s = lane; s < n_split; s += 32)
         any |= __ldcg(sy.flags + (size_t)s * n_gz + gz) != 0;
-    for (int p = lane; p < n_part; p += 32) {
+    for (int p = lane; p < n_split; p += 32) {
         const float2 ml = ml_of(p);
         if (p == lane)
             mine = ml;
@@ -462,16 +462,16 @@ __device__ __forceinline__ void combine_row(const AttnQ8Args &a, const TreeMasks
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
     float L = 0.f;
     if (!any) {
-        for (int p0 = 0; p0 < n_part; p0 += kB) {
+        for (int p0 = 0; p0 < n_split; p0 += kB) {
             if (p0 > 0) {
 #pragma unroll
                 for (int u = 0; u < kB; ++u)
-                    x[u] = p0 + u < n_part ? acc_of(p0 + u) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    x[u] = p0 + u < n_split ? acc_of(p0 + u) : make_float4(0.f, 0.f, 0.f, 0.f);
             }
 #pragma unroll
             for (int u = 0; u < kB; ++u) {
                 const int p = p0 + u;
-                if (p >= n_part)
+                if (p >= n_split)
                     break;
                 float2 ml;
                 if (p < 32) {
@@ -499,12 +499,10 @@ __device__ __forceinline__ void combine_row(const AttnQ8Args &a, const TreeMasks
         const float q4[4] = {q01.x, q01.y, q23.x, q23.y};
         const uint8_t *own = sy.owner + (size_t)gz * n_tiles_all;
         float Mr = -INFINITY;
-        for (int p = 0; p < n_part; ++p) {
-            const int s = p / ng;
+        for (int p = 0; p < n_split; ++p) {
+            const int s = p;
             float ms, ls, as[4];
             if (__ldcg(sy.flags + (size_t)s * n_gz + gz) != 0) {
-                if (p % ng != 0)
-                    continue;   // the split as a whole, once
                 ms = -INFINITY;
                 ls = as[0] = as[1] = as[2] = as[3] = 0.f;
                 for (int t0 = 0; t0 < n_tiles_all; t0 += 32) {
@@ -566,14 +564,94 @@ __device__ __forceinline__ bool wait_count_bounded(const int32_t *p, int target,
     }
 }
 
-// (lane quarter, unit of 16 lanes) pairs that hold query rows of a block of
-// `rows` rows in runs of rq per quarter.
-__device__ __forceinline__ int active_units(int rows, int rq)
+// The keys of tail tile t into its two K slots, by the 128 threads of one
+// warpgroup, a row each: scaled by block of 64 rows, split into e4m3 and e5m2
+// codes; notes the rows with an infinity or a NaN (and zeroes them).  False
+// when a wait ran out.
+__device__ __noinline__ bool tail_keys(const AttnQ8Args &a, Aux *aux, unsigned char *sK, int SK, int g,
+                                       int nq, int t, int grp, int &met, volatile uint32_t *abort,
+                                       WorkspaceHeader *hdr)
 {
-    int n = 0;
-    for (int q = 0; q < 4; ++q)
-        n += (max(0, min(rq, rows - q * rq)) + 15) / 16;
-    return n;
+    Bars *bar = &aux->bar;
+    const Q8Cache &kc = a.c;
+    const int tid = threadIdx.x & 127, lane = threadIdx.x & 31, w = tid >> 5;
+    const int row = (bar->tile_of[t % kTileRing] - nq) * kTileN + tid;
+    const bool have = row < kc.n_tail + a.n_tree;
+    const int64_t at = ((int64_t)g * kc.tail_cap + row) * kD;
+    const uint4 *kr = reinterpret_cast<const uint4 *>(kc.k_tail + at);
+    const uint4 *vr = reinterpret_cast<const uint4 *>(kc.v_tail + at);
+    uint32_t tk = 0, tv = 0;
+    if (have) {
+#pragma unroll 8
+        for (int c = 0; c < kD / 8; ++c) {
+            tk = __vmaxu2(tk, top_word(__ldg(kr + c)));
+            tv = __vmaxu2(tv, top_word(__ldg(vr + c)));
+        }
+    }
+    tk = top_of(tk);
+    tv = top_of(tv);
+    const bool bad_k = tk >= 0x7F80u, bad = bad_k || tv >= 0x7F80u;
+    const uint32_t wk = __ballot_sync(0xffffffffu, bad_k), wb = __ballot_sync(0xffffffffu, bad);
+    const uint32_t wtop = __reduce_max_sync(0xffffffffu, bad ? 0u : tk);
+    if (lane == 0) {
+        bar->bad_k[t & 3][w] = wk;
+        bar->bad[t & 3][w] = wb;
+        bar->top[grp][w] = wtop;
+        mbar_arrive(smem_addr(&bar->conv[grp]));
+    }
+    if (!warp_wait_bounded(smem_addr(&bar->conv[grp]), met++ & 1, abort, hdr))
+        return false;
+    volatile uint32_t *top = bar->top[grp];
+    const int e = split_exp(max(top[w & 2], top[(w & 2) + 1]));
+    if (tid == 0) {
+        aux->scale_of[t % kTileRing][0].x = two_to(e);
+        aux->scale_of[t % kTileRing][1].x = two_to(split_exp(max(top[2], top[3])));
+    }
+    const int e0 = bar->entry_of[t % kTileRing];
+    unsigned char *khi = sK + (e0 % SK) * kRawBytes, *klo = sK + ((e0 + 1) % SK) * kRawBytes;
+    const float f = two_to(-e);
+#pragma unroll 2
+    for (int c = 0; c < kD / 16; ++c) {   // 16 codes a step
+        uint4 hi = make_uint4(0u, 0u, 0u, 0u), lo = hi;
+        if (have && !bad) {
+            uint2 h0, l0, h1, l1;
+            split_16b(__ldg(kr + 2 * c), f, h0, l0);
+            split_16b(__ldg(kr + 2 * c + 1), f, h1, l1);
+            hi = make_uint4(h0.x, h0.y, h1.x, h1.y);
+            lo = make_uint4(l0.x, l0.y, l1.x, l1.y);
+        }
+        const int off = tid * 128 + ((c ^ (tid & 7)) << 4);
+        *reinterpret_cast<uint4 *>(khi + off) = hi;
+        *reinterpret_cast<uint4 *>(klo + off) = lo;
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0)
+        mbar_arrive(smem_addr(&bar->conv[grp]));
+    if (!warp_wait_bounded(smem_addr(&bar->conv[grp]), met++ & 1, abort, hdr))
+        return false;
+    if (tid == 0) {
+        mbar_arrive(smem_addr(&bar->full_k[e0 % SK]));
+        mbar_arrive(smem_addr(&bar->full_k[(e0 + 1) % SK]));
+    }
+    __syncwarp();
+    return true;
+}
+
+// The values of tail tile t (rows that are none, or noted by tail_keys, as
+// zeros) into a bf16 V tile, by the same 128 threads.
+__device__ __noinline__ void tail_values(const AttnQ8Args &a, Bars *bar, unsigned char *vb, int g, int nq,
+                                         int tile, int t)
+{
+    const Q8Cache &kc = a.c;
+    const int tid = threadIdx.x & 127;
+    const int row = (tile - nq) * kTileN + tid;
+    const bool use = row < kc.n_tail + a.n_tree && !((bar->bad[t & 3][tid >> 5] >> (tid & 31)) & 1u);
+    const uint4 *vr = reinterpret_cast<const uint4 *>(kc.v_tail + ((int64_t)g * kc.tail_cap + row) * kD);
+#pragma unroll 4
+    for (int c = 0; c < kD / 8; ++c)
+        *reinterpret_cast<uint4 *>(vb + (c >> 3) * kBoxBytes + tid * 128 + (((c & 7) ^ (tid & 7)) << 4)) =
+            use ? __ldg(vr + c) : make_uint4(0u, 0u, 0u, 0u);
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -595,8 +673,6 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
     const int rq0 = max((R0 + 3) / 4, min(R0, 8)), rq1 = max((R1 + 3) / 4, min(R1, 8));
     const int u0 = (rq0 + 15) / 16, u1 = (rq1 + 15) / 16;
     const int U = u0 + u1;  // softmax warps per lane quarter and group
-    // (quarter, unit) pairs with query rows: their warps arrive on the barriers
-    const int act0 = active_units(R0, rq0), act1 = active_units(R1, rq1);
     const bool rs_warp0 = a.root_scores != nullptr && node0 == 0;
     const Layout lay = q8_layout(R, NG);
     const int SK = lay.stages_k, SV = lay.stages_v, SVB = lay.stages_vb, r_pad = lay.r_pad;
@@ -631,21 +707,21 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
         }
         for (int s = 0; s < SV; ++s) {
             mbar_init(smem_addr(&bar->full_v[s]), 1);
-            mbar_init(smem_addr(&bar->empty_v[s]), kConvWarps);
+            mbar_init(smem_addr(&bar->empty_v[s]), NG == 3 ? 4 : 4 * U);
         }
         const int rs = rs_warp0 ? 1 : 0;
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_addr(&bar->vb_full[i]), kConvWarps);
-            mbar_init(smem_addr(&bar->drain[i]), 1);
-        }
+        mbar_init(smem_addr(&bar->drain[0]), 1);
+        mbar_init(smem_addr(&bar->drain[1]), 1);
+        for (int i = 0; i < kTileRing; ++i)
+            mbar_init(smem_addr(&bar->info[i]), 1);
         for (int i = 0; i < 3; ++i) {
             mbar_init(smem_addr(&bar->s_full[i]), 1);
-            mbar_init(smem_addr(&bar->s_free[i]), NB == 1 ? act0 + rs : (i == 0 ? act0 : act1 + rs));
-            mbar_init(smem_addr(&bar->sm_done[i]), act0 + act1);
+            mbar_init(smem_addr(&bar->s_free[i]), NB == 1 ? 4 * u0 + rs : (i == 0 ? 4 * u0 : 4 * u1 + rs));
+            mbar_init(smem_addr(&bar->sm_done[i]), 4 * U);
+            mbar_init(smem_addr(&bar->conv[i]), 4);
             mbar_init(smem_addr(&bar->pv_done[i]), 1);
         }
         mbar_init(smem_addr(&bar->o_final), 1);
-        mbar_init(smem_addr(&bar->conv), kConvWarps);
         bar->abort = 0u;
         bar->overflow = 0;
         fence_mbar_init();
@@ -677,79 +753,87 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 aux->anc[i] = masks.anc[i];
         if (warp != 3) {
             tc_fence_before();
-            named_bar_sync(kBarQuery, kThreads - 32 * (1 + kConvWarps));
+            named_bar_sync(kBarQuery, kThreads - 32);
             tc_fence_after();
         }
         if (warp == 3) {
             // ------------------------------------------------ TMA producer
             // (the query rows first: not behind every CTA's first ring of tiles)
             named_bar_sync(kBarQLoads, kQLoadThreads);
-            if (lane == 0) {
-                auto tile_at = [&](int k) { return n_tiles_all - 1 - k; };
-                int32_t *ctr = sy.sync + 4 * gz;
-                const uint8_t *ksc = kc.k_scale + (int64_t)g * (kc.q8_cap / kQ8Block);
-                const uint8_t *vsc = kc.v_scale + (int64_t)g * (kc.q8_cap / kQ8Block);
-                const int n_blk = kc.n_q8 / kQ8Block;
-                // scale bytes of a tile's two blocks (127, a factor of one,
-                // past the last block and on a tail tile)
-                auto scales = [&](int tile, uint32_t (&b)[4]) {
-                    const int b0 = 2 * tile;
-                    const bool h0 = tile >= 0 && b0 < n_blk, h1 = tile >= 0 && b0 + 1 < n_blk;
-                    b[0] = h0 ? __ldg(ksc + b0) : 127u;
-                    b[1] = h1 ? __ldg(ksc + b0 + 1) : 127u;
-                    b[2] = h0 ? __ldg(vsc + b0) : 127u;
-                    b[3] = h1 ? __ldg(vsc + b0 + 1) : 127u;
-                };
-                // tile i is issued while the scales of tile i + 1 and the
-                // hand-out of tile i + 2 are on their way
-                uint32_t sc_cur[4], sc_nxt[4];
-                int cur = tile_at(split);
-                scales(cur, sc_cur);
-                int nxt = tile_at(n_split + atomicAdd(&ctr[0], 1));
-                scales(nxt, sc_nxt);
-                int k_nn = atomicAdd(&ctr[0], 1);
-                uint8_t *owner = sy.owner + (size_t)gz * n_tiles_all;
-                const uint64_t pol = l2_evict_first_policy();
-                int ke = 0;             // K ring entries used
-                int vn = 0;             // V ring entries used
-                int k_tma = -1, v_tma = -1;   // last entries that were TMA loads
-                bool ok = true;
-                auto issue_v = [&](int t) {
-                    const int s = t % SV;
-                    if (t >= SV && !wait_bounded(smem_addr(&bar->empty_v[s]), ((t / SV) & 1) ^ 1,
-                                                 abort, hdr))
-                        return false;
-                    const uint32_t fb = smem_addr(&bar->full_v[s]);
-                    const int tile = bar->tile_of[t % kTileRing];
-                    if (tile < 0 || tile >= nq) {
-                        mbar_arrive(fb);   // the end, or a tail tile: the converters take it
-                    } else {
-                        mbar_arrive_expect_tx(fb, kRawBytes);
-                        tma_load_3d_hint(smem_addr(sV + s * kRawBytes), &tmap_v, 0, tile * kTileN,
-                                         g, fb, pol);
-                        v_tma = t;
-                    }
-                    return true;
-                };
-                for (int i = 0; ok; ++i) {
-                    const int tile = cur < 0 ? -1 : cur;
+            // Tiles are taken from the end of the cache backwards, four per
+            // claim: lanes 0-3 hold a round's tiles and their scale bytes while
+            // lane 0 issues them, and the next round's claim is on its way.
+            // (Claimed and looked up one by one, the two trips to memory came to
+            // 3600 cycles a tile, more than twice the tile's stream.)
+            constexpr int kRound = 4;
+            auto tile_at = [&](int k) { return n_tiles_all - 1 - k; };
+            int32_t *ctr = sy.sync + 4 * gz;
+            const uint8_t *ksc = kc.k_scale + (int64_t)g * (kc.q8_cap / kQ8Block);
+            const uint8_t *vsc = kc.v_scale + (int64_t)g * (kc.q8_cap / kQ8Block);
+            const int n_blk = kc.n_q8 / kQ8Block;
+            // scale bytes of a tile's two blocks (127, a factor of one, past the
+            // last block and on a tail tile): k, k, v, v
+            auto scales = [&](int tile) {
+                const int b0 = 2 * tile;
+                uint32_t w = 0x7F7F7F7Fu;
+                if (lane < kRound && tile >= 0 && b0 < n_blk) {
+                    const bool two = b0 + 1 < n_blk;
+                    w = __ldg(ksc + b0) | ((two ? (uint32_t)__ldg(ksc + b0 + 1) : 127u) << 8) |
+                        ((uint32_t)__ldg(vsc + b0) << 16) |
+                        ((two ? (uint32_t)__ldg(vsc + b0 + 1) : 127u) << 24);
+                }
+                return w;
+            };
+            auto claim = [&](int n) { return lane == 0 ? atomicAdd(&ctr[0], n) : 0; };
+            // the split's own tile is the first; the round's others are claimed
+            int base = claim(kRound - 1);
+            const int first = __shfl_sync(0xffffffffu, base, 0);
+            int my_tile = lane == 0 ? tile_at(split) : tile_at(n_split + first + lane - 1);
+            uint32_t my_sc = scales(my_tile);
+            base = claim(kRound);
+            uint8_t *owner = sy.owner + (size_t)gz * n_tiles_all;
+            const uint64_t pol = l2_evict_first_policy();
+            int ke = 0;             // K ring entries used
+            int vn = 0;             // V ring entries used
+            int k_tma = -1, v_tma = -1;   // last entries that were TMA loads
+            bool ok = true, more = true;
+            auto issue_v = [&](int t) {
+                const int s = t % SV;
+                if (t >= SV && !wait_bounded(smem_addr(&bar->empty_v[s]), ((t / SV) & 1) ^ 1, abort, hdr))
+                    return false;
+                const uint32_t fb = smem_addr(&bar->full_v[s]);
+                const int tile = bar->tile_of[t % kTileRing];
+                if (tile >= nq) {
+                    mbar_arrive(fb);   // a tail tile: the softmax warps read it themselves
+                } else {
+                    mbar_arrive_expect_tx(fb, kRawBytes);
+                    tma_load_3d_hint(smem_addr(sV + s * kRawBytes), &tmap_v, 0, tile * kTileN, g, fb, pol);
+                    v_tma = t;
+                }
+                return true;
+            };
+            for (int i = 0; ok && more; ++i) {
+                const int tile = max(-1, __shfl_sync(0xffffffffu, my_tile, i % kRound));
+                const uint32_t sc = __shfl_sync(0xffffffffu, my_sc, i % kRound);
+                if (lane == 0) {
                     const bool tail = tile >= nq;
                     bar->tile_of[i % kTileRing] = tile;
                     if (tile < 0)   // every group's end
                         bar->tile_of[(i + 1) % kTileRing] = bar->tile_of[(i + 2) % kTileRing] = -1;
+                    else
+                        owner[tile] = (uint8_t)split;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const float kf = q8_factor(sc_cur[h]);
-                        const uint32_t vb = sc_cur[h] == 255u ? 255u : sc_cur[2 + h];
-                        aux->scale_of[i % kTileRing][h] = make_float4(kf, q8_log2(vb), q8_inverse(vb), 0.f);
+                        const uint32_t kb = (sc >> (8 * h)) & 0xFFu;
+                        const uint32_t vb = kb == 255u ? 255u : (sc >> (16 + 8 * h)) & 0xFFu;
+                        aux->scale_of[i % kTileRing][h] =
+                            make_float4(q8_factor(kb), q8_log2(vb), q8_inverse(vb), 0.f);
                     }
                     bar->entry_of[i % kTileRing] = ke;
-                    if (tile >= 0)
-                        owner[tile] = (uint8_t)split;
-                    for (int part = 0; part < (tail ? 2 : 1) && ok; ++part, ++ke) {
+                    for (int part = 0; part < (tail ? 2 : 1); ++part, ++ke) {
                         const int s = ke % SK;
-                        if (ke >= SK && !wait_bounded(smem_addr(&bar->empty_k[s]),
-                                                      ((ke / SK) & 1) ^ 1, abort, hdr)) {
+                        if (ke >= SK && !wait_bounded(smem_addr(&bar->empty_k[s]), ((ke / SK) & 1) ^ 1,
+                                                      abort, hdr)) {
                             ok = false;
                             break;
                         }
@@ -758,34 +842,31 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                             mbar_arrive(fb);   // no tile left: the QK issuer passes it on
                         } else if (!tail) {
                             mbar_arrive_expect_tx(fb, kRawBytes);
-                            tma_load_3d_hint(smem_addr(sK + s * kRawBytes), &tmap_k, 0,
-                                             tile * kTileN, g, fb, pol);
+                            tma_load_3d_hint(smem_addr(sK + s * kRawBytes), &tmap_k, 0, tile * kTileN, g,
+                                             fb, pol);
                             k_tma = ke;
-                        }   // a tail tile's slots are filled by the converters
+                        }   // a tail tile's slots, free now, are filled by the softmax warps
                     }
-                    if (!ok)
-                        break;
-                    cur = nxt;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        sc_cur[e] = sc_nxt[e];
-                    nxt = tile_at(n_split + k_nn);
-                    scales(nxt, sc_nxt);
-                    if (nxt >= 0)
-                        k_nn = atomicAdd(&ctr[0], 1);
-                    // V one tile behind K; a tail tile's (and the end) at once
-                    while (ok && (vn < i || (vn == i && (tail || tile < 0))))
+                    for (int j = 0; j < (tile < 0 ? 3 : 1); ++j)
+                        mbar_arrive(smem_addr(&bar->info[(i + j) % kTileRing]));
+                    if (ok && vn < i)   // V one tile behind K
                         ok = issue_v(vn++);
-                    if (tile < 0)
-                        break;
                 }
-                if (*abort) {
-                    // our own copies land before the CTA exits
-                    for (int t = max(0, k_tma - SK + 1); t <= k_tma; ++t)
-                        wait_drain(smem_addr(&bar->full_k[t % SK]), (t / SK) & 1);
-                    for (int t = max(0, v_tma - SV + 1); t <= v_tma; ++t)
-                        wait_drain(smem_addr(&bar->full_v[t % SV]), (t / SV) & 1);
+                ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+                more = tile >= 0;
+                if (i % kRound == kRound - 1) {
+                    my_tile = tile_at(n_split + __shfl_sync(0xffffffffu, base, 0) + lane);
+                    my_sc = scales(my_tile);
+                    if (more)
+                        base = claim(kRound);
                 }
+            }
+            if (lane == 0 && *abort) {
+                // our own copies land before the CTA exits
+                for (int t = max(0, k_tma - SK + 1); t <= k_tma; ++t)
+                    wait_drain(smem_addr(&bar->full_k[t % SK]), (t / SK) & 1);
+                for (int t = max(0, v_tma - SV + 1); t <= v_tma; ++t)
+                    wait_drain(smem_addr(&bar->full_v[t % SV]), (t / SV) & 1);
             }
         } else if (warp == 0) {
             // ------------------------------------ root node's scores out of S
@@ -919,7 +1000,7 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
             const uint32_t p_half = (uint32_t)r_pad * 128;
             for (int t = 0;; ++t) {
                 const int s = t % SVB;
-                if (!wait_bounded(smem_addr(&bar->vb_full[s]), (t / SVB) & 1, abort, hdr))
+                if (!wait_bounded(smem_addr(&bar->info[t % kTileRing]), (t / kTileRing) & 1, abort, hdr))
                     break;
                 if (bar->tile_of[t % kTileRing] < 0) {
                     mma_commit(smem_addr(&bar->o_final));   // after the last PV
@@ -945,126 +1026,6 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
             }
             mma_commit(smem_addr(&bar->drain[1]));
             wait_drain(smem_addr(&bar->drain[1]), 0);
-        }
-    } else if (warp >= 16) {
-        // ------------------------------------------------ converters
-        const int tid = threadIdx.x - 512;   // 0..127
-        int met = 0;                         // meetings of the converter warps so far
-        for (int t = 0;; ++t) {
-            const int s = t % SV;
-            if (!warp_wait_bounded(smem_addr(&bar->full_v[s]), (t / SV) & 1, abort, hdr))
-                break;
-            const int tile = bar->tile_of[t % kTileRing];
-            if (tile < 0) {
-                // the PV issuer's end, once it is past the slot's last tile (two
-                // phases at once would pass it by)
-                if (t >= SVB && !warp_wait_bounded(smem_addr(&bar->pv_done[(t - SVB) % NP]),
-                                                   ((t - SVB) / NP) & 1, abort, hdr))
-                    break;
-                if (lane == 0)
-                    mbar_arrive(smem_addr(&bar->vb_full[t % SVB]));
-                break;
-            }
-            unsigned char *vb = sVb + (t % SVB) * kVbBytes;
-            const __nv_bfloat16 *vrow = nullptr;
-            if (tile >= nq) {
-                // a tail tile, one row per thread: keys into two K slots
-                const int row = (tile - nq) * kTileN + tid;
-                const int64_t at = ((int64_t)g * kc.tail_cap + row) * kD;
-                const bool have = row < tail_rows;
-                const uint4 *kr = reinterpret_cast<const uint4 *>(kc.k_tail + at);
-                const uint4 *vr = reinterpret_cast<const uint4 *>(kc.v_tail + at);
-                uint32_t tk = 0, tv = 0;
-                if (have) {
-#pragma unroll 4
-                    for (int c = 0; c < kD / 8; ++c) {
-                        tk = __vmaxu2(tk, top_word(__ldg(kr + c)));
-                        tv = __vmaxu2(tv, top_word(__ldg(vr + c)));
-                    }
-                }
-                tk = top_of(tk);
-                tv = top_of(tv);
-                const bool bad_k = tk >= 0x7F80u, bad = bad_k || tv >= 0x7F80u;
-                const uint32_t wk = __ballot_sync(0xffffffffu, bad_k), wb = __ballot_sync(0xffffffffu, bad);
-                const uint32_t wtop = __reduce_max_sync(0xffffffffu, bad ? 0u : tk);
-                if (lane == 0) {
-                    bar->bad_k[t & 3][warp - 16] = wk;
-                    bar->bad[t & 3][warp - 16] = wb;
-                    bar->top[warp - 16] = wtop;
-                    mbar_arrive(smem_addr(&bar->conv));
-                }
-                if (!warp_wait_bounded(smem_addr(&bar->conv), met++ & 1, abort, hdr))
-                    break;
-                // a block's two warps share its scale
-                const int w2 = (warp - 16) & 2;
-                const uint32_t top = max(*(volatile uint32_t *)&bar->top[w2],
-                                         *(volatile uint32_t *)&bar->top[w2 + 1]);
-                const int e = split_exp(top);
-                if (tid == 0) {
-                    const int e1 = split_exp(max(*(volatile uint32_t *)&bar->top[2],
-                                                 *(volatile uint32_t *)&bar->top[3]));
-                    aux->scale_of[t % kTileRing][0].x = two_to(e);
-                    aux->scale_of[t % kTileRing][1].x = two_to(e1);
-                }
-                const int e0 = bar->entry_of[t % kTileRing];
-                unsigned char *khi = sK + (e0 % SK) * kRawBytes, *klo = sK + ((e0 + 1) % SK) * kRawBytes;
-                const float f = two_to(-e);
-#pragma unroll 2
-                for (int c = 0; c < kD / 16; ++c) {   // 16 codes a step
-                    uint4 hi = make_uint4(0u, 0u, 0u, 0u), lo = hi;
-                    if (have && !bad) {
-                        uint2 h0, l0, h1, l1;
-                        split_16b(__ldg(kr + 2 * c), f, h0, l0);
-                        split_16b(__ldg(kr + 2 * c + 1), f, h1, l1);
-                        hi = make_uint4(h0.x, h0.y, h1.x, h1.y);
-                        lo = make_uint4(l0.x, l0.y, l1.x, l1.y);
-                    }
-                    const int off = tid * 128 + ((c ^ (tid & 7)) << 4);
-                    *reinterpret_cast<uint4 *>(khi + off) = hi;
-                    *reinterpret_cast<uint4 *>(klo + off) = lo;
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(smem_addr(&bar->conv));
-                if (!warp_wait_bounded(smem_addr(&bar->conv), met++ & 1, abort, hdr))
-                    break;
-                if (tid == 0) {
-                    mbar_arrive(smem_addr(&bar->full_k[e0 % SK]));
-                    mbar_arrive(smem_addr(&bar->full_k[(e0 + 1) % SK]));
-                }
-                vrow = have && !bad ? kc.v_tail + at : nullptr;
-            }
-            // the bf16 slot is free once PV of the tile before it in it is done
-            if (t >= SVB && !warp_wait_bounded(smem_addr(&bar->pv_done[(t - SVB) % NP]),
-                                               ((t - SVB) / NP) & 1, abort, hdr))
-                break;
-            if (tile < nq) {
-                // 8 codes per thread and step: a thread keeps its column chunk
-                // and its row mod 8, so every address is an offset of two bases
-                const int ch = tid & 15, r8 = tid >> 4;
-                const unsigned char *src = sV + s * kRawBytes + 8 * tid;
-                unsigned char *dst = vb + (ch >> 3) * kBoxBytes + r8 * 128 + (((ch & 7) ^ r8) << 4);
-#pragma unroll 4
-                for (int i = 0; i < kTileN / 8; ++i) {
-                    const uint2 w = *reinterpret_cast<const uint2 *>(src + i * 8 * kD);
-                    const uint2 x = codes_to_bf16(w.x), y = codes_to_bf16(w.y);
-                    *reinterpret_cast<uint4 *>(dst + i * 1024) = make_uint4(x.x, x.y, y.x, y.y);
-                }
-            } else {
-#pragma unroll 4
-                for (int c = 0; c < kD / 8; ++c)
-                    *reinterpret_cast<uint4 *>(vb + (c >> 3) * kBoxBytes + tid * 128 +
-                                               (((c & 7) ^ (tid & 7)) << 4)) =
-                        vrow ? __ldg(reinterpret_cast<const uint4 *>(vrow) + c)
-                             : make_uint4(0u, 0u, 0u, 0u);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(smem_addr(&bar->vb_full[t % SVB]));
-                mbar_arrive(smem_addr(&bar->empty_v[s]));
-            }
         }
     } else {
         // ---- query rows of this KV head: row n = node * G + (head - g*G),
@@ -1124,7 +1085,7 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
             named_bar_arrive(kBarQLoads, kQLoadThreads);   // one block: no rows to load
         }
         tc_fence_before();
-        named_bar_sync(kBarQuery, kThreads - 32 * (1 + kConvWarps));
+        named_bar_sync(kBarQuery, kThreads - 32);
         tc_fence_after();
         if ((warp - 4) / 4 < U * NG) {
             // ------------------------------------------------ softmax
@@ -1164,7 +1125,28 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
             float lA = rsA == rsA ? 0.f : rsA, lB = rsB == rsB ? 0.f : rsB;
             bool fresh = true;   // some row has no reference yet (uniform)
             bool ok = true;
-            for (int t = grp; hasA; t += NG) {
+            // this thread's share of V's codes: a column chunk and every
+            // (threads / 16)-th row, all with the same row mod 8
+            const int n_thr = NG == 3 ? 128 : 128 * U, tid = NG == 3 ? threadIdx.x & 127 : threadIdx.x - 128;
+            const int cch = tid & 15, cr0 = tid >> 4, crs = n_thr >> 4;
+            const uint32_t c_src = (uint32_t)(8 * tid);
+            const uint32_t c_dst = (uint32_t)((cch >> 3) * kBoxBytes + cr0 * 128 + (((cch & 7) ^ (cr0 & 7)) << 4));
+            bool first_q8 = true;   // tail tiles, if any, come first
+            int met = 0;            // meetings of this warpgroup over tail tiles
+            for (int t = grp;; t += NG) {
+                unsigned char *vb = sVb + (t % SVB) * kVbBytes;
+                if (first_q8) {
+                    if (!warp_wait_bounded(smem_addr(&bar->info[t % kTileRing]), (t / kTileRing) & 1, abort, hdr)) {
+                        ok = false;
+                        break;
+                    }
+                    first_q8 = bar->tile_of[t % kTileRing] >= nq;
+                    if (first_q8 && (NG == 3 || warp < 8) &&
+                        !tail_keys(a, aux, sK, SK, g, nq, t, grp, met, abort, hdr)) {
+                        ok = false;
+                        break;
+                    }
+                }
                 const int slot = NB == 2 ? b : (t & 1), sb = NB == 2 ? b : t % SI;
                 if (!warp_wait_bounded(smem_addr(&bar->s_full[sb]), (t / SI) & 1, abort, hdr)) {
                     ok = false;
@@ -1178,11 +1160,16 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 int left = tail ? kc.n_tail - (tile - nq) * kTileN : kc.n_q8 - tile * kTileN;
                 const float4 *scl = aux->scale_of[t % kTileRing];
                 const int ps = t % NP;
+                if (!hasA) {   // no rows: only V, below
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(smem_addr(&bar->s_free[sb]));
+                }
                 uint32_t atA = p_rowA + 2 * ps * p_stepA, atB = p_rowB + 2 * ps * p_stepB;
                 // the halves are the tile's two scale blocks; one copy of the code
                 // serves both (the loop must stay inside the instruction cache)
 #pragma unroll 1
-                for (int h = 0; h < 2; ++h, left -= 64) {
+                for (int h = hasA ? 0 : 2; h < 2; ++h, left -= 64) {
                     tc_fence_after();
                     uint32_t r[32];
                     tmem_ld16x256_x8(s_addr + 128 * slot + 64 * h, r);
@@ -1252,10 +1239,34 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 }
                 if (!ok)
                     break;
+                // ---- V of this tile to bf16, once PV of the tile before it in
+                // the slot is done
+                if (!warp_wait_bounded(smem_addr(&bar->full_v[t % SV]), (t / SV) & 1, abort, hdr) ||
+                    (t >= SVB && !warp_wait_bounded(smem_addr(&bar->pv_done[(t - SVB) % NP]),
+                                                    ((t - SVB) / NP) & 1, abort, hdr))) {
+                    ok = false;
+                    break;
+                }
+                if (!tail) {
+                    const unsigned char *src = sV + (t % SV) * kRawBytes + c_src;
+                    unsigned char *dst = vb + c_dst;
+#pragma unroll 2
+                    for (int r = cr0; r < kTileN; r += crs) {
+                        const uint2 w = *reinterpret_cast<const uint2 *>(src);
+                        const uint2 x = codes_to_bf16(w.x), y = codes_to_bf16(w.y);
+                        *reinterpret_cast<uint4 *>(dst) = make_uint4(x.x, x.y, y.x, y.y);
+                        src += crs * kD;
+                        dst += crs * 128;
+                    }
+                } else if (NG == 3 || warp < 8) {
+                    tail_values(a, bar, vb, g, nq, tile, t);
+                }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0)
+                if (lane == 0) {
+                    mbar_arrive(smem_addr(&bar->empty_v[t % SV]));
                     mbar_arrive(smem_addr(&bar->sm_done[ps]));
+                }
             }
             // ---- (m, l) of each row (four threads' partial sums), then O^T
 #pragma unroll
@@ -1270,17 +1281,25 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 bar->overflow = 1;
             const int rows_all = a.n_tree * a.n_heads_q;
             float *ws_o = sy.part;
-            float2 *ws_ml = reinterpret_cast<float2 *>(ws_o + (size_t)n_split * NG * rows_all * kD);
-            const size_t part_row = ((size_t)split * NG + grp) * rows_all;
+            float2 *ws_ml = reinterpret_cast<float2 *>(ws_o + (size_t)n_split * rows_all * kD);
+            const size_t part_row = (size_t)split * rows_all;
             auto orow_of = [&](int n) {
                 const int m = q8_row_of(n, R);
                 return (node0 + m / G) * a.n_heads_q + g * G + m % G;
             };
             if (ok && (lane & 3) == 0) {
-                if (vA)
-                    ws_ml[part_row + orow_of(nA)] = make_float2(mA, lA);
-                if (vB)
-                    ws_ml[part_row + orow_of(nB)] = make_float2(mB, lB);
+                if (vA) {
+                    if (NG == 3)
+                        aux->ml[grp][nA] = make_float2(mA, lA);
+                    else
+                        ws_ml[part_row + orow_of(nA)] = make_float2(mA, lA);
+                }
+                if (vB) {
+                    if (NG == 3)
+                        aux->ml[grp][nB] = make_float2(mB, lB);
+                    else
+                        ws_ml[part_row + orow_of(nB)] = make_float2(mB, lB);
+                }
             }
             // O^T out of TMEM into shared memory in output order, from the P^T
             // tiles on (all of it is free after the last PV; one group's rows
@@ -1302,11 +1321,35 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
             }
             fence_proxy_async_smem();
             named_bar_sync(kBarOut, 128 * U * NG);   // every softmax warp, whatever its path
+            if (NG == 3) {
+                // the groups' partials into one (all of a row's by one warp)
+                for (int r = warp - 4; r < R && !*abort; r += 12) {
+                    const float2 p0 = aux->ml[0][r], p1 = aux->ml[1][r], p2 = aux->ml[2][r];
+                    const float M = max3f(p0.x, p1.x, p2.x);
+                    // a group that saw nothing (m = -inf) has l = 0, or NaN, and any O
+                    const float w0 = p0.x == -INFINITY ? 0.f : exp2f(p0.x - M);
+                    const float w1 = p1.x == -INFINITY ? 0.f : exp2f(p1.x - M);
+                    const float w2 = p2.x == -INFINITY ? 0.f : exp2f(p2.x - M);
+                    float4 *o = reinterpret_cast<float4 *>(sP) + r * (kD / 4) + lane;
+                    float4 x = w0 != 0.f ? *o : make_float4(0.f, 0.f, 0.f, 0.f);
+                    const float4 y = w1 != 0.f ? o[R * (kD / 4)] : make_float4(0.f, 0.f, 0.f, 0.f);
+                    const float4 z = w2 != 0.f ? o[2 * R * (kD / 4)] : make_float4(0.f, 0.f, 0.f, 0.f);
+                    x.x = w0 * x.x + w1 * y.x + w2 * z.x;
+                    x.y = w0 * x.y + w1 * y.y + w2 * z.y;
+                    x.z = w0 * x.z + w1 * y.z + w2 * z.z;
+                    x.w = w0 * x.w + w1 * y.w + w2 * z.w;
+                    *o = x;
+                    if (lane == 0)
+                        ws_ml[part_row + orow_of(r)] = make_float2(M, w0 * p0.y + w1 * p1.y + w2 * p2.y);
+                }
+                fence_proxy_async_smem();
+                named_bar_sync(kBarOut, 128 * U * NG);
+            }
             if (!*abort && lane == 0) {
-                const int sw = 4 * j + q;   // 0 .. 4U-1
-                for (int node = sw; node < T; node += 4 * U)
+                const int sw = warp - 4, n_sw = 4 * U * NG;
+                for (int node = sw; node < T; node += n_sw)
                     bulk_store(ws_o + (part_row + (size_t)(node0 + node) * a.n_heads_q + g * G) * kD,
-                               smem_addr(stage) + (uint32_t)(node * G * kD * 4), (uint32_t)(G * kD * 4));
+                               smem_addr(sP) + (uint32_t)(node * G * kD * 4), (uint32_t)(G * kD * 4));
                 bulk_commit();
                 bulk_wait_all();
                 fence_proxy_async_global();
@@ -1335,7 +1378,7 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
     if (!*abort) {
         for (int m = split + warp * n_split; m < R; m += (kThreads / 32) * n_split)
             combine_row(a, masks, (node0 + m / G) * a.n_heads_q + g * G + m % G, g, gz, n_gz,
-                        n_split, NG, nq, n_tiles_all, sy);
+                        n_split, nq, n_tiles_all, sy);
     }
     __syncthreads();
     if (threadIdx.x == 0 && atomicAdd(&ctr[2], 1) == n_split - 1) {
@@ -1368,7 +1411,7 @@ T128Plan q8_plan(int n_heads_q, int n_heads_kv, int n_q8, int n_tail, int n_tree
     const size_t n_gz = (size_t)n_heads_kv * p.node_groups;
     p.part = kHeaderBytes + kQ8SyncBytes;
     p.groups = q8_groups(p.nodes_per_group * G);
-    p.flags = p.part + align_up((size_t)p.n_split * p.groups * n_tree * n_heads_q * (kD + 2) * sizeof(float), 256);
+    p.flags = p.part + align_up((size_t)p.n_split * n_tree * n_heads_q * (kD + 2) * sizeof(float), 256);
     p.owner = p.flags + align_up((size_t)p.n_split * n_gz * sizeof(int32_t), 256);
     p.total = p.owner + align_up(n_gz * n_tiles, 256);
     return p;
