@@ -81,6 +81,7 @@ constexpr size_t kSmemLimit = 232448;        // dynamic shared memory per CTA
 constexpr int kBarQuery = 1;                 // named barrier: query rows in place
 constexpr int kBarOut = 2;                   // named barrier: O^T staged, or merged, in shared memory
 constexpr int kTileRing = 16;                // entries of the tile rings (> any role's lead)
+static_assert(kTileRing == 1 << 4, "indexed by shifts");
 constexpr int kBarQLoads = 3;                // named barrier: the query rows are read
 constexpr int kQLoadThreads = 32 * 9;        // warps 4-11 arrive, the producer warp waits
 constexpr int kMaxGz = 256;                  // (KV head, node group) pairs: counters in the workspace
@@ -99,7 +100,7 @@ struct Bars {
     uint64_t drain[2];
     uint64_t conv[3];               // a warpgroup that turns a tail tile meets
     uint64_t info[kTileRing];       // tile_of, scale_of of that tile are written
-    // per tile, at [t % kTileRing]: its index (-1 after the last) and its
+    // per tile, at [t & (kTileRing - 1)]: its index (-1 after the last) and its
     // first K ring entry.  Written by the producer before the arrival that
     // the readers wait for.
     volatile int32_t tile_of[kTileRing];
@@ -167,37 +168,35 @@ constexpr uint32_t idesc_f8(int m, int n, int a5, int b5)
            ((uint32_t)(m >> 4) << 24);
 }
 
-__device__ __forceinline__ void mma8_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc)
+// tcgen05.mma with shared-memory descriptors given by their low words; the
+// high words are the same for every operand here (swizzle, version, 1024-byte
+// groups).  KIND 0: f8f6f4, 1: f16.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+template <int KIND>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc)
 {
-    asm volatile(
-        "{\n"
-        " .reg .pred p;\n"
-        " setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n"
-        "}\n" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
-        : "memory");
+    if (KIND == 0)
+        asm volatile(
+            "{\n .reg .pred p;\n .reg .b64 x, y;\n mov.b64 x, {%1, %5};\n mov.b64 y, {%2, %5};\n"
+            " setp.ne.b32 p, %4, 0;\n"
+            " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, p;\n}\n" ::"r"(d), "r"(a), "r"(b),
+            "r"(idesc), "r"(acc), "r"(kDescHi)
+            : "memory");
+    else
+        asm volatile(
+            "{\n .reg .pred p;\n .reg .b64 x, y;\n mov.b64 x, {%1, %5};\n mov.b64 y, {%2, %5};\n"
+            " setp.ne.b32 p, %4, 0;\n"
+            " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}\n" ::"r"(d), "r"(a), "r"(b),
+            "r"(idesc), "r"(acc), "r"(kDescHi)
+            : "memory");
 }
-
-__device__ __forceinline__ void mma16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc)
+__device__ __forceinline__ void mma8_ts(uint32_t d, uint32_t a_tmem, uint32_t b, uint32_t idesc,
+                                        uint32_t acc)
 {
     asm volatile(
-        "{\n"
-        " .reg .pred p;\n"
-        " setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
-        "}\n" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
-        : "memory");
-}
-
-__device__ __forceinline__ void mma8_ts(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc,
-                                        bool acc)
-{
-    asm volatile(
-        "{\n"
-        " .reg .pred p;\n"
-        " setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n"
-        "}\n" ::"r"(d), "r"(a_tmem), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+        "{\n .reg .pred p;\n .reg .b64 y;\n mov.b64 y, {%2, %5};\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], y, %3, p;\n}\n" ::"r"(d), "r"(a_tmem), "r"(b),
+        "r"(idesc), "r"(acc), "r"(kDescHi)
         : "memory");
 }
 
@@ -228,6 +227,42 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
         "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
         "r"(r[15])
         : "memory");
+}
+
+// A place in a ring of n slots and its phase, advanced by counting: the
+// quotients t / n and t % n by a run-time n, several per tile and warp, cost
+// more instructions than the softmax.
+struct Ring {
+    int n, i;
+    uint32_t ph;
+    __device__ __forceinline__ explicit Ring(int slots) : n(slots), i(0), ph(0) {}
+    __device__ __forceinline__ void next()
+    {
+        if (++i == n) {
+            i = 0;
+            ph ^= 1u;
+        }
+    }
+};
+
+// sm100's bounded waits with a uniform fast path: one try, one vote, no
+// divergent branch (a satisfied wait is taken several times per tile).
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile uint32_t *abort,
+                                       WorkspaceHeader *ws)
+{
+    return wait_bounded(bar, parity, abort, ws);
+}
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile uint32_t *abort,
+                                          WorkspaceHeader *ws)
+{
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
+        return true;
+    return __all_sync(0xffffffffu, wait_slow(bar, parity, abort, ws));
+}
+__device__ __forceinline__ bool lane_wait(uint32_t bar, uint32_t parity, volatile uint32_t *abort,
+                                          WorkspaceHeader *ws)
+{
+    return mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort, ws);
 }
 
 // Four values (times f) as e4m3 codes, and what that leaves as e5m2 codes.
@@ -575,7 +610,7 @@ __device__ __noinline__ bool tail_keys(const AttnQ8Args &a, Aux *aux, unsigned c
     Bars *bar = &aux->bar;
     const Q8Cache &kc = a.c;
     const int tid = threadIdx.x & 127, lane = threadIdx.x & 31, w = tid >> 5;
-    const int row = (bar->tile_of[t % kTileRing] - nq) * kTileN + tid;
+    const int row = (bar->tile_of[t & (kTileRing - 1)] - nq) * kTileN + tid;
     const bool have = row < kc.n_tail + a.n_tree;
     const int64_t at = ((int64_t)g * kc.tail_cap + row) * kD;
     const uint4 *kr = reinterpret_cast<const uint4 *>(kc.k_tail + at);
@@ -599,15 +634,15 @@ __device__ __noinline__ bool tail_keys(const AttnQ8Args &a, Aux *aux, unsigned c
         bar->top[grp][w] = wtop;
         mbar_arrive(smem_addr(&bar->conv[grp]));
     }
-    if (!warp_wait_bounded(smem_addr(&bar->conv[grp]), met++ & 1, abort, hdr))
+    if (!warp_wait(smem_addr(&bar->conv[grp]), met++ & 1, abort, hdr))
         return false;
     volatile uint32_t *top = bar->top[grp];
     const int e = split_exp(max(top[w & 2], top[(w & 2) + 1]));
     if (tid == 0) {
-        aux->scale_of[t % kTileRing][0].x = two_to(e);
-        aux->scale_of[t % kTileRing][1].x = two_to(split_exp(max(top[2], top[3])));
+        aux->scale_of[t & (kTileRing - 1)][0].x = two_to(e);
+        aux->scale_of[t & (kTileRing - 1)][1].x = two_to(split_exp(max(top[2], top[3])));
     }
-    const int e0 = bar->entry_of[t % kTileRing];
+    const int e0 = bar->entry_of[t & (kTileRing - 1)];
     unsigned char *khi = sK + (e0 % SK) * kRawBytes, *klo = sK + ((e0 + 1) % SK) * kRawBytes;
     const float f = two_to(-e);
 #pragma unroll 2
@@ -628,7 +663,7 @@ __device__ __noinline__ bool tail_keys(const AttnQ8Args &a, Aux *aux, unsigned c
     __syncwarp();
     if (lane == 0)
         mbar_arrive(smem_addr(&bar->conv[grp]));
-    if (!warp_wait_bounded(smem_addr(&bar->conv[grp]), met++ & 1, abort, hdr))
+    if (!warp_wait(smem_addr(&bar->conv[grp]), met++ & 1, abort, hdr))
         return false;
     if (tid == 0) {
         mbar_arrive(smem_addr(&bar->full_k[e0 % SK]));
@@ -793,16 +828,18 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
             base = claim(kRound);
             uint8_t *owner = sy.owner + (size_t)gz * n_tiles_all;
             const uint64_t pol = l2_evict_first_policy();
+            Ring rk(SK), rv(SV);
             int ke = 0;             // K ring entries used
             int vn = 0;             // V ring entries used
             int k_tma = -1, v_tma = -1;   // last entries that were TMA loads
             bool ok = true, more = true;
             auto issue_v = [&](int t) {
-                const int s = t % SV;
-                if (t >= SV && !wait_bounded(smem_addr(&bar->empty_v[s]), ((t / SV) & 1) ^ 1, abort, hdr))
+                const int s = rv.i;
+                if (t >= SV && !lane_wait(smem_addr(&bar->empty_v[s]), rv.ph ^ 1, abort, hdr))
                     return false;
+                rv.next();
                 const uint32_t fb = smem_addr(&bar->full_v[s]);
-                const int tile = bar->tile_of[t % kTileRing];
+                const int tile = bar->tile_of[t & (kTileRing - 1)];
                 if (tile >= nq) {
                     mbar_arrive(fb);   // a tail tile: the softmax warps read it themselves
                 } else {
@@ -817,23 +854,22 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 const uint32_t sc = __shfl_sync(0xffffffffu, my_sc, i % kRound);
                 if (lane == 0) {
                     const bool tail = tile >= nq;
-                    bar->tile_of[i % kTileRing] = tile;
+                    bar->tile_of[i & (kTileRing - 1)] = tile;
                     if (tile < 0)   // every group's end
-                        bar->tile_of[(i + 1) % kTileRing] = bar->tile_of[(i + 2) % kTileRing] = -1;
+                        bar->tile_of[(i + 1) & (kTileRing - 1)] = bar->tile_of[(i + 2) & (kTileRing - 1)] = -1;
                     else
                         owner[tile] = (uint8_t)split;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const uint32_t kb = (sc >> (8 * h)) & 0xFFu;
                         const uint32_t vb = kb == 255u ? 255u : (sc >> (16 + 8 * h)) & 0xFFu;
-                        aux->scale_of[i % kTileRing][h] =
+                        aux->scale_of[i & (kTileRing - 1)][h] =
                             make_float4(q8_factor(kb), q8_log2(vb), q8_inverse(vb), 0.f);
                     }
-                    bar->entry_of[i % kTileRing] = ke;
-                    for (int part = 0; part < (tail ? 2 : 1); ++part, ++ke) {
-                        const int s = ke % SK;
-                        if (ke >= SK && !wait_bounded(smem_addr(&bar->empty_k[s]), ((ke / SK) & 1) ^ 1,
-                                                      abort, hdr)) {
+                    bar->entry_of[i & (kTileRing - 1)] = ke;
+                    for (int part = 0; part < (tail ? 2 : 1); ++part, ++ke, rk.next()) {
+                        const int s = rk.i;
+                        if (ke >= SK && !lane_wait(smem_addr(&bar->empty_k[s]), rk.ph ^ 1, abort, hdr)) {
                             ok = false;
                             break;
                         }
@@ -848,7 +884,7 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                         }   // a tail tile's slots, free now, are filled by the softmax warps
                     }
                     for (int j = 0; j < (tile < 0 ? 3 : 1); ++j)
-                        mbar_arrive(smem_addr(&bar->info[(i + j) % kTileRing]));
+                        mbar_arrive(smem_addr(&bar->info[(i + j) & (kTileRing - 1)]));
                     if (ok && vn < i)   // V one tile behind K
                         ok = issue_v(vn++);
                 }
@@ -877,11 +913,12 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 const float rsc = aux->row_scale[NB == 2 ? kBlockM + (mine ? r : 0) : (mine ? r : 0)];
                 float *dst_row = a.root_scores + (size_t)(g * G + (mine ? r : 0)) * n_ctx;
                 const bool vec = ((reinterpret_cast<uintptr_t>(a.root_scores) | (uintptr_t)n_ctx * 4) & 7) == 0;
-                for (int t = 0;; ++t) {
-                    const int slot = NB == 2 ? 1 : (t & 1), sb = NB == 2 ? 1 : t % SI;
-                    if (!warp_wait_bounded(smem_addr(&bar->s_full[sb]), (t / SI) & 1, abort, hdr))
+                Ring rs(SI);
+                for (int t = 0;; ++t, rs.next()) {
+                    const int slot = NB == 2 ? 1 : (t & 1), sb = NB == 2 ? 1 : rs.i;
+                    if (!warp_wait(smem_addr(&bar->s_full[sb]), rs.ph, abort, hdr))
                         break;
-                    const int tile = bar->tile_of[t % kTileRing];
+                    const int tile = bar->tile_of[t & (kTileRing - 1)];
                     if (tile < 0)
                         break;
                     tc_fence_after();
@@ -897,7 +934,7 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                         uint32_t rr[32];
                         tmem_ld16x256_x8(tmem + kSCol + 128 * slot + 64 * h, rr);
                         if (mine) {
-                            const float f = rsc * aux->scale_of[t % kTileRing][h].x;
+                            const float f = rsc * aux->scale_of[t & (kTileRing - 1)][h].x;
                             float *dst = dst_row + pos0 + 64 * h + c0;
                             unsigned long long nan = 0ull;
                             if (!q8)
@@ -930,98 +967,103 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
             }
         } else if (lane == 0 && warp == 1) {
             // ------------------------------------------------ QK issuer
-            const uint64_t kd0 = sdesc_sw128(smem_addr(sK), 16, 1024);
-            const uint64_t qd0 = sdesc_sw128(smem_addr(sQ1), 16, 1024);
-            int ke = 0;
+            const uint32_t kd0 = (uint32_t)sdesc_sw128(smem_addr(sK), 16, 1024);
+            const uint32_t qd0 = (uint32_t)sdesc_sw128(smem_addr(sQ1), 16, 1024);
+            // rb: S barrier of tile t; rf: of the tile before it in its slot
+            Ring rk(SK), rb(SI), rf(SI);
             for (int t = 0;; ++t) {
-                if (!wait_bounded(smem_addr(&bar->full_k[ke % SK]), (ke / SK) & 1, abort, hdr))
+                if (!lane_wait(smem_addr(&bar->full_k[rk.i]), rk.ph, abort, hdr))
                     break;
-                const int tile = bar->tile_of[t % kTileRing];
+                const int tile = bar->tile_of[t & (kTileRing - 1)];
                 const int parts = tile >= nq ? 2 : 1;
-                bool ok = parts == 1 || wait_bounded(smem_addr(&bar->full_k[(ke + 1) % SK]),
-                                                     ((ke + 1) / SK) & 1, abort, hdr);
+                const int k0 = rk.i;
+                rk.next();
+                bool ok = parts == 1 || lane_wait(smem_addr(&bar->full_k[rk.i]), rk.ph, abort, hdr);
+                const int k1 = rk.i;
+                if (parts == 2)
+                    rk.next();
                 if (tile < 0) {
                     // the end, to each block or each group, once its readers are
                     // past the barrier's last phase
                     for (int i = 0; i < (NB == 2 ? 2 : NG); ++i) {
-                        const int sb = NB == 2 ? i : (t + i) % SI, before = NB == 2 ? t - 1 : t + i - SI;
-                        if (before >= 0 && !wait_bounded(smem_addr(&bar->s_free[sb]), (before / SI) & 1,
-                                                         abort, hdr))
+                        const int sb = NB == 2 ? i : rb.i, before = NB == 2 ? t - 1 : t + i - SI;
+                        // (one phase before this barrier's next)
+                        if (before >= 0 && !lane_wait(smem_addr(&bar->s_free[sb]), rb.ph ^ 1, abort, hdr))
                             break;
                         mbar_arrive(smem_addr(&bar->s_full[sb]));
+                        if (NB == 1)
+                            rb.next();
                     }
                     break;
                 }
                 for (int b = 0; b < NB && ok; ++b) {
-                    const int slot = NB == 2 ? b : (t & 1), sb = NB == 2 ? b : t % SI;
+                    const int slot = NB == 2 ? b : (t & 1), sb = NB == 2 ? b : rb.i;
                     // the tile before it in this slot is in its readers' registers
-                    const int before = NB == 2 ? t - 1 : t - 2;
-                    if (before >= 0 && !wait_bounded(smem_addr(&bar->s_free[NB == 2 ? b : before % SI]),
-                                                     (before / SI) & 1, abort, hdr)) {
-                        ok = false;
-                        break;
+                    if (t >= (NB == 2 ? 1 : 2)) {
+                        if (!lane_wait(smem_addr(&bar->s_free[NB == 2 ? b : rf.i]), rf.ph, abort, hdr)) {
+                            ok = false;
+                            break;
+                        }
                     }
                     tc_fence_after();
                     const uint32_t d = tmem + kSCol + 128 * slot;
                     // parts: K's codes (hi, lo on a tail tile), each times Q's hi
                     // and lo
 #pragma unroll 1
-                    for (int i = 0; i < 2 * parts; ++i) {
-                        const int lo = i & 1, part = i >> 1;
-                        const uint64_t kd = kd0 + (uint64_t)((ke + part) % SK) * (kRawBytes >> 4);
-                        const uint32_t idesc = idesc_f8(kBlockM, kTileN, 0, 0) | ((uint32_t)lo << 7) |
-                                               ((uint32_t)part << 10);
-                        if (b == 0) {
+                    for (int part = 0; part < parts; ++part) {
+                        const uint32_t kd = kd0 + (uint32_t)(part ? k1 : k0) * (kRawBytes >> 4);
+                        const uint32_t id = idesc_f8(kBlockM, kTileN, 0, 0) | ((uint32_t)part << 10);
 #pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
-                                mma8_ts(d, tmem + kQCol + 32 * lo + 8 * kk, kd + 2 * kk, idesc, i + kk > 0);
-                        } else {
-                            const uint64_t qd = qd0 + lo * ((kBlockM * kD) >> 4);
-#pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
-                                mma8_ss(d, qd + 2 * kk, kd + 2 * kk, idesc, i + kk > 0);
+                        for (int kk = 0; kk < 8; ++kk) {
+                            const int lo = kk >> 2, k4 = kk & 3;
+                            const uint32_t acc = kk > 0 ? 1u : (uint32_t)part;
+                            if (b == 0)
+                                mma8_ts(d, tmem + kQCol + 32 * lo + 8 * k4, kd + 2 * k4, id | (lo << 7), acc);
+                            else
+                                mma_ss<0>(d, qd0 + lo * ((kBlockM * kD) >> 4) + 2 * k4, kd + 2 * k4,
+                                          id | (lo << 7), acc);
                         }
                     }
                     mma_commit(smem_addr(&bar->s_full[sb]));
                 }
                 if (!ok)
                     break;
-                for (int part = 0; part < parts; ++part)
-                    mma_commit(smem_addr(&bar->empty_k[(ke + part) % SK]));
-                ke += parts;
+                mma_commit(smem_addr(&bar->empty_k[k0]));
+                if (parts == 2)
+                    mma_commit(smem_addr(&bar->empty_k[k1]));
+                rb.next();
+                if (t >= (NB == 2 ? 1 : 2))
+                    rf.next();
             }
             mma_commit(smem_addr(&bar->drain[0]));
             wait_drain(smem_addr(&bar->drain[0]), 0);
         } else if (lane == 0) {
             // ------------------------------------------------ PV issuer
             const uint32_t idesc = idesc_bf16(kD, r_pad, 1, 0);
-            const uint64_t vd0 = sdesc_sw128(smem_addr(sVb), kBoxBytes, 1024);
-            const uint64_t pd0 = sdesc_sw128(smem_addr(sP), 16, 1024);
+            const uint32_t vd0 = (uint32_t)sdesc_sw128(smem_addr(sVb), kBoxBytes, 1024);
+            const uint32_t pd0 = (uint32_t)sdesc_sw128(smem_addr(sP), 16, 1024);
             const uint32_t p_half = (uint32_t)r_pad * 128;
-            for (int t = 0;; ++t) {
-                const int s = t % SVB;
-                if (!wait_bounded(smem_addr(&bar->info[t % kTileRing]), (t / kTileRing) & 1, abort, hdr))
+            Ring rp(NP);
+            for (int t = 0;; ++t, rp.next()) {
+                if (!lane_wait(smem_addr(&bar->info[t & (kTileRing - 1)]), (t >> 4) & 1, abort, hdr))
                     break;
-                if (bar->tile_of[t % kTileRing] < 0) {
+                if (bar->tile_of[t & (kTileRing - 1)] < 0) {
                     mma_commit(smem_addr(&bar->o_final));   // after the last PV
                     break;
                 }
-                const int ps = t % NP, ph = (t / NP) & 1;
-                if (!wait_bounded(smem_addr(&bar->sm_done[ps]), ph, abort, hdr))
+                const int ps = rp.i, s = SVB == 1 ? 0 : ps;
+                if (!lane_wait(smem_addr(&bar->sm_done[ps]), rp.ph, abort, hdr))
                     break;
                 tc_fence_after();
-                uint64_t vd = vd0 + (uint64_t)s * (kVbBytes >> 4);
-                uint64_t pd = pd0 + (uint64_t)ps * ((uint64_t)(r_pad * 256) >> 4);
+                const uint32_t vd = vd0 + (uint32_t)s * (kVbBytes >> 4);
+                const uint32_t pd = pd0 + (uint32_t)(ps * r_pad * 256) / 16;
+                const uint32_t pd1 = pd + (p_half >> 4);
                 const uint32_t d = tmem + (NG == 3 ? 64 * ps : 0);
-#pragma unroll 1
-                for (int h = 0; h < 2; ++h) {
+                const uint32_t acc = t >= NG;
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma16_ss(d, vd + ((kk * 2048) >> 4), pd + ((kk * 32) >> 4), idesc,
-                                 t >= NG || h + kk > 0);
-                    vd += (4 * 2048) >> 4;
-                    pd += p_half >> 4;
-                }
+                for (int kk = 0; kk < 8; ++kk)
+                    mma_ss<1>(d, vd + ((kk * 2048) >> 4), (kk < 4 ? pd : pd1) + 2 * (kk & 3), idesc,
+                              kk > 0 ? 1u : acc);
                 mma_commit(smem_addr(&bar->pv_done[ps]));
             }
             mma_commit(smem_addr(&bar->drain[1]));
@@ -1133,33 +1175,38 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
             const uint32_t c_dst = (uint32_t)((cch >> 3) * kBoxBytes + cr0 * 128 + (((cch & 7) ^ (cr0 & 7)) << 4));
             bool first_q8 = true;   // tail tiles, if any, come first
             int met = 0;            // meetings of this warpgroup over tail tiles
-            for (int t = grp;; t += NG) {
-                unsigned char *vb = sVb + (t % SVB) * kVbBytes;
+            // Rings this warp steps through: S barriers and P^T slots, fixed for a
+            // group (phases alternate) or by tile; V's codes by tile
+            Ring rsb(NG == 3 || NB == 2 ? 1 : 2), rps(NG == 3 ? 1 : 2), rv(SV);
+            for (int i = 0; i < grp; ++i)
+                rv.next();
+            for (int t = grp;; t += NG, rsb.next(), rps.next()) {
+                const int ps = NG == 3 ? grp : rps.i;
+                unsigned char *vb = sVb + (SVB == 1 ? 0 : ps) * kVbBytes;
                 if (first_q8) {
-                    if (!warp_wait_bounded(smem_addr(&bar->info[t % kTileRing]), (t / kTileRing) & 1, abort, hdr)) {
+                    if (!warp_wait(smem_addr(&bar->info[t & (kTileRing - 1)]), (t >> 4) & 1, abort, hdr)) {
                         ok = false;
                         break;
                     }
-                    first_q8 = bar->tile_of[t % kTileRing] >= nq;
+                    first_q8 = bar->tile_of[t & (kTileRing - 1)] >= nq;
                     if (first_q8 && (NG == 3 || warp < 8) &&
                         !tail_keys(a, aux, sK, SK, g, nq, t, grp, met, abort, hdr)) {
                         ok = false;
                         break;
                     }
                 }
-                const int slot = NB == 2 ? b : (t & 1), sb = NB == 2 ? b : t % SI;
-                if (!warp_wait_bounded(smem_addr(&bar->s_full[sb]), (t / SI) & 1, abort, hdr)) {
+                const int slot = NB == 2 ? b : (t & 1), sb = NB == 2 ? b : (NG == 3 ? grp : rsb.i);
+                if (!warp_wait(smem_addr(&bar->s_full[sb]), rsb.ph, abort, hdr)) {
                     ok = false;
                     break;
                 }
-                const int tile = bar->tile_of[t % kTileRing];
+                const int tile = bar->tile_of[t & (kTileRing - 1)];
                 if (tile < 0)
                     break;
                 const bool tail = tile >= nq;
                 // context positions from the half tile's first on
                 int left = tail ? kc.n_tail - (tile - nq) * kTileN : kc.n_q8 - tile * kTileN;
-                const float4 *scl = aux->scale_of[t % kTileRing];
-                const int ps = t % NP;
+                const float4 *scl = aux->scale_of[t & (kTileRing - 1)];
                 if (!hasA) {   // no rows: only V, below
                     __syncwarp();
                     if (lane == 0)
@@ -1227,7 +1274,7 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                         lB += exp_row<2>(r, cB, nmB + sc.y, pB) * sc.z;
                     // this P^T tile is free once PV(t - NP) is done
                     if (h == 0 && t >= NP &&
-                        !warp_wait_bounded(smem_addr(&bar->pv_done[ps]), (t / NP - 1) & 1, abort, hdr)) {
+                        !warp_wait(smem_addr(&bar->pv_done[ps]), rps.ph ^ 1, abort, hdr)) {
                         ok = false;
                         break;
                     }
@@ -1241,16 +1288,23 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     break;
                 // ---- V of this tile to bf16, once PV of the tile before it in
                 // the slot is done
-                if (!warp_wait_bounded(smem_addr(&bar->full_v[t % SV]), (t / SV) & 1, abort, hdr) ||
-                    (t >= SVB && !warp_wait_bounded(smem_addr(&bar->pv_done[(t - SVB) % NP]),
-                                                    ((t - SVB) / NP) & 1, abort, hdr))) {
+                if (!warp_wait(smem_addr(&bar->full_v[rv.i]), rv.ph, abort, hdr)) {
+                    ok = false;
+                    break;
+                }
+                // (a V slot of its own per P^T slot: PV(t - NP), as above; one
+                // slot: PV(t - 1), which the other P^T slot's barrier tells)
+                if (SVB == 1 ? t > 0 && !warp_wait(smem_addr(&bar->pv_done[ps ^ 1]), ps ? rps.ph : rps.ph ^ 1,
+                                                   abort, hdr)
+                             : !hasA && t >= NP &&
+                                   !warp_wait(smem_addr(&bar->pv_done[ps]), rps.ph ^ 1, abort, hdr)) {
                     ok = false;
                     break;
                 }
                 if (!tail) {
-                    const unsigned char *src = sV + (t % SV) * kRawBytes + c_src;
+                    const unsigned char *src = sV + rv.i * kRawBytes + c_src;
                     unsigned char *dst = vb + c_dst;
-#pragma unroll 2
+#pragma unroll 4
                     for (int r = cr0; r < kTileN; r += crs) {
                         const uint2 w = *reinterpret_cast<const uint2 *>(src);
                         const uint2 x = codes_to_bf16(w.x), y = codes_to_bf16(w.y);
@@ -1264,9 +1318,11 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(smem_addr(&bar->empty_v[t % SV]));
+                    mbar_arrive(smem_addr(&bar->empty_v[rv.i]));
                     mbar_arrive(smem_addr(&bar->sm_done[ps]));
                 }
+                for (int i = 0; i < NG; ++i)
+                    rv.next();
             }
             // ---- (m, l) of each row (four threads' partial sums), then O^T
 #pragma unroll
@@ -1305,7 +1361,7 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
             // tiles on (all of it is free after the last PV; one group's rows
             // are as large as two P^T tiles), then one bulk copy per node
             unsigned char *stage = sP + (size_t)grp * R * kD * 4;
-            const bool have_o = ok && warp_wait_bounded(smem_addr(&bar->o_final), 0, abort, hdr);
+            const bool have_o = ok && warp_wait(smem_addr(&bar->o_final), 0, abort, hdr);
             if (have_o) {
                 tc_fence_after();
                 for (int c = 32 * j; c < r_pad; c += 32 * U) {
