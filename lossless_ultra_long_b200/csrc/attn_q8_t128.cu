@@ -168,36 +168,104 @@ constexpr uint32_t idesc_f8(int m, int n, int a5, int b5)
            ((uint32_t)(m >> 4) << 24);
 }
 
-// tcgen05.mma with shared-memory descriptors given by their low words; the
-// high words are the same for every operand here (swizzle, version, 1024-byte
-// groups).  KIND 0: f8f6f4, 1: f16.
+// The products of one tile, eight instructions each.  Shared-memory
+// descriptors are given by their low words; the high words are the same for
+// every operand here (swizzle, version, 1024-byte groups).
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
-template <int KIND>
-__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc)
-{
-    if (KIND == 0)
-        asm volatile(
-            "{\n .reg .pred p;\n .reg .b64 x, y;\n mov.b64 x, {%1, %5};\n mov.b64 y, {%2, %5};\n"
-            " setp.ne.b32 p, %4, 0;\n"
-            " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, p;\n}\n" ::"r"(d), "r"(a), "r"(b),
-            "r"(idesc), "r"(acc), "r"(kDescHi)
-            : "memory");
-    else
-        asm volatile(
-            "{\n .reg .pred p;\n .reg .b64 x, y;\n mov.b64 x, {%1, %5};\n mov.b64 y, {%2, %5};\n"
-            " setp.ne.b32 p, %4, 0;\n"
-            " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}\n" ::"r"(d), "r"(a), "r"(b),
-            "r"(idesc), "r"(acc), "r"(kDescHi)
-            : "memory");
-}
-__device__ __forceinline__ void mma8_ts(uint32_t d, uint32_t a_tmem, uint32_t b, uint32_t idesc,
-                                        uint32_t acc)
+
+// S (+)= (Q_hi + Q_lo) K^T, Q's codes in TMEM (hi, lo: 32 columns each).
+__device__ __forceinline__ void mma_qk_ts(uint32_t d, uint32_t q, uint32_t k, uint32_t idesc, uint32_t acc)
 {
     asm volatile(
-        "{\n .reg .pred p;\n .reg .b64 y;\n mov.b64 y, {%2, %5};\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], y, %3, p;\n}\n" ::"r"(d), "r"(a_tmem), "r"(b),
-        "r"(idesc), "r"(acc), "r"(kDescHi)
+        "{\n .reg .pred p, o;\n .reg .b64 x, y;\n .reg .b32 s, t, u;\n setp.eq.u32 o, 0, 0;\n"
+        " setp.ne.b32 p, %4, 0;\n or.b32 u, %3, 128;\n"
+        " add.u32 s, %1, 0;\n add.u32 t, %2, 0;\n mov.b64 y, {t, %5};\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [s], y, %3, p;\n"
+        " add.u32 s, %1, 8;\n add.u32 t, %2, 2;\n mov.b64 y, {t, %5};\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [s], y, %3, o;\n"
+        " add.u32 s, %1, 16;\n add.u32 t, %2, 4;\n mov.b64 y, {t, %5};\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [s], y, %3, o;\n"
+        " add.u32 s, %1, 24;\n add.u32 t, %2, 6;\n mov.b64 y, {t, %5};\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [s], y, %3, o;\n"
+        " add.u32 s, %1, 32;\n add.u32 t, %2, 0;\n mov.b64 y, {t, %5};\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [s], y, u, o;\n"
+        " add.u32 s, %1, 40;\n add.u32 t, %2, 2;\n mov.b64 y, {t, %5};\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [s], y, u, o;\n"
+        " add.u32 s, %1, 48;\n add.u32 t, %2, 4;\n mov.b64 y, {t, %5};\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [s], y, u, o;\n"
+        " add.u32 s, %1, 56;\n add.u32 t, %2, 6;\n mov.b64 y, {t, %5};\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [s], y, u, o;\n"
+        "}\n" ::"r"(d), "r"(q), "r"(k), "r"(idesc), "r"(acc), "r"(kDescHi)
         : "memory");
+}
+
+// The same with Q's codes in shared memory (hi, then lo: 16 KB each).
+__device__ __forceinline__ void mma_qk_ss(uint32_t d, uint32_t q, uint32_t k, uint32_t idesc, uint32_t acc)
+{
+    asm volatile(
+        "{\n .reg .pred p, o;\n .reg .b64 x, y;\n .reg .b32 s, t, u;\n setp.eq.u32 o, 0, 0;\n"
+        " setp.ne.b32 p, %4, 0;\n or.b32 u, %3, 128;\n"
+        " add.u32 s, %1, 0;\n add.u32 t, %2, 0;\n mov.b64 y, {t, %5};\n"
+        " mov.b64 x, {s, %5};\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, p;\n"
+        " add.u32 s, %1, 2;\n add.u32 t, %2, 2;\n mov.b64 y, {t, %5};\n"
+        " mov.b64 x, {s, %5};\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, o;\n"
+        " add.u32 s, %1, 4;\n add.u32 t, %2, 4;\n mov.b64 y, {t, %5};\n"
+        " mov.b64 x, {s, %5};\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, o;\n"
+        " add.u32 s, %1, 6;\n add.u32 t, %2, 6;\n mov.b64 y, {t, %5};\n"
+        " mov.b64 x, {s, %5};\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, o;\n"
+        " add.u32 s, %1, 1024;\n add.u32 t, %2, 0;\n mov.b64 y, {t, %5};\n"
+        " mov.b64 x, {s, %5};\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, u, o;\n"
+        " add.u32 s, %1, 1026;\n add.u32 t, %2, 2;\n mov.b64 y, {t, %5};\n"
+        " mov.b64 x, {s, %5};\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, u, o;\n"
+        " add.u32 s, %1, 1028;\n add.u32 t, %2, 4;\n mov.b64 y, {t, %5};\n"
+        " mov.b64 x, {s, %5};\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, u, o;\n"
+        " add.u32 s, %1, 1030;\n add.u32 t, %2, 6;\n mov.b64 y, {t, %5};\n"
+        " mov.b64 x, {s, %5};\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, u, o;\n"
+        "}\n" ::"r"(d), "r"(q), "r"(k), "r"(idesc), "r"(acc), "r"(kDescHi)
+        : "memory");
+}
+
+// O^T (+)= V^T P^T; p0, p1: P^T of the tile's first and second 64 positions.
+__device__ __forceinline__ void mma_pv(uint32_t d, uint32_t v, uint32_t p0, uint32_t p1, uint32_t idesc,
+                                       uint32_t acc)
+{
+    asm volatile(
+        "{\n .reg .pred p, o;\n .reg .b64 x, y;\n .reg .b32 s, t;\n setp.eq.u32 o, 0, 0;\n"
+        " setp.ne.b32 p, %5, 0;\n"
+        " add.u32 s, %1, 0;\n add.u32 t, %2, 0;\n mov.b64 x, {s, %6};\n mov.b64 y, {t, %6};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n"
+        " add.u32 s, %1, 128;\n add.u32 t, %2, 2;\n mov.b64 x, {s, %6};\n mov.b64 y, {t, %6};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, o;\n"
+        " add.u32 s, %1, 256;\n add.u32 t, %2, 4;\n mov.b64 x, {s, %6};\n mov.b64 y, {t, %6};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, o;\n"
+        " add.u32 s, %1, 384;\n add.u32 t, %2, 6;\n mov.b64 x, {s, %6};\n mov.b64 y, {t, %6};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, o;\n"
+        " add.u32 s, %1, 512;\n add.u32 t, %3, 0;\n mov.b64 x, {s, %6};\n mov.b64 y, {t, %6};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, o;\n"
+        " add.u32 s, %1, 640;\n add.u32 t, %3, 2;\n mov.b64 x, {s, %6};\n mov.b64 y, {t, %6};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, o;\n"
+        " add.u32 s, %1, 768;\n add.u32 t, %3, 4;\n mov.b64 x, {s, %6};\n mov.b64 y, {t, %6};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, o;\n"
+        " add.u32 s, %1, 896;\n add.u32 t, %3, 6;\n mov.b64 x, {s, %6};\n mov.b64 y, {t, %6};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, o;\n"
+        "}\n" ::"r"(d), "r"(v), "r"(p0), "r"(p1), "r"(idesc), "r"(acc), "r"(kDescHi)
+        : "memory");
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+    return r != 0;
 }
 
 // 16 TMEM lanes x 64 columns, the layout of tmem_ld16x256_x16; waits.
@@ -965,109 +1033,121 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                         mbar_arrive(smem_addr(&bar->s_free[sb]));
                 }
             }
-        } else if (lane == 0 && warp == 1) {
+        } else if (warp == 1) {
             // ------------------------------------------------ QK issuer
+            // (the whole warp keeps the loop, so that descriptors stay uniform;
+            // one elected lane issues)
             const uint32_t kd0 = (uint32_t)sdesc_sw128(smem_addr(sK), 16, 1024);
             const uint32_t qd0 = (uint32_t)sdesc_sw128(smem_addr(sQ1), 16, 1024);
+            const bool leader = elect_one();
             // rb: S barrier of tile t; rf: of the tile before it in its slot
             Ring rk(SK), rb(SI), rf(SI);
             for (int t = 0;; ++t) {
-                if (!lane_wait(smem_addr(&bar->full_k[rk.i]), rk.ph, abort, hdr))
+                if (!warp_wait(smem_addr(&bar->full_k[rk.i]), rk.ph, abort, hdr))
                     break;
                 const int tile = bar->tile_of[t & (kTileRing - 1)];
-                const int parts = tile >= nq ? 2 : 1;
-                const int k0 = rk.i;
-                rk.next();
-                bool ok = parts == 1 || lane_wait(smem_addr(&bar->full_k[rk.i]), rk.ph, abort, hdr);
-                const int k1 = rk.i;
-                if (parts == 2)
-                    rk.next();
-                if (tile < 0) {
+                if (__any_sync(0xffffffffu, tile < 0)) {
                     // the end, to each block or each group, once its readers are
                     // past the barrier's last phase
                     for (int i = 0; i < (NB == 2 ? 2 : NG); ++i) {
                         const int sb = NB == 2 ? i : rb.i, before = NB == 2 ? t - 1 : t + i - SI;
                         // (one phase before this barrier's next)
-                        if (before >= 0 && !lane_wait(smem_addr(&bar->s_free[sb]), rb.ph ^ 1, abort, hdr))
+                        if (before >= 0 && !warp_wait(smem_addr(&bar->s_free[sb]), rb.ph ^ 1, abort, hdr))
                             break;
-                        mbar_arrive(smem_addr(&bar->s_full[sb]));
+                        if (leader)
+                            mbar_arrive(smem_addr(&bar->s_full[sb]));
                         if (NB == 1)
                             rb.next();
                     }
                     break;
                 }
+                const bool two = __any_sync(0xffffffffu, tile >= nq);
+                const int k0 = rk.i;
+                rk.next();
+                bool ok = !two || warp_wait(smem_addr(&bar->full_k[rk.i]), rk.ph, abort, hdr);
+                const int k1 = rk.i;
+                if (two)
+                    rk.next();
                 for (int b = 0; b < NB && ok; ++b) {
                     const int slot = NB == 2 ? b : (t & 1), sb = NB == 2 ? b : rb.i;
                     // the tile before it in this slot is in its readers' registers
-                    if (t >= (NB == 2 ? 1 : 2)) {
-                        if (!lane_wait(smem_addr(&bar->s_free[NB == 2 ? b : rf.i]), rf.ph, abort, hdr)) {
-                            ok = false;
-                            break;
-                        }
+                    if (t >= (NB == 2 ? 1 : 2) &&
+                        !warp_wait(smem_addr(&bar->s_free[NB == 2 ? b : rf.i]), rf.ph, abort, hdr)) {
+                        ok = false;
+                        break;
                     }
                     tc_fence_after();
                     const uint32_t d = tmem + kSCol + 128 * slot;
-                    // parts: K's codes (hi, lo on a tail tile), each times Q's hi
-                    // and lo
-#pragma unroll 1
-                    for (int part = 0; part < parts; ++part) {
-                        const uint32_t kd = kd0 + (uint32_t)(part ? k1 : k0) * (kRawBytes >> 4);
-                        const uint32_t id = idesc_f8(kBlockM, kTileN, 0, 0) | ((uint32_t)part << 10);
-#pragma unroll
-                        for (int kk = 0; kk < 8; ++kk) {
-                            const int lo = kk >> 2, k4 = kk & 3;
-                            const uint32_t acc = kk > 0 ? 1u : (uint32_t)part;
+                    constexpr uint32_t id = idesc_f8(kBlockM, kTileN, 0, 0);
+                    // K's codes (hi, then lo on a tail tile), each times Q's hi and lo
+                    uint32_t kd = kd0 + (uint32_t)k0 * (kRawBytes >> 4);
+                    if (leader) {
+                        if (b == 0)
+                            mma_qk_ts(d, tmem + kQCol, kd, id, 0);
+                        else
+                            mma_qk_ss(d, qd0, kd, id, 0);
+                    }
+                    if (two) {
+                        kd = kd0 + (uint32_t)k1 * (kRawBytes >> 4);
+                        if (leader) {
                             if (b == 0)
-                                mma8_ts(d, tmem + kQCol + 32 * lo + 8 * k4, kd + 2 * k4, id | (lo << 7), acc);
+                                mma_qk_ts(d, tmem + kQCol, kd, id | (1u << 10), 1);
                             else
-                                mma_ss<0>(d, qd0 + lo * ((kBlockM * kD) >> 4) + 2 * k4, kd + 2 * k4,
-                                          id | (lo << 7), acc);
+                                mma_qk_ss(d, qd0, kd, id | (1u << 10), 1);
                         }
                     }
-                    mma_commit(smem_addr(&bar->s_full[sb]));
+                    if (leader)
+                        mma_commit(smem_addr(&bar->s_full[sb]));
                 }
                 if (!ok)
                     break;
-                mma_commit(smem_addr(&bar->empty_k[k0]));
-                if (parts == 2)
-                    mma_commit(smem_addr(&bar->empty_k[k1]));
+                if (leader) {
+                    mma_commit(smem_addr(&bar->empty_k[k0]));
+                    if (two)
+                        mma_commit(smem_addr(&bar->empty_k[k1]));
+                }
                 rb.next();
                 if (t >= (NB == 2 ? 1 : 2))
                     rf.next();
             }
-            mma_commit(smem_addr(&bar->drain[0]));
-            wait_drain(smem_addr(&bar->drain[0]), 0);
-        } else if (lane == 0) {
+            if (leader) {
+                mma_commit(smem_addr(&bar->drain[0]));
+                wait_drain(smem_addr(&bar->drain[0]), 0);
+            }
+            __syncwarp();
+        } else {
             // ------------------------------------------------ PV issuer
             const uint32_t idesc = idesc_bf16(kD, r_pad, 1, 0);
             const uint32_t vd0 = (uint32_t)sdesc_sw128(smem_addr(sVb), kBoxBytes, 1024);
             const uint32_t pd0 = (uint32_t)sdesc_sw128(smem_addr(sP), 16, 1024);
             const uint32_t p_half = (uint32_t)r_pad * 128;
+            const bool leader = elect_one();
             Ring rp(NP);
             for (int t = 0;; ++t, rp.next()) {
-                if (!lane_wait(smem_addr(&bar->info[t & (kTileRing - 1)]), (t >> 4) & 1, abort, hdr))
+                if (!warp_wait(smem_addr(&bar->info[t & (kTileRing - 1)]), (t >> 4) & 1, abort, hdr))
                     break;
-                if (bar->tile_of[t & (kTileRing - 1)] < 0) {
-                    mma_commit(smem_addr(&bar->o_final));   // after the last PV
+                if (__any_sync(0xffffffffu, bar->tile_of[t & (kTileRing - 1)] < 0)) {
+                    if (leader)
+                        mma_commit(smem_addr(&bar->o_final));   // after the last PV
                     break;
                 }
                 const int ps = rp.i, s = SVB == 1 ? 0 : ps;
-                if (!lane_wait(smem_addr(&bar->sm_done[ps]), rp.ph, abort, hdr))
+                if (!warp_wait(smem_addr(&bar->sm_done[ps]), rp.ph, abort, hdr))
                     break;
                 tc_fence_after();
                 const uint32_t vd = vd0 + (uint32_t)s * (kVbBytes >> 4);
-                const uint32_t pd = pd0 + (uint32_t)(ps * r_pad * 256) / 16;
-                const uint32_t pd1 = pd + (p_half >> 4);
-                const uint32_t d = tmem + (NG == 3 ? 64 * ps : 0);
-                const uint32_t acc = t >= NG;
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    mma_ss<1>(d, vd + ((kk * 2048) >> 4), (kk < 4 ? pd : pd1) + 2 * (kk & 3), idesc,
-                              kk > 0 ? 1u : acc);
-                mma_commit(smem_addr(&bar->pv_done[ps]));
+                const uint32_t pd = pd0 + (uint32_t)ps * (uint32_t)(r_pad * 16);
+                if (leader) {
+                    mma_pv(tmem + (NG == 3 ? 64 * ps : 0), vd, pd, pd + (p_half >> 4), idesc,
+                           t >= NG ? 1u : 0u);
+                    mma_commit(smem_addr(&bar->pv_done[ps]));
+                }
             }
-            mma_commit(smem_addr(&bar->drain[1]));
-            wait_drain(smem_addr(&bar->drain[1]), 0);
+            if (leader) {
+                mma_commit(smem_addr(&bar->drain[1]));
+                wait_drain(smem_addr(&bar->drain[1]), 0);
+            }
+            __syncwarp();
         }
     } else {
         // ---- query rows of this KV head: row n = node * G + (head - g*G),
