@@ -10,15 +10,15 @@
 //                      bit, which 3 bits represent), down to 2^-16 of the
 //                      scaled row.  So S = hi K^T + lo K^T costs what one
 //                      bf16 product costs, and K is never converted.
-//   O^T += V^T P^T     kind::f16 on bf16: V's codes are bf16 numbers; the
-//                      softmax warps write them out once per tile.
+//   O^T += V^T P^T     kind::f16 on bf16: V's codes are bf16 numbers;
+//                      the converter warps write them out once per tile.
 // The scales (a power of two per 64 rows) never touch the products' inputs:
 // K's multiplies the score inside the exponent's FMA, V's is added to the
 // exponent, so the weight leaves as p * s_v with its one rounding to bf16,
 // and each block's sum is multiplied back by 1 / s_v.
 //
 // A tail tile (bf16 rows: newest context, tree) goes through the same
-// products: a softmax warpgroup scales its keys by block and splits them like
+// products: the converter warps scale its keys by block and splits them like
 // the queries into an e4m3 and an e5m2 tile (two K slots, four products),
 // and copies V.  Rows with an infinity or a NaN are zeroed there and noted;
 // a query row that sees one gets a NaN sum.
@@ -31,18 +31,17 @@
 // weights' own rounding, so rows that rest on few positions need no second
 // look.
 //
-// CTA = (split, KV head, node group), 16 warps, one CTA per SM:
+// CTA = (split, KV head, node group), 20 warps, one CTA per SM:
 //   warp 0      root scores out of S        warp 1  QK issuer, TMEM
 //   warp 2      PV issuer                   warp 3  TMA producer
-//   warps 4-15  softmax, and V's codes to bf16
-// (Separate converter warps were slower: every sub-partition then ran three
-// unlike loops at once and waited for instructions.)
+//   warps 4-15  softmax, as many as the rows need; the others and
+//   warps 16-19 V's codes to bf16
 // P^T is double-buffered, and with one query block (R <= 128) S too, so a
 // tile's exponentials overlap the previous tile's PV and the next one's QK.
 // With at most 64 query rows one warpgroup is enough for a tile, but its chain
-// of waits and loads is longer than the tile's stream from HBM: the three
-// softmax warpgroups then take tiles in turn, each with its own reference,
-// O^T, P^T and V, and their partials are merged before they leave.
+// of waits and loads is longer than the tile's stream from HBM: two softmax
+// warpgroups then take tiles in turn, each with its own reference,
+// O^T and P^T, and their partials are merged before they leave.
 // TMEM: O^T in [0, 192), Q_0 (hi, lo) in [192, 256), S in [256, 512).
 //
 // Every wait is bounded (about a second): on expiry the kernel records
@@ -69,7 +68,7 @@ constexpr int kBlockM = 128;                 // query rows per QK block (TMEM la
 constexpr int kRawBytes = kTileN * kD;       // codes of K (or V) of a tile: 16 KB
 constexpr int kBoxBytes = kTileN * 64 * 2;   // one 64-column half of a bf16 V tile
 constexpr int kVbBytes = 2 * kBoxBytes;
-constexpr int kThreads = 512;                // 16 warps
+constexpr int kThreads = 640;                // 20 warps
 constexpr int kMaxStages = 5;
 constexpr int kMaxRows = 192;
 constexpr int kQCol = 192;                   // Q of block 0: hi 32 columns, lo 32 columns
@@ -77,6 +76,7 @@ constexpr int kSCol = 256;                   // S slots: 128 columns each
 constexpr int kTmemCols = 512;
 constexpr int kQ1Bytes = 2 * kBlockM * kD;   // Q of block 1 in shared memory: hi, lo
 constexpr float kMaxRowSum = 9.223372036854775808e18f;   // 2^63
+constexpr int kTailWarps = 4;                // warps 16-19, which also turn the tail tiles
 constexpr size_t kSmemLimit = 232448;        // dynamic shared memory per CTA
 constexpr int kBarQuery = 1;                 // named barrier: query rows in place
 constexpr int kBarOut = 2;                   // named barrier: O^T staged, or merged, in shared memory
@@ -94,11 +94,12 @@ struct Bars {
     uint64_t empty_v[kMaxStages];
     uint64_t s_full[3];             // QK landed: by block, or (one block) by tile in turn
     uint64_t s_free[3];             // its readers hold S in registers
-    uint64_t sm_done[3];            // per P^T slot: P^T and V are written
+    uint64_t vb_full[2];            // V in bf16
+    uint64_t sm_done[3];            // per P^T slot: P^T is written
     uint64_t pv_done[3];            // per P^T slot: PV is complete
     uint64_t o_final;
     uint64_t drain[2];
-    uint64_t conv[3];               // a warpgroup that turns a tail tile meets
+    uint64_t conv;                  // the converter warps meet (tail tiles)
     uint64_t info[kTileRing];       // tile_of, scale_of of that tile are written
     // per tile, at [t & (kTileRing - 1)]: its index (-1 after the last) and its
     // first K ring entry.  Written by the producer before the arrival that
@@ -107,7 +108,7 @@ struct Bars {
     volatile int32_t entry_of[kTileRing];
     uint32_t bad[4][4];             // tail tile t % 4: rows with a value that is no number
     uint32_t bad_k[4][4];
-    uint32_t top[3][4];             // tail tile: largest key magnitude of each 32 rows
+    uint32_t top[4];                // tail tile: largest key magnitude of each 32 rows
     uint32_t tmem_base;
     uint32_t abort;
     int32_t overflow;
@@ -115,12 +116,12 @@ struct Bars {
 
 struct Aux {
     Bars bar;
-    // per tile and half, written like tile_of (a tail tile's k by the warps that turn it):
+    // per tile and half, written like tile_of (a tail tile's k by a converter):
     // K's scale, V's as an exponent, V's inverse.  A block that is NaN, in K
     // or V, has a NaN exponent and inverse: its weights and sums are NaN.
     float4 scale_of[kTileRing][2];
     unsigned long long anc[TS_MAX_TREE];
-    float2 ml[3][64];               // (m, l) of each group's rows, to be merged
+    float2 ml[2][64];               // (m, l) of each group's rows, to be merged
     float row_scale[2 * kBlockM];   // softmax scale * log2 e * the query row's scale
 };
 constexpr size_t kAuxBytes = (sizeof(Aux) + 1023) / 1024 * 1024;
@@ -136,18 +137,18 @@ __host__ __device__ inline int q8_row_of(int n, int R)
 }
 
 // Softmax warpgroups that take tiles in turn (one partial each per split).
-__host__ __device__ inline int q8_groups(int rows) { return rows <= 64 ? 3 : 1; }
+__host__ __device__ inline int q8_groups(int rows) { return rows <= 64 ? 2 : 1; }
 
 __host__ __device__ inline Layout q8_layout(int rows, int groups)
 {
     Layout L;
     L.r_pad = (rows + 15) / 16 * 16;
-    L.p_slots = groups == 3 ? 3 : 2;
+    L.p_slots = 2;
     L.q1_off = 0;
     L.p_off = rows > kBlockM ? kQ1Bytes : 0;
     // the P^T tiles, then 1 KB that rows past the query rows are written to
     L.vb_off = L.p_off + (size_t)L.r_pad * 256 * L.p_slots + 1024;
-    L.stages_vb = rows > kBlockM ? 1 : L.p_slots;
+    L.stages_vb = rows > kBlockM ? 1 : 2;
     L.k_off = L.vb_off + (size_t)L.stages_vb * kVbBytes;
     const size_t fixed = 1024 + L.k_off + kAuxBytes;
     int stages = (int)((kSmemLimit - fixed) / kRawBytes);
@@ -667,12 +668,12 @@ __device__ __forceinline__ bool wait_count_bounded(const int32_t *p, int target,
     }
 }
 
-// The keys of tail tile t into its two K slots, by the 128 threads of one
-// warpgroup, a row each: scaled by block of 64 rows, split into e4m3 and e5m2
+// The keys of tail tile t into its two K slots, by the converters' 128 threads,
+// a row each: scaled by block of 64 rows, split into e4m3 and e5m2
 // codes; notes the rows with an infinity or a NaN (and zeroes them).  False
 // when a wait ran out.
 __device__ __noinline__ bool tail_keys(const AttnQ8Args &a, Aux *aux, unsigned char *sK, int SK, int g,
-                                       int nq, int t, int grp, int &met, volatile uint32_t *abort,
+                                       int nq, int t, int &met, volatile uint32_t *abort,
                                        WorkspaceHeader *hdr)
 {
     Bars *bar = &aux->bar;
@@ -699,12 +700,12 @@ __device__ __noinline__ bool tail_keys(const AttnQ8Args &a, Aux *aux, unsigned c
     if (lane == 0) {
         bar->bad_k[t & 3][w] = wk;
         bar->bad[t & 3][w] = wb;
-        bar->top[grp][w] = wtop;
-        mbar_arrive(smem_addr(&bar->conv[grp]));
+        bar->top[w] = wtop;
+        mbar_arrive(smem_addr(&bar->conv));
     }
-    if (!warp_wait(smem_addr(&bar->conv[grp]), met++ & 1, abort, hdr))
+    if (!warp_wait(smem_addr(&bar->conv), met++ & 1, abort, hdr))
         return false;
-    volatile uint32_t *top = bar->top[grp];
+    volatile uint32_t *top = bar->top;
     const int e = split_exp(max(top[w & 2], top[(w & 2) + 1]));
     if (tid == 0) {
         aux->scale_of[t & (kTileRing - 1)][0].x = two_to(e);
@@ -730,8 +731,8 @@ __device__ __noinline__ bool tail_keys(const AttnQ8Args &a, Aux *aux, unsigned c
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0)
-        mbar_arrive(smem_addr(&bar->conv[grp]));
-    if (!warp_wait(smem_addr(&bar->conv[grp]), met++ & 1, abort, hdr))
+        mbar_arrive(smem_addr(&bar->conv));
+    if (!warp_wait(smem_addr(&bar->conv), met++ & 1, abort, hdr))
         return false;
     if (tid == 0) {
         mbar_arrive(smem_addr(&bar->full_k[e0 % SK]));
@@ -757,6 +758,16 @@ __device__ __noinline__ void tail_values(const AttnQ8Args &a, Bars *bar, unsigne
             use ? __ldg(vr + c) : make_uint4(0u, 0u, 0u, 0u);
 }
 
+// (lane quarter, unit of 16 lanes) pairs that hold query rows of a block of
+// `rows` rows in runs of rq per quarter.
+__device__ __forceinline__ int active_units(int rows, int rq)
+{
+    int n = 0;
+    for (int q = 0; q < 4; ++q)
+        n += (max(0, min(rq, rows - q * rq)) + 15) / 16;
+    return n;
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
 attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ AttnQ8Args a,
@@ -776,9 +787,12 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
     const int rq0 = max((R0 + 3) / 4, min(R0, 8)), rq1 = max((R1 + 3) / 4, min(R1, 8));
     const int u0 = (rq0 + 15) / 16, u1 = (rq1 + 15) / 16;
     const int U = u0 + u1;  // softmax warps per lane quarter and group
+    // (quarter, unit) pairs with query rows: their warps arrive on the barriers
+    const int act0 = active_units(R0, rq0), act1 = active_units(R1, rq1);
     const bool rs_warp0 = a.root_scores != nullptr && node0 == 0;
     const Layout lay = q8_layout(R, NG);
     const int SK = lay.stages_k, SV = lay.stages_v, SVB = lay.stages_vb, r_pad = lay.r_pad;
+    const int n_conv = kThreads / 32 - 4 - 4 * U * NG;   // converter warps, the last ones
     const int NP = lay.p_slots;
     const int SI = NB == 2 ? 1 : NP;   // one block: S barriers of tile t are [t % SI], its slot t & 1
 
@@ -810,18 +824,20 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
         }
         for (int s = 0; s < SV; ++s) {
             mbar_init(smem_addr(&bar->full_v[s]), 1);
-            mbar_init(smem_addr(&bar->empty_v[s]), NG == 3 ? 4 : 4 * U);
+            mbar_init(smem_addr(&bar->empty_v[s]), n_conv);
         }
         const int rs = rs_warp0 ? 1 : 0;
+        mbar_init(smem_addr(&bar->conv), kTailWarps);
+        mbar_init(smem_addr(&bar->vb_full[0]), n_conv);
+        mbar_init(smem_addr(&bar->vb_full[1]), n_conv);
         mbar_init(smem_addr(&bar->drain[0]), 1);
         mbar_init(smem_addr(&bar->drain[1]), 1);
         for (int i = 0; i < kTileRing; ++i)
             mbar_init(smem_addr(&bar->info[i]), 1);
         for (int i = 0; i < 3; ++i) {
             mbar_init(smem_addr(&bar->s_full[i]), 1);
-            mbar_init(smem_addr(&bar->s_free[i]), NB == 1 ? 4 * u0 + rs : (i == 0 ? 4 * u0 : 4 * u1 + rs));
-            mbar_init(smem_addr(&bar->sm_done[i]), 4 * U);
-            mbar_init(smem_addr(&bar->conv[i]), 4);
+            mbar_init(smem_addr(&bar->s_free[i]), NB == 1 ? act0 + rs : (i == 0 ? act0 : act1 + rs));
+            mbar_init(smem_addr(&bar->sm_done[i]), act0 + act1);
             mbar_init(smem_addr(&bar->pv_done[i]), 1);
         }
         mbar_init(smem_addr(&bar->o_final), 1);
@@ -856,7 +872,7 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 aux->anc[i] = masks.anc[i];
         if (warp != 3) {
             tc_fence_before();
-            named_bar_sync(kBarQuery, kThreads - 32);
+            named_bar_sync(kBarQuery, kThreads - 32 * (1 + n_conv));
             tc_fence_after();
         }
         if (warp == 3) {
@@ -909,7 +925,7 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 const uint32_t fb = smem_addr(&bar->full_v[s]);
                 const int tile = bar->tile_of[t & (kTileRing - 1)];
                 if (tile >= nq) {
-                    mbar_arrive(fb);   // a tail tile: the softmax warps read it themselves
+                    mbar_arrive(fb);   // a tail tile: the converters read it themselves
                 } else {
                     mbar_arrive_expect_tx(fb, kRawBytes);
                     tma_load_3d_hint(smem_addr(sV + s * kRawBytes), &tmap_v, 0, tile * kTileN, g, fb, pol);
@@ -949,7 +965,7 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                             tma_load_3d_hint(smem_addr(sK + s * kRawBytes), &tmap_k, 0, tile * kTileN, g,
                                              fb, pol);
                             k_tma = ke;
-                        }   // a tail tile's slots, free now, are filled by the softmax warps
+                        }   // a tail tile's slots, free now, are filled by the converters
                     }
                     for (int j = 0; j < (tile < 0 ? 3 : 1); ++j)
                         mbar_arrive(smem_addr(&bar->info[(i + j) & (kTileRing - 1)]));
@@ -1122,8 +1138,8 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
             const uint32_t pd0 = (uint32_t)sdesc_sw128(smem_addr(sP), 16, 1024);
             const uint32_t p_half = (uint32_t)r_pad * 128;
             const bool leader = elect_one();
-            Ring rp(NP);
-            for (int t = 0;; ++t, rp.next()) {
+            Ring rp(NP), rvb(SVB);
+            for (int t = 0;; ++t, rp.next(), rvb.next()) {
                 if (!warp_wait(smem_addr(&bar->info[t & (kTileRing - 1)]), (t >> 4) & 1, abort, hdr))
                     break;
                 if (__any_sync(0xffffffffu, bar->tile_of[t & (kTileRing - 1)] < 0)) {
@@ -1131,14 +1147,15 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                         mma_commit(smem_addr(&bar->o_final));   // after the last PV
                     break;
                 }
-                const int ps = rp.i, s = SVB == 1 ? 0 : ps;
-                if (!warp_wait(smem_addr(&bar->sm_done[ps]), rp.ph, abort, hdr))
+                const int ps = rp.i, s = rvb.i;
+                if (!warp_wait(smem_addr(&bar->vb_full[s]), rvb.ph, abort, hdr) ||
+                    !warp_wait(smem_addr(&bar->sm_done[ps]), rp.ph, abort, hdr))
                     break;
                 tc_fence_after();
                 const uint32_t vd = vd0 + (uint32_t)s * (kVbBytes >> 4);
                 const uint32_t pd = pd0 + (uint32_t)ps * (uint32_t)(r_pad * 16);
                 if (leader) {
-                    mma_pv(tmem + (NG == 3 ? 64 * ps : 0), vd, pd, pd + (p_half >> 4), idesc,
+                    mma_pv(tmem + (NG == 2 ? 64 * ps : 0), vd, pd, pd + (p_half >> 4), idesc,
                            t >= NG ? 1u : 0u);
                     mma_commit(smem_addr(&bar->pv_done[ps]));
                 }
@@ -1148,6 +1165,53 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 wait_drain(smem_addr(&bar->drain[1]), 0);
             }
             __syncwarp();
+        }
+    } else if (warp >= kThreads / 32 - n_conv) {
+        // ------------------------------------------------ converters
+        const int tid = threadIdx.x - (kThreads - 32 * n_conv), rows = 2 * n_conv;   // rows per step
+        // this thread's share of V's codes: a column chunk and every `rows`-th
+        // row, all with the same row mod 8
+        const int ch = tid & 15, r0 = tid >> 4;
+        const uint32_t c_dst = (uint32_t)((ch >> 3) * kBoxBytes + r0 * 128 + (((ch & 7) ^ (r0 & 7)) << 4));
+        int met = 0;   // meetings of the converters over tail tiles
+        Ring rv(SV), rvb(SVB), rpv(NP);   // rpv: PV of the tile before in the bf16 slot
+        for (int t = 0;; ++t, rv.next(), rvb.next()) {
+            if (!warp_wait(smem_addr(&bar->info[t & (kTileRing - 1)]), (t >> 4) & 1, abort, hdr))
+                break;
+            const int tile = bar->tile_of[t & (kTileRing - 1)];
+            if (tile < 0)
+                break;
+            const bool tail = __any_sync(0xffffffffu, tile >= nq);
+            if (tail && warp >= 16 && !tail_keys(a, aux, sK, SK, g, nq, t, met, abort, hdr))
+                break;
+            if (!warp_wait(smem_addr(&bar->full_v[rv.i]), rv.ph, abort, hdr))
+                break;
+            if (t >= SVB) {
+                if (!warp_wait(smem_addr(&bar->pv_done[rpv.i]), rpv.ph, abort, hdr))
+                    break;
+                rpv.next();
+            }
+            unsigned char *vb = sVb + rvb.i * kVbBytes;
+            if (!tail) {
+                const unsigned char *src = sV + rv.i * kRawBytes + 8 * tid;
+                unsigned char *dst = vb + c_dst;
+#pragma unroll 4
+                for (int r = r0; r < kTileN; r += rows) {
+                    const uint2 w = *reinterpret_cast<const uint2 *>(src);
+                    const uint2 x = codes_to_bf16(w.x), y = codes_to_bf16(w.y);
+                    *reinterpret_cast<uint4 *>(dst) = make_uint4(x.x, x.y, y.x, y.y);
+                    src += rows * kD;
+                    dst += rows * 128;
+                }
+            } else if (warp >= 16) {
+                tail_values(a, bar, vb, g, nq, tile, t);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(smem_addr(&bar->vb_full[rvb.i]));
+                mbar_arrive(smem_addr(&bar->empty_v[rv.i]));
+            }
         }
     } else {
         // ---- query rows of this KV head: row n = node * G + (head - g*G),
@@ -1207,12 +1271,12 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
             named_bar_arrive(kBarQLoads, kQLoadThreads);   // one block: no rows to load
         }
         tc_fence_before();
-        named_bar_sync(kBarQuery, kThreads - 32);
+        named_bar_sync(kBarQuery, kThreads - 32 * (1 + n_conv));
         tc_fence_after();
         if ((warp - 4) / 4 < U * NG) {
             // ------------------------------------------------ softmax
-            const int q = warp & 3, j = NG == 3 ? 0 : (warp - 4) >> 2;
-            const int grp = NG == 3 ? (warp - 4) >> 2 : 0;
+            const int q = warp & 3, j = NG == 2 ? 0 : (warp - 4) >> 2;
+            const int grp = NG == 2 ? (warp - 4) >> 2 : 0;
             const int b = j < u0 ? 0 : 1;
             const int lb = 16 * (b == 0 ? j : j - u0);  // unit's first lane in the quarter
             const int Rb = b == 0 ? R0 : R1, rqb = b == 0 ? rq0 : rq1;
@@ -1247,35 +1311,12 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
             float lA = rsA == rsA ? 0.f : rsA, lB = rsB == rsB ? 0.f : rsB;
             bool fresh = true;   // some row has no reference yet (uniform)
             bool ok = true;
-            // this thread's share of V's codes: a column chunk and every
-            // (threads / 16)-th row, all with the same row mod 8
-            const int n_thr = NG == 3 ? 128 : 128 * U, tid = NG == 3 ? threadIdx.x & 127 : threadIdx.x - 128;
-            const int cch = tid & 15, cr0 = tid >> 4, crs = n_thr >> 4;
-            const uint32_t c_src = (uint32_t)(8 * tid);
-            const uint32_t c_dst = (uint32_t)((cch >> 3) * kBoxBytes + cr0 * 128 + (((cch & 7) ^ (cr0 & 7)) << 4));
-            bool first_q8 = true;   // tail tiles, if any, come first
-            int met = 0;            // meetings of this warpgroup over tail tiles
-            // Rings this warp steps through: S barriers and P^T slots, fixed for a
-            // group (phases alternate) or by tile; V's codes by tile
-            Ring rsb(NG == 3 || NB == 2 ? 1 : 2), rps(NG == 3 ? 1 : 2), rv(SV);
-            for (int i = 0; i < grp; ++i)
-                rv.next();
-            for (int t = grp;; t += NG, rsb.next(), rps.next()) {
-                const int ps = NG == 3 ? grp : rps.i;
-                unsigned char *vb = sVb + (SVB == 1 ? 0 : ps) * kVbBytes;
-                if (first_q8) {
-                    if (!warp_wait(smem_addr(&bar->info[t & (kTileRing - 1)]), (t >> 4) & 1, abort, hdr)) {
-                        ok = false;
-                        break;
-                    }
-                    first_q8 = bar->tile_of[t & (kTileRing - 1)] >= nq;
-                    if (first_q8 && (NG == 3 || warp < 8) &&
-                        !tail_keys(a, aux, sK, SK, g, nq, t, grp, met, abort, hdr)) {
-                        ok = false;
-                        break;
-                    }
-                }
-                const int slot = NB == 2 ? b : (t & 1), sb = NB == 2 ? b : (NG == 3 ? grp : rsb.i);
+            // S barriers and P^T slots, fixed for a group (phases alternate) or by
+            // tile
+            Ring rsb(NG == 2 || NB == 2 ? 1 : 2), rps(NG == 2 ? 1 : 2);
+            for (int t = grp; hasA; t += NG, rsb.next(), rps.next()) {
+                const int ps = NG == 2 ? grp : rps.i;
+                const int slot = NB == 2 ? b : (t & 1), sb = NB == 2 ? b : (NG == 2 ? grp : rsb.i);
                 if (!warp_wait(smem_addr(&bar->s_full[sb]), rsb.ph, abort, hdr)) {
                     ok = false;
                     break;
@@ -1287,16 +1328,11 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 // context positions from the half tile's first on
                 int left = tail ? kc.n_tail - (tile - nq) * kTileN : kc.n_q8 - tile * kTileN;
                 const float4 *scl = aux->scale_of[t & (kTileRing - 1)];
-                if (!hasA) {   // no rows: only V, below
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(smem_addr(&bar->s_free[sb]));
-                }
                 uint32_t atA = p_rowA + 2 * ps * p_stepA, atB = p_rowB + 2 * ps * p_stepB;
                 // the halves are the tile's two scale blocks; one copy of the code
                 // serves both (the loop must stay inside the instruction cache)
 #pragma unroll 1
-                for (int h = hasA ? 0 : 2; h < 2; ++h, left -= 64) {
+                for (int h = 0; h < 2; ++h, left -= 64) {
                     tc_fence_after();
                     uint32_t r[32];
                     tmem_ld16x256_x8(s_addr + 128 * slot + 64 * h, r);
@@ -1366,43 +1402,10 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 }
                 if (!ok)
                     break;
-                // ---- V of this tile to bf16, once PV of the tile before it in
-                // the slot is done
-                if (!warp_wait(smem_addr(&bar->full_v[rv.i]), rv.ph, abort, hdr)) {
-                    ok = false;
-                    break;
-                }
-                // (a V slot of its own per P^T slot: PV(t - NP), as above; one
-                // slot: PV(t - 1), which the other P^T slot's barrier tells)
-                if (SVB == 1 ? t > 0 && !warp_wait(smem_addr(&bar->pv_done[ps ^ 1]), ps ? rps.ph : rps.ph ^ 1,
-                                                   abort, hdr)
-                             : !hasA && t >= NP &&
-                                   !warp_wait(smem_addr(&bar->pv_done[ps]), rps.ph ^ 1, abort, hdr)) {
-                    ok = false;
-                    break;
-                }
-                if (!tail) {
-                    const unsigned char *src = sV + rv.i * kRawBytes + c_src;
-                    unsigned char *dst = vb + c_dst;
-#pragma unroll 4
-                    for (int r = cr0; r < kTileN; r += crs) {
-                        const uint2 w = *reinterpret_cast<const uint2 *>(src);
-                        const uint2 x = codes_to_bf16(w.x), y = codes_to_bf16(w.y);
-                        *reinterpret_cast<uint4 *>(dst) = make_uint4(x.x, x.y, y.x, y.y);
-                        src += crs * kD;
-                        dst += crs * 128;
-                    }
-                } else if (NG == 3 || warp < 8) {
-                    tail_values(a, bar, vb, g, nq, tile, t);
-                }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(smem_addr(&bar->empty_v[rv.i]));
+                if (lane == 0)
                     mbar_arrive(smem_addr(&bar->sm_done[ps]));
-                }
-                for (int i = 0; i < NG; ++i)
-                    rv.next();
             }
             // ---- (m, l) of each row (four threads' partial sums), then O^T
 #pragma unroll
@@ -1425,13 +1428,13 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
             };
             if (ok && (lane & 3) == 0) {
                 if (vA) {
-                    if (NG == 3)
+                    if (NG == 2)
                         aux->ml[grp][nA] = make_float2(mA, lA);
                     else
                         ws_ml[part_row + orow_of(nA)] = make_float2(mA, lA);
                 }
                 if (vB) {
-                    if (NG == 3)
+                    if (NG == 2)
                         aux->ml[grp][nB] = make_float2(mB, lB);
                     else
                         ws_ml[part_row + orow_of(nB)] = make_float2(mB, lB);
@@ -1457,26 +1460,24 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
             }
             fence_proxy_async_smem();
             named_bar_sync(kBarOut, 128 * U * NG);   // every softmax warp, whatever its path
-            if (NG == 3) {
+            if (NG == 2) {
                 // the groups' partials into one (all of a row's by one warp)
-                for (int r = warp - 4; r < R && !*abort; r += 12) {
-                    const float2 p0 = aux->ml[0][r], p1 = aux->ml[1][r], p2 = aux->ml[2][r];
-                    const float M = max3f(p0.x, p1.x, p2.x);
+                for (int r = warp - 4; r < R && !*abort; r += 8) {
+                    const float2 p0 = aux->ml[0][r], p1 = aux->ml[1][r];
+                    const float M = fmaxf(p0.x, p1.x);
                     // a group that saw nothing (m = -inf) has l = 0, or NaN, and any O
                     const float w0 = p0.x == -INFINITY ? 0.f : exp2f(p0.x - M);
                     const float w1 = p1.x == -INFINITY ? 0.f : exp2f(p1.x - M);
-                    const float w2 = p2.x == -INFINITY ? 0.f : exp2f(p2.x - M);
                     float4 *o = reinterpret_cast<float4 *>(sP) + r * (kD / 4) + lane;
                     float4 x = w0 != 0.f ? *o : make_float4(0.f, 0.f, 0.f, 0.f);
                     const float4 y = w1 != 0.f ? o[R * (kD / 4)] : make_float4(0.f, 0.f, 0.f, 0.f);
-                    const float4 z = w2 != 0.f ? o[2 * R * (kD / 4)] : make_float4(0.f, 0.f, 0.f, 0.f);
-                    x.x = w0 * x.x + w1 * y.x + w2 * z.x;
-                    x.y = w0 * x.y + w1 * y.y + w2 * z.y;
-                    x.z = w0 * x.z + w1 * y.z + w2 * z.z;
-                    x.w = w0 * x.w + w1 * y.w + w2 * z.w;
+                    x.x = w0 * x.x + w1 * y.x;
+                    x.y = w0 * x.y + w1 * y.y;
+                    x.z = w0 * x.z + w1 * y.z;
+                    x.w = w0 * x.w + w1 * y.w;
                     *o = x;
                     if (lane == 0)
-                        ws_ml[part_row + orow_of(r)] = make_float2(M, w0 * p0.y + w1 * p1.y + w2 * p2.y);
+                        ws_ml[part_row + orow_of(r)] = make_float2(M, w0 * p0.y + w1 * p1.y);
                 }
                 fence_proxy_async_smem();
                 named_bar_sync(kBarOut, 128 * U * NG);
