@@ -1195,13 +1195,21 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
             if (!tail) {
                 const unsigned char *src = sV + rv.i * kRawBytes + 8 * tid;
                 unsigned char *dst = vb + c_dst;
-#pragma unroll 4
-                for (int r = r0; r < kTileN; r += rows) {
-                    const uint2 w = *reinterpret_cast<const uint2 *>(src);
-                    const uint2 x = codes_to_bf16(w.x), y = codes_to_bf16(w.y);
-                    *reinterpret_cast<uint4 *>(dst) = make_uint4(x.x, x.y, y.x, y.y);
-                    src += rows * kD;
-                    dst += rows * 128;
+                // four steps' loads before their stores (which could alias them
+                // as far as the compiler knows); 16 steps, or 8, of four each
+#pragma unroll 1
+                for (int r = r0; r < kTileN; r += 4 * rows) {
+                    uint2 w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        w[i] = *reinterpret_cast<const uint2 *>(src + i * rows * kD);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint2 x = codes_to_bf16(w[i].x), y = codes_to_bf16(w[i].y);
+                        *reinterpret_cast<uint4 *>(dst + i * rows * 128) = make_uint4(x.x, x.y, y.x, y.y);
+                    }
+                    src += 4 * rows * kD;
+                    dst += 4 * rows * 128;
                 }
             } else if (warp >= 16) {
                 tail_values(a, bar, vb, g, nq, tile, t);
