@@ -87,6 +87,8 @@ constexpr int kQLoadThreads = 32 * 9;        // warps 4-11 arrive, the producer 
 constexpr int kMaxGz = 256;                  // (KV head, node group) pairs: counters in the workspace
 static_assert(kMaxGz * 16 <= (int)kQ8SyncBytes, "counters fit their region");
 
+constexpr int kTailMark = 1 << 20, kEndMark = -(1 << 30);
+
 struct Bars {
     uint64_t full_k[kMaxStages];
     uint64_t empty_k[kMaxStages];
@@ -117,8 +119,10 @@ struct Bars {
 struct Aux {
     Bars bar;
     // per tile and half, written like tile_of (a tail tile's k by a converter):
-    // K's scale, V's as an exponent, V's inverse.  A block that is NaN, in K
-    // or V, has a NaN exponent and inverse: its weights and sums are NaN.
+    // K's scale, V's as an exponent, V's inverse, and (as an int) how many of
+    // the half's positions are context, kTailMark added on a tail tile, or
+    // kEndMark.  A block that is NaN, in K or V, has a NaN exponent and
+    // inverse: its weights and sums are NaN.
     float4 scale_of[kTileRing][2];
     unsigned long long anc[TS_MAX_TREE];
     float2 ml[2][64];               // (m, l) of each group's rows, to be merged
@@ -127,7 +131,7 @@ struct Aux {
 constexpr size_t kAuxBytes = (sizeof(Aux) + 1023) / 1024 * 1024;
 
 struct Layout {
-    int r_pad, p_slots, stages_k, stages_v, stages_vb;
+    int r_pad, stages_k, stages_v, stages_vb;
     size_t q1_off, p_off, vb_off, k_off, v_off, aux_off, smem_bytes;
 };
 
@@ -136,18 +140,14 @@ __host__ __device__ inline int q8_row_of(int n, int R)
     return R > kBlockM ? (n < kBlockM ? (R - kBlockM) + n : n - kBlockM) : n;
 }
 
-// Softmax warpgroups that take tiles in turn (one partial each per split).
-__host__ __device__ inline int q8_groups(int rows) { return rows <= 64 ? 2 : 1; }
-
-__host__ __device__ inline Layout q8_layout(int rows, int groups)
+__host__ __device__ inline Layout q8_layout(int rows)
 {
     Layout L;
     L.r_pad = (rows + 15) / 16 * 16;
-    L.p_slots = 2;
     L.q1_off = 0;
     L.p_off = rows > kBlockM ? kQ1Bytes : 0;
     // the P^T tiles, then 1 KB that rows past the query rows are written to
-    L.vb_off = L.p_off + (size_t)L.r_pad * 256 * L.p_slots + 1024;
+    L.vb_off = L.p_off + (size_t)L.r_pad * 512 + 1024;
     L.stages_vb = rows > kBlockM ? 1 : 2;
     L.k_off = L.vb_off + (size_t)L.stages_vb * kVbBytes;
     const size_t fixed = 1024 + L.k_off + kAuxBytes;
@@ -286,6 +286,29 @@ __device__ __forceinline__ void tmem_ld16x256_x8(uint32_t taddr, uint32_t (&r)[3
         : "memory");
 }
 
+// 16 TMEM lanes x 32 columns, the same layout; the registers hold the values
+// after tmem_ld_wait16.
+__device__ __forceinline__ void tmem_ld16x256_x4(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld_wait16(uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                   "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
+                   "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+}
+
 // 16 consecutive 32-bit TMEM columns of this thread's lane; not waited.
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16])
 {
@@ -401,24 +424,15 @@ __device__ __forceinline__ unsigned long long row_vis(unsigned long long anc, in
     return d > 0 ? ((1ull << d) - 1ull) | (anc << d) : (d > -64 ? anc >> -d : 0ull);
 }
 
-// bits 8 j + c0 + e (e = 0, 1) -> bit 2 j + e
-__device__ __forceinline__ uint32_t thread_vis(unsigned long long w, int c0)
-{
-    unsigned long long x = (w >> c0) & 0x0303030303030303ull;
-    x = (x | (x >> 6)) & 0x000F000F000F000Full;
-    x = (x | (x >> 12)) & 0x000000FF000000FFull;
-    return (uint32_t)(x | (x >> 24)) & 0xFFFFu;
-}
-
-// Weights 2^(x * c + n) of the 16 scores a thread holds of row E / 2 (E = 0:
-// row A, E = 2: row B) of a half tile, packed to bf16 pairs; returns their sum.
-template <int E>
-__device__ __forceinline__ float exp_row(const uint32_t (&r)[32], float c, float n, uint32_t (&p)[8])
+// Weights 2^(x * c + n) of the 2 J scores a thread holds of row E / 2 (E = 0:
+// row A, E = 2: row B) of 8 J positions, packed to bf16 pairs; adds them to sum.
+template <int E, int J>
+__device__ __forceinline__ void exp_row(const uint32_t (&r)[4 * J], float c, float n, uint32_t (&p)[J],
+                                        uint64_t &sum)
 {
     const uint64_t c2 = pack2(c, c), n2 = pack2(n, n);
-    uint64_t sum = 0ull;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < J; ++j) {
         const uint64_t y = fma2(pack2(__uint_as_float(r[4 * j + E]), __uint_as_float(r[4 * j + E + 1])),
                                 c2, n2);
         float y0, y1;
@@ -428,31 +442,17 @@ __device__ __forceinline__ float exp_row(const uint32_t (&r)[32], float c, float
         p[j] = *reinterpret_cast<const uint32_t *>(&hv);
         sum = add2(sum, pack2(x0, x1));
     }
-    float a0, a1;
-    unpack2(sum, a0, a1);
-    return a0 + a1;
 }
 
-// Maximum of the 16 scores that a thread holds of row A (E = 0) or B (E = 2).
-template <int E>
-__device__ __forceinline__ float half_max(const uint32_t (&r)[32])
+// Maximum of the scores that a thread holds of row A (E = 0) or B (E = 2).
+template <int E, int J>
+__device__ __forceinline__ float part_max(const uint32_t (&r)[4 * J])
 {
     float m = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
+    for (int j = 0; j < J; ++j)
         m = max3f(m, __uint_as_float(r[4 * j + E]), __uint_as_float(r[4 * j + E + 1]));
     return m;
-}
-
-// Eight rows' P of one half tile (64 positions: a 128-byte row of the K-major,
-// 128-byte-swizzled P^T tile): `row` is this lane's row address, rx its row
-// index mod 8.
-__device__ __forceinline__ void store_p(uint32_t row, int rx, int lane, const uint32_t (&pk)[8])
-{
-#pragma unroll
-    for (int m = 0; m < 2; ++m)
-        stmatrix_x4(row + (uint32_t)(((4 * m + (lane >> 3)) ^ rx) << 4), pk[4 * m], pk[4 * m + 1],
-                    pk[4 * m + 2], pk[4 * m + 3]);
 }
 
 // The kernel's workspace, after the header and the counters.
@@ -768,33 +768,49 @@ __device__ __forceinline__ int active_units(int rows, int rq)
     return n;
 }
 
+// The kernel's three forms by the query rows of a CTA: up to 64 (one block,
+// two groups of four softmax warps), up to 128 (one block, eight warps), up
+// to 192 (two blocks, twelve warps).
+template <int N>
+struct Const {
+    static constexpr int value = N;
+};
+
+template <int MODE>
+struct Form {
+    static constexpr int NB = MODE == 2 ? 2 : 1;     // query blocks
+    static constexpr int NG = MODE == 0 ? 2 : 1;     // softmax groups
+    static constexpr int U = MODE + 1;               // softmax warps per lane quarter and group
+    static constexpr int U0 = MODE == 0 ? 1 : 2;     // of these in block 0
+    static constexpr int SVB = MODE == 2 ? 1 : 2;    // bf16 V slots
+    static constexpr int n_conv = kThreads / 32 - 4 - 4 * U * NG;   // converter warps, the last ones
+};
+
+template <int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ AttnQ8Args a,
-                    const __grid_constant__ TreeMasks masks, int n_split, int NG,
-                    int nodes_per_group, Q8Sync sy)
+                    const __grid_constant__ TreeMasks masks, int n_split, int nodes_per_group,
+                    Q8Sync sy)
 {
     const Q8Cache &kc = a.c;
     const int G = a.n_heads_q / a.n_heads_kv;
     const int node0 = blockIdx.z * nodes_per_group;
     const int T = min(nodes_per_group, a.n_tree - node0);
     const int R = G * T;
-    const int NB = R > kBlockM ? 2 : 1;
+    using F = Form<MODE>;
+    constexpr int NB = F::NB, NG = F::NG, U = F::U, SVB = F::SVB, n_conv = F::n_conv, NP = 2;
     const int R0 = R < kBlockM ? R : kBlockM, R1 = R - R0;
     // rows per lane quarter: a quarter of the block's, but at least 8 while
     // that needs no more warps (a warp takes 8 rows as fast as one), so that
     // the root node's rows 0..G-1, G <= 8, are the last block's first lanes
     const int rq0 = max((R0 + 3) / 4, min(R0, 8)), rq1 = max((R1 + 3) / 4, min(R1, 8));
-    const int u0 = (rq0 + 15) / 16, u1 = (rq1 + 15) / 16;
-    const int U = u0 + u1;  // softmax warps per lane quarter and group
     // (quarter, unit) pairs with query rows: their warps arrive on the barriers
     const int act0 = active_units(R0, rq0), act1 = active_units(R1, rq1);
     const bool rs_warp0 = a.root_scores != nullptr && node0 == 0;
-    const Layout lay = q8_layout(R, NG);
-    const int SK = lay.stages_k, SV = lay.stages_v, SVB = lay.stages_vb, r_pad = lay.r_pad;
-    const int n_conv = kThreads / 32 - 4 - 4 * U * NG;   // converter warps, the last ones
-    const int NP = lay.p_slots;
-    const int SI = NB == 2 ? 1 : NP;   // one block: S barriers of tile t are [t % SI], its slot t & 1
+    const Layout lay = q8_layout(R);
+    const int SK = lay.stages_k, SV = lay.stages_v, r_pad = lay.r_pad;
+    constexpr int SI = NB == 2 ? 1 : NP;   // one block: S barriers of tile t are [t % SI], its slot t & 1
 
     extern __shared__ unsigned char smem_raw[];
     unsigned char *base = reinterpret_cast<unsigned char *>(
@@ -924,8 +940,8 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 rv.next();
                 const uint32_t fb = smem_addr(&bar->full_v[s]);
                 const int tile = bar->tile_of[t & (kTileRing - 1)];
-                if (tile >= nq) {
-                    mbar_arrive(fb);   // a tail tile: the converters read it themselves
+                if (tile < 0 || tile >= nq) {
+                    mbar_arrive(fb);   // the end, or a tail tile: the converters read it themselves
                 } else {
                     mbar_arrive_expect_tx(fb, kRawBytes);
                     tma_load_3d_hint(smem_addr(sV + s * kRawBytes), &tmap_v, 0, tile * kTileN, g, fb, pol);
@@ -939,16 +955,21 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 if (lane == 0) {
                     const bool tail = tile >= nq;
                     bar->tile_of[i & (kTileRing - 1)] = tile;
-                    if (tile < 0)   // every group's end
-                        bar->tile_of[(i + 1) & (kTileRing - 1)] = bar->tile_of[(i + 2) & (kTileRing - 1)] = -1;
+                    if (tile < 0)   // (the second group's end)
+                        aux->scale_of[(i + 1) & (kTileRing - 1)][0].w = __int_as_float(kEndMark);
                     else
                         owner[tile] = (uint8_t)split;
+                    // context positions from the tile's first on
+                    const int left = tail ? kc.n_tail - (tile - nq) * kTileN : kc.n_q8 - tile * kTileN;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const uint32_t kb = (sc >> (8 * h)) & 0xFFu;
                         const uint32_t vb = kb == 255u ? 255u : (sc >> (16 + 8 * h)) & 0xFFu;
                         aux->scale_of[i & (kTileRing - 1)][h] =
-                            make_float4(q8_factor(kb), q8_log2(vb), q8_inverse(vb), 0.f);
+                            make_float4(q8_factor(kb), q8_log2(vb), q8_inverse(vb),
+                                        __int_as_float(tile < 0 ? kEndMark
+                                                                : min(max(left - 64 * h, -kTileN), 64) +
+                                                                      (tail ? kTailMark : 0)));
                     }
                     bar->entry_of[i & (kTileRing - 1)] = ke;
                     for (int part = 0; part < (tail ? 2 : 1); ++part, ++ke, rk.next()) {
@@ -967,9 +988,8 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                             k_tma = ke;
                         }   // a tail tile's slots, free now, are filled by the converters
                     }
-                    for (int j = 0; j < (tile < 0 ? 3 : 1); ++j)
-                        mbar_arrive(smem_addr(&bar->info[(i + j) & (kTileRing - 1)]));
-                    if (ok && vn < i)   // V one tile behind K
+                    mbar_arrive(smem_addr(&bar->info[i & (kTileRing - 1)]));
+                    while (ok && (vn < i || (vn == i && tile < 0)))   // V one tile behind K
                         ok = issue_v(vn++);
                 }
                 ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
@@ -1057,7 +1077,8 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
             const uint32_t qd0 = (uint32_t)sdesc_sw128(smem_addr(sQ1), 16, 1024);
             const bool leader = elect_one();
             // rb: S barrier of tile t; rf: of the tile before it in its slot
-            Ring rk(SK), rb(SI), rf(SI);
+            // rp: P^T slot of tile t - 2
+            Ring rk(SK), rb(SI), rf(SI), rp(2);
             for (int t = 0;; ++t) {
                 if (!warp_wait(smem_addr(&bar->full_k[rk.i]), rk.ph, abort, hdr))
                     break;
@@ -1084,6 +1105,11 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 const int k1 = rk.i;
                 if (two)
                     rk.next();
+                // one group: S(t) stands for its P^T slot, too (PV(t - 2) is done)
+                if (NG == 1 && t >= 2) {
+                    ok = ok && warp_wait(smem_addr(&bar->pv_done[rp.i]), rp.ph, abort, hdr);
+                    rp.next();
+                }
                 for (int b = 0; b < NB && ok; ++b) {
                     const int slot = NB == 2 ? b : (t & 1), sb = NB == 2 ? b : rb.i;
                     // the tile before it in this slot is in its readers' registers
@@ -1174,17 +1200,21 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
         const int ch = tid & 15, r0 = tid >> 4;
         const uint32_t c_dst = (uint32_t)((ch >> 3) * kBoxBytes + r0 * 128 + (((ch & 7) ^ (r0 & 7)) << 4));
         int met = 0;   // meetings of the converters over tail tiles
+        bool tail = true;
         Ring rv(SV), rvb(SVB), rpv(NP);   // rpv: PV of the tile before in the bf16 slot
         for (int t = 0;; ++t, rv.next(), rvb.next()) {
-            if (!warp_wait(smem_addr(&bar->info[t & (kTileRing - 1)]), (t >> 4) & 1, abort, hdr))
+            // tail tiles, if any, come first, and their keys before their values
+            if (tail) {
+                if (!warp_wait(smem_addr(&bar->info[t & (kTileRing - 1)]), (t >> 4) & 1, abort, hdr))
+                    break;
+                tail = __any_sync(0xffffffffu, bar->tile_of[t & (kTileRing - 1)] >= nq);
+                if (tail && warp >= 16 && !tail_keys(a, aux, sK, SK, g, nq, t, met, abort, hdr))
+                    break;
+            }
+            if (!warp_wait(smem_addr(&bar->full_v[rv.i]), rv.ph, abort, hdr))
                 break;
             const int tile = bar->tile_of[t & (kTileRing - 1)];
             if (tile < 0)
-                break;
-            const bool tail = __any_sync(0xffffffffu, tile >= nq);
-            if (tail && warp >= 16 && !tail_keys(a, aux, sK, SK, g, nq, t, met, abort, hdr))
-                break;
-            if (!warp_wait(smem_addr(&bar->full_v[rv.i]), rv.ph, abort, hdr))
                 break;
             if (t >= SVB) {
                 if (!warp_wait(smem_addr(&bar->pv_done[rpv.i]), rpv.ph, abort, hdr))
@@ -1285,8 +1315,8 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
             // ------------------------------------------------ softmax
             const int q = warp & 3, j = NG == 2 ? 0 : (warp - 4) >> 2;
             const int grp = NG == 2 ? (warp - 4) >> 2 : 0;
-            const int b = j < u0 ? 0 : 1;
-            const int lb = 16 * (b == 0 ? j : j - u0);  // unit's first lane in the quarter
+            const int b = j < F::U0 ? 0 : 1;
+            const int lb = 16 * (b == 0 ? j : j - F::U0);  // unit's first lane in the quarter
             const int Rb = b == 0 ? R0 : R1, rqb = b == 0 ? rq0 : rq1;
             const int iA = lb + (lane >> 2), iB = iA + 8;
             const bool vA = iA < rqb && q * rqb + iA < Rb;
@@ -1322,91 +1352,143 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
             // S barriers and P^T slots, fixed for a group (phases alternate) or by
             // tile
             Ring rsb(NG == 2 || NB == 2 ? 1 : 2), rps(NG == 2 ? 1 : 2);
-            for (int t = grp; hasA; t += NG, rsb.next(), rps.next()) {
-                const int ps = NG == 2 ? grp : rps.i;
-                const int slot = NB == 2 ? b : (t & 1), sb = NB == 2 ? b : (NG == 2 ? grp : rsb.i);
-                if (!warp_wait(smem_addr(&bar->s_full[sb]), rsb.ph, abort, hdr)) {
-                    ok = false;
-                    break;
-                }
-                const int tile = bar->tile_of[t & (kTileRing - 1)];
-                if (tile < 0)
-                    break;
-                const bool tail = tile >= nq;
-                // context positions from the half tile's first on
-                int left = tail ? kc.n_tail - (tile - nq) * kTileN : kc.n_q8 - tile * kTileN;
-                const float4 *scl = aux->scale_of[t & (kTileRing - 1)];
-                uint32_t atA = p_rowA + 2 * ps * p_stepA, atB = p_rowB + 2 * ps * p_stepB;
-                // the halves are the tile's two scale blocks; one copy of the code
-                // serves both (the loop must stay inside the instruction cache)
-#pragma unroll 1
-                for (int h = 0; h < 2; ++h, left -= 64) {
-                    tc_fence_after();
-                    uint32_t r[32];
-                    tmem_ld16x256_x8(s_addr + 128 * slot + 64 * h, r);
-                    if (h == 1) {
-                        // S is in registers: QK of a later tile may overwrite it
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0)
-                            mbar_arrive(smem_addr(&bar->s_free[sb]));
-                    }
-                    const float4 sc = scl[h];
-                    // factor of the scores: never zero, as a masked score is -inf
-                    constexpr float kTiny = 1.17549435e-38f;
-                    const float cA = fmaxf(rsA * sc.x, kTiny), cB = fmaxf(rsB * sc.x, kTiny);
-                    if (left < 64) {
-                        const unsigned long long wA = row_vis(tail ? ancA : 0ull, left);
-                        const unsigned long long wB = row_vis(tail ? ancB : 0ull, left);
-                        const uint32_t visA = thread_vis(wA, c0), visB = thread_vis(wB, c0);
+            // Part of a half tile in registers (8 J positions, from the half's
+            // 32 odd on): weights to P^T
+            auto part = [&](auto &r, auto jc, int odd, int left, int t, int h, float cA, float cB, float ve,
+                            uint64_t &sA, uint64_t &sB, uint32_t atA, uint32_t atB) {
+                constexpr int J = decltype(jc)::value;
+                if (left < 64 || left > kTailMark / 2) {
+                    // masked: the first positions of the half are context, then (a
+                    // tail tile) come the tree's, of which a row sees its path
+                    const bool tail = left > kTailMark / 2;
+                    const int d = tail ? left - kTailMark : left;
+                    const unsigned long long wA = row_vis(tail ? ancA : 0ull, d);
+                    const unsigned long long wB = row_vis(tail ? ancB : 0ull, d);
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            if (!((visA >> k) & 1u))
-                                r[4 * (k >> 1) + (k & 1)] = __float_as_uint(-INFINITY);
-                            if (!((visB >> k) & 1u))
-                                r[4 * (k >> 1) + 2 + (k & 1)] = __float_as_uint(-INFINITY);
+                    for (int w = 0; w < J / 4; ++w) {
+                        const uint32_t qA = (uint32_t)(wA >> (32 * (odd + w))) >> c0;
+                        const uint32_t qB = (uint32_t)(wB >> (32 * (odd + w))) >> c0;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const int bit = 8 * (k >> 1) + (k & 1), e = 16 * w + 4 * (k >> 1) + (k & 1);
+                            if (!((qA >> bit) & 1u))
+                                r[e] = __float_as_uint(-INFINITY);
+                            if (!((qB >> bit) & 1u))
+                                r[e + 2] = __float_as_uint(-INFINITY);
                         }
                     }
                     if (tail) {
                         // a row that sees a value that is no number
                         const unsigned long long bw =
                             bar->bad[t & 3][2 * h] | ((unsigned long long)bar->bad[t & 3][2 * h + 1] << 32);
-                        if (row_vis(ancA, left) & bw)
+                        if (wA & bw)
                             lA = __uint_as_float(0x7FC00000u);
-                        if (row_vis(ancB, left) & bw)
+                        if (wB & bw)
                             lB = __uint_as_float(0x7FC00000u);
                     }
-                    // a row that has seen nothing yet takes this half's max,
+                }
+                if (fresh) {
+                    // a row that has seen nothing yet takes this part's max,
                     // rounded up to an integer, as its reference
-                    if (fresh) {
-                        float yA = half_max<0>(r) * cA, yB = half_max<2>(r) * cB;
-                        yA = fmaxf(yA, __shfl_xor_sync(0xffffffffu, yA, 1));
-                        yB = fmaxf(yB, __shfl_xor_sync(0xffffffffu, yB, 1));
-                        yA = fmaxf(yA, __shfl_xor_sync(0xffffffffu, yA, 2));
-                        yB = fmaxf(yB, __shfl_xor_sync(0xffffffffu, yB, 2));
-                        if (mA == -INFINITY)
-                            mA = ceilf(yA);
-                        if (mB == -INFINITY)
-                            mB = ceilf(yB);
-                        nmA = mA == -INFINITY ? 0.f : -mA;
-                        nmB = mB == -INFINITY ? 0.f : -mB;
-                        fresh = __any_sync(0xffffffffu, (vA && mA == -INFINITY) || (vB && mB == -INFINITY));
+                    float yA = part_max<0, J>(r) * cA, yB = part_max<2, J>(r) * cB;
+                    yA = fmaxf(yA, __shfl_xor_sync(0xffffffffu, yA, 1));
+                    yB = fmaxf(yB, __shfl_xor_sync(0xffffffffu, yB, 1));
+                    yA = fmaxf(yA, __shfl_xor_sync(0xffffffffu, yA, 2));
+                    yB = fmaxf(yB, __shfl_xor_sync(0xffffffffu, yB, 2));
+                    if (mA == -INFINITY)
+                        mA = ceilf(yA);
+                    if (mB == -INFINITY)
+                        mB = ceilf(yB);
+                    nmA = mA == -INFINITY ? 0.f : -mA;
+                    nmB = mB == -INFINITY ? 0.f : -mB;
+                    fresh = __any_sync(0xffffffffu, (vA && mA == -INFINITY) || (vB && mB == -INFINITY));
+                }
+                uint32_t pA[J], pB[J];
+                exp_row<0, J>(r, cA, nmA + ve, pA, sA);
+                if (hasB)
+                    exp_row<2, J>(r, cB, nmB + ve, pB, sB);
+                if (NG == 2 && h == 0 && t >= 2 &&
+                    !warp_wait(smem_addr(&bar->pv_done[grp]), rps.ph ^ 1, abort, hdr))
+                    ok = false;
+#pragma unroll
+                for (int w = 0; w < J / 4; ++w)
+                    stmatrix_x4(atA + (uint32_t)(((4 * (odd + w) + (lane >> 3)) ^ rxA) << 4), pA[4 * w],
+                                pA[4 * w + 1], pA[4 * w + 2], pA[4 * w + 3]);
+                if (hasB) {
+#pragma unroll
+                    for (int w = 0; w < J / 4; ++w)
+                        stmatrix_x4(atB + (uint32_t)(((4 * (odd + w) + (lane >> 3)) ^ rxB) << 4), pB[4 * w],
+                                    pB[4 * w + 1], pB[4 * w + 2], pB[4 * w + 3]);
+                }
+            };
+            for (int t = grp; hasA; t += NG, rsb.next(), rps.next()) {
+                const int ps = NG == 2 ? grp : rps.i;
+                const int slot = NB == 2 ? b : (t & 1), sb = NB == 2 ? b : (NG == 2 ? grp : rsb.i);
+                // (with one group S(t) in place also says that this P^T slot is
+                // free; with two that would tie a group to its own PV)
+                if (!warp_wait(smem_addr(&bar->s_full[sb]), rsb.ph, abort, hdr)) {
+                    ok = false;
+                    break;
+                }
+                const float4 *scl = aux->scale_of[t & (kTileRing - 1)];
+                float4 sc = scl[0];
+                if (__float_as_int(sc.w) == kEndMark)
+                    break;
+                uint32_t atA = p_rowA + 2 * ps * p_stepA, atB = p_rowB + 2 * ps * p_stepB;
+                tc_fence_after();
+                const uint32_t s0 = s_addr + 128 * slot;
+                // The halves are the tile's two scale blocks; one copy of the code
+                // serves both (the loop must stay inside the instruction cache).
+                // With a warp or two per sub-partition a half at once has the
+                // longer independent stretches; with more, quarters, each on its
+                // way while the one before is turned to weights, hide the loads
+                // (T = 13: 66 us against 71, T = 40: 98 against 104).
+                uint32_t r0[NG == 2 ? 32 : 16], r1[16];
+                if constexpr (NG == 1) {
+                    tmem_ld16x256_x4(s0, r0);
+                    tmem_ld_wait16(r0);
+                }
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    if constexpr (NG == 1)
+                        tmem_ld16x256_x4(s0 + 64 * h + 32, r1);
+                    else
+                        tmem_ld16x256_x8(s0 + 64 * h, r0);
+                    // factor of the scores: never zero, as a masked score is -inf
+                    constexpr float kTiny = 1.17549435e-38f;
+                    const float cA = fmaxf(rsA * sc.x, kTiny), cB = fmaxf(rsB * sc.x, kTiny);
+                    const int left = __float_as_int(sc.w);
+                    const float ve = sc.y, vi = sc.z;
+                    uint64_t sA = 0ull, sB = 0ull;
+                    if constexpr (NG == 1) {
+                        part(r0, Const<4>(), 0, left, t, h, cA, cB, ve, sA, sB, atA, atB);
+                        tmem_ld_wait16(r1);
                     }
-                    uint32_t pA[8], pB[8];
-                    lA += exp_row<0>(r, cA, nmA + sc.y, pA) * sc.z;
-                    if (hasB)
-                        lB += exp_row<2>(r, cB, nmB + sc.y, pB) * sc.z;
-                    // this P^T tile is free once PV(t - NP) is done
-                    if (h == 0 && t >= NP &&
-                        !warp_wait(smem_addr(&bar->pv_done[ps]), rps.ph ^ 1, abort, hdr)) {
-                        ok = false;
-                        break;
+                    if (h == 0) {
+                        if constexpr (NG == 1)
+                            tmem_ld16x256_x4(s0 + 64, r0);
+                        sc = scl[1];
+                    } else {
+                        // S is in registers: QK of a later tile may overwrite it
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(smem_addr(&bar->s_free[sb]));
                     }
-                    store_p(atA, rxA, lane, pA);
-                    if (hasB)
-                        store_p(atB, rxB, lane, pB);
+                    if constexpr (NG == 1)
+                        part(r1, Const<4>(), 1, left, t, h, cA, cB, ve, sA, sB, atA, atB);
+                    else
+                        part(r0, Const<8>(), 0, left, t, h, cA, cB, ve, sA, sB, atA, atB);
+                    float a0, a1;
+                    unpack2(sA, a0, a1);
+                    lA += (a0 + a1) * vi;
+                    unpack2(sB, a0, a1);
+                    lB += (a0 + a1) * vi;
                     atA += p_stepA;
                     atB += p_stepB;
+                    if constexpr (NG == 1)
+                        if (h == 0)
+                            tmem_ld_wait16(r0);
                 }
                 if (!ok)
                     break;
@@ -1534,7 +1616,7 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
 }
 
 struct T128Plan {
-    int n_split, node_groups, nodes_per_group, groups;
+    int n_split, node_groups, nodes_per_group;
     size_t part, flags, owner, total;
 };
 
@@ -1555,7 +1637,6 @@ T128Plan q8_plan(int n_heads_q, int n_heads_kv, int n_q8, int n_tail, int n_tree
     p.n_split = want > 255 ? 255 : want;
     const size_t n_gz = (size_t)n_heads_kv * p.node_groups;
     p.part = kHeaderBytes + kQ8SyncBytes;
-    p.groups = q8_groups(p.nodes_per_group * G);
     p.flags = p.part + align_up((size_t)p.n_split * n_tree * n_heads_q * (kD + 2) * sizeof(float), 256);
     p.owner = p.flags + align_up((size_t)p.n_split * n_gz * sizeof(int32_t), 256);
     p.total = p.owner + align_up(n_gz * n_tiles, 256);
@@ -1607,8 +1688,13 @@ cudaError_t attn_q8_t128_launch(const AttnQ8Args &a, const TreeMasks &masks, int
         (!encode_codes_map(&mk, a.c.k8, a.c.n_q8, a.c.q8_cap, a.n_heads_kv, true) ||
          !encode_codes_map(&mv, a.c.v8, a.c.n_q8, a.c.q8_cap, a.n_heads_kv, false)))
         return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(attn_q8_t128_kernel,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemLimit);
+    // by the rows of the first node group, the largest
+    const int rows = (a.n_heads_q / a.n_heads_kv) * p.nodes_per_group;
+    const auto kernel = rows <= 64        ? attn_q8_t128_kernel<0>
+                        : rows <= kBlockM ? attn_q8_t128_kernel<1>
+                                          : attn_q8_t128_kernel<2>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)kSmemLimit);
     if (e != cudaSuccess)
         return e;
     char *ws = reinterpret_cast<char *>(a.workspace);
@@ -1629,8 +1715,7 @@ cudaError_t attn_q8_t128_launch(const AttnQ8Args &a, const TreeMasks &masks, int
     at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, attn_q8_t128_kernel, mk, mv, a, masks, p.n_split, p.groups,
-                           p.nodes_per_group, sy);
+    e = cudaLaunchKernelEx(&cfg, kernel, mk, mv, a, masks, p.n_split, p.nodes_per_group, sy);
     if (e == cudaSuccess)
         e = cudaGetLastError();
     if (e == cudaSuccess)
