@@ -83,6 +83,7 @@ constexpr int kBarOut = 2;                   // named barrier: O^T staged, or me
 constexpr int kTileRing = 16;                // entries of the tile rings (> any role's lead)
 static_assert(kTileRing == 1 << 4, "indexed by shifts");
 constexpr int kBarQLoads = 3;                // named barrier: the query rows are read
+constexpr int kBarScales = 4;                // named barrier: the scale bytes are in shared memory
 constexpr int kQLoadThreads = 32 * 9;        // warps 4-11 arrive, the producer warp waits
 constexpr int kMaxGz = 256;                  // (KV head, node group) pairs: counters in the workspace
 static_assert(kMaxGz * 16 <= (int)kQ8SyncBytes, "counters fit their region");
@@ -132,7 +133,7 @@ constexpr size_t kAuxBytes = (sizeof(Aux) + 1023) / 1024 * 1024;
 
 struct Layout {
     int r_pad, stages_k, stages_v, stages_vb;
-    size_t q1_off, p_off, vb_off, k_off, v_off, aux_off, smem_bytes;
+    size_t q1_off, p_off, vb_off, k_off, v_off, sc_off, aux_off, smem_bytes;
 };
 
 __host__ __device__ inline int q8_row_of(int n, int R)
@@ -140,7 +141,7 @@ __host__ __device__ inline int q8_row_of(int n, int R)
     return R > kBlockM ? (n < kBlockM ? (R - kBlockM) + n : n - kBlockM) : n;
 }
 
-__host__ __device__ inline Layout q8_layout(int rows)
+__host__ __device__ inline Layout q8_layout(int rows, int n_blk)
 {
     Layout L;
     L.r_pad = (rows + 15) / 16 * 16;
@@ -150,14 +151,17 @@ __host__ __device__ inline Layout q8_layout(int rows)
     L.vb_off = L.p_off + (size_t)L.r_pad * 512 + 1024;
     L.stages_vb = rows > kBlockM ? 1 : 2;
     L.k_off = L.vb_off + (size_t)L.stages_vb * kVbBytes;
-    const size_t fixed = 1024 + L.k_off + kAuxBytes;
-    int stages = (int)((kSmemLimit - fixed) / kRawBytes);
+    // the scale bytes of every block of the head, K's then V's
+    const size_t sc_bytes = ((size_t)2 * n_blk + 127) / 128 * 128;
+    const size_t fixed = 1024 + L.k_off + sc_bytes + kAuxBytes;
+    int stages = fixed > kSmemLimit ? 0 : (int)((kSmemLimit - fixed) / kRawBytes);
     stages = stages > 2 * kMaxStages ? 2 * kMaxStages : stages;
     L.stages_v = stages / 2;
     L.stages_k = stages - L.stages_v;   // at least 2: a tail tile takes two
     L.v_off = L.k_off + (size_t)L.stages_k * kRawBytes;
     L.aux_off = L.v_off + (size_t)L.stages_v * kRawBytes;
-    L.smem_bytes = 1024 + L.aux_off + kAuxBytes;
+    L.sc_off = L.aux_off + kAuxBytes;
+    L.smem_bytes = 1024 + L.sc_off + sc_bytes;
     return L;
 }
 
@@ -402,17 +406,21 @@ __device__ __forceinline__ float two_to(int e) { return __uint_as_float((uint32_
 
 // Four codes -> two bf16 pairs (low codes first).  The seven low bits of a
 // code, shifted to bf16's exponent and mantissa, are its magnitude times
-// 2^-120 (subnormals included); NaN codes read as 480.
+// 2^-120 (subnormals included); NaN codes read as 480.  With a code in the
+// low byte of each half word, code * 16 + sign * 30720 puts the magnitude at
+// bit 4 and the sign at bit 15: two multiply-adds a pair, which leave the
+// integer pipe, the busiest one, to the softmax.
+__device__ __forceinline__ uint32_t code_pair(uint32_t two)
+{
+    const uint32_t a = two * 16u + (two & 0x00800080u) * 240u;
+    const uint32_t f = 0x7B807B80u;   // 2^120
+    const __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&a),
+                                     *reinterpret_cast<const __nv_bfloat162 *>(&f));
+    return *reinterpret_cast<const uint32_t *>(&x);
+}
 __device__ __forceinline__ uint2 codes_to_bf16(uint32_t w)
 {
-    const uint32_t lo = __byte_perm(w, 0u, 0x1404), hi = __byte_perm(w, 0u, 0x3424);
-    const uint32_t a = (lo & 0x80008000u) | ((lo & 0x7F007F00u) >> 4);
-    const uint32_t b = (hi & 0x80008000u) | ((hi & 0x7F007F00u) >> 4);
-    const uint32_t f = 0x7B807B80u;   // 2^120
-    const __nv_bfloat162 fb = *reinterpret_cast<const __nv_bfloat162 *>(&f);
-    const __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&a), fb);
-    const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&b), fb);
-    return make_uint2(*reinterpret_cast<const uint32_t *>(&x), *reinterpret_cast<const uint32_t *>(&y));
+    return make_uint2(code_pair(__byte_perm(w, 0u, 0x4140)), code_pair(__byte_perm(w, 0u, 0x4342)));
 }
 
 // A half tile's 64 positions that a row sees: the first d, then the bits of
@@ -808,7 +816,8 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
     // (quarter, unit) pairs with query rows: their warps arrive on the barriers
     const int act0 = active_units(R0, rq0), act1 = active_units(R1, rq1);
     const bool rs_warp0 = a.root_scores != nullptr && node0 == 0;
-    const Layout lay = q8_layout(R);
+    const int n_blk = kc.n_q8 / kQ8Block;
+    const Layout lay = q8_layout(R, n_blk);
     const int SK = lay.stages_k, SV = lay.stages_v, r_pad = lay.r_pad;
     constexpr int SI = NB == 2 ? 1 : NP;   // one block: S barriers of tile t are [t % SI], its slot t & 1
 
@@ -821,6 +830,7 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
     unsigned char *sK = base + lay.k_off;
     unsigned char *sV = base + lay.v_off;
     Aux *aux = reinterpret_cast<Aux *>(base + lay.aux_off);
+    uint8_t *s_scale = base + lay.sc_off;   // [2][n_blk]: K's bytes, V's
     Bars *bar = &aux->bar;
     WorkspaceHeader *hdr = reinterpret_cast<WorkspaceHeader *>(a.workspace);
     volatile uint32_t *abort = &bar->abort;
@@ -895,38 +905,47 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
             // ------------------------------------------------ TMA producer
             // (the query rows first: not behind every CTA's first ring of tiles)
             named_bar_sync(kBarQLoads, kQLoadThreads);
+            named_bar_sync(kBarScales, 32 * (n_conv + 1));
             // Tiles are taken from the end of the cache backwards, four per
-            // claim: lanes 0-3 hold a round's tiles and their scale bytes while
-            // lane 0 issues them, and the next round's claim is on its way.
-            // (Claimed and looked up one by one, the two trips to memory came to
-            // 3600 cycles a tile, more than twice the tile's stream.)
+            // claim: lanes 0-3 post a round's tiles (index, scales), lane 0 issues
+            // their loads, and the next round's claim is on its way meanwhile
             constexpr int kRound = 4;
             auto tile_at = [&](int k) { return n_tiles_all - 1 - k; };
             int32_t *ctr = sy.sync + 4 * gz;
-            const uint8_t *ksc = kc.k_scale + (int64_t)g * (kc.q8_cap / kQ8Block);
-            const uint8_t *vsc = kc.v_scale + (int64_t)g * (kc.q8_cap / kQ8Block);
-            const int n_blk = kc.n_q8 / kQ8Block;
-            // scale bytes of a tile's two blocks (127, a factor of one, past the
-            // last block and on a tail tile): k, k, v, v
-            auto scales = [&](int tile) {
-                const int b0 = 2 * tile;
-                uint32_t w = 0x7F7F7F7Fu;
-                if (lane < kRound && tile >= 0 && b0 < n_blk) {
-                    const bool two = b0 + 1 < n_blk;
-                    w = __ldg(ksc + b0) | ((two ? (uint32_t)__ldg(ksc + b0 + 1) : 127u) << 8) |
-                        ((uint32_t)__ldg(vsc + b0) << 16) |
-                        ((two ? (uint32_t)__ldg(vsc + b0 + 1) : 127u) << 24);
-                }
-                return w;
-            };
             auto claim = [&](int n) { return lane == 0 ? atomicAdd(&ctr[0], n) : 0; };
+            uint8_t *owner = sy.owner + (size_t)gz * n_tiles_all;
+            // tile t of this CTA, from lane t % kRound
+            auto post = [&](int t, int tile) {
+                if (lane >= kRound)
+                    return;
+                const int at = t & (kTileRing - 1);
+                const bool tail = tile >= nq;
+                bar->tile_of[at] = max(tile, -1);
+                // context positions from the tile's first on
+                const int left = tail ? kc.n_tail - (tile - nq) * kTileN : kc.n_q8 - tile * kTileN;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    // (127, a factor of one, past the last block and on a tail tile)
+                    const int b = 2 * tile + h;
+                    const bool have = tile >= 0 && b < n_blk;
+                    const uint32_t kb = have ? s_scale[b] : 127u;
+                    const uint32_t vb = kb == 255u ? 255u : (have ? s_scale[n_blk + b] : 127u);
+                    aux->scale_of[at][h] =
+                        make_float4(q8_factor(kb), q8_log2(vb), q8_inverse(vb),
+                                    __int_as_float(tile < 0 ? kEndMark
+                                                            : min(max(left - 64 * h, -kTileN), 64) +
+                                                                  (tail ? kTailMark : 0)));
+                }
+                if (tile >= 0)
+                    owner[tile] = (uint8_t)split;
+            };
             // the split's own tile is the first; the round's others are claimed
             int base = claim(kRound - 1);
             const int first = __shfl_sync(0xffffffffu, base, 0);
             int my_tile = lane == 0 ? tile_at(split) : tile_at(n_split + first + lane - 1);
-            uint32_t my_sc = scales(my_tile);
             base = claim(kRound);
-            uint8_t *owner = sy.owner + (size_t)gz * n_tiles_all;
+            post(lane, my_tile);
+            __syncwarp();
             const uint64_t pol = l2_evict_first_policy();
             Ring rk(SK), rv(SV);
             int ke = 0;             // K ring entries used
@@ -951,27 +970,10 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
             };
             for (int i = 0; ok && more; ++i) {
                 const int tile = max(-1, __shfl_sync(0xffffffffu, my_tile, i % kRound));
-                const uint32_t sc = __shfl_sync(0xffffffffu, my_sc, i % kRound);
                 if (lane == 0) {
                     const bool tail = tile >= nq;
-                    bar->tile_of[i & (kTileRing - 1)] = tile;
-                    if (tile < 0)   // (the second group's end)
-                        aux->scale_of[(i + 1) & (kTileRing - 1)][0].w = __int_as_float(kEndMark);
-                    else
-                        owner[tile] = (uint8_t)split;
-                    // context positions from the tile's first on
-                    const int left = tail ? kc.n_tail - (tile - nq) * kTileN : kc.n_q8 - tile * kTileN;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint32_t kb = (sc >> (8 * h)) & 0xFFu;
-                        const uint32_t vb = kb == 255u ? 255u : (sc >> (16 + 8 * h)) & 0xFFu;
-                        aux->scale_of[i & (kTileRing - 1)][h] =
-                            make_float4(q8_factor(kb), q8_log2(vb), q8_inverse(vb),
-                                        __int_as_float(tile < 0 ? kEndMark
-                                                                : min(max(left - 64 * h, -kTileN), 64) +
-                                                                      (tail ? kTailMark : 0)));
-                    }
-                    bar->entry_of[i & (kTileRing - 1)] = ke;
+                    if (tail)
+                        bar->entry_of[i & (kTileRing - 1)] = ke;
                     for (int part = 0; part < (tail ? 2 : 1); ++part, ++ke, rk.next()) {
                         const int s = rk.i;
                         if (ke >= SK && !lane_wait(smem_addr(&bar->empty_k[s]), rk.ph ^ 1, abort, hdr)) {
@@ -980,6 +982,8 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                         }
                         const uint32_t fb = smem_addr(&bar->full_k[s]);
                         if (tile < 0) {
+                            // (the second group's end may lie in a round of its own)
+                            aux->scale_of[(i + 1) & (kTileRing - 1)][0].w = __int_as_float(kEndMark);
                             mbar_arrive(fb);   // no tile left: the QK issuer passes it on
                         } else if (!tail) {
                             mbar_arrive_expect_tx(fb, kRawBytes);
@@ -994,11 +998,11 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 }
                 ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
                 more = tile >= 0;
-                if (i % kRound == kRound - 1) {
+                if (more && i % kRound == kRound - 1) {
                     my_tile = tile_at(n_split + __shfl_sync(0xffffffffu, base, 0) + lane);
-                    my_sc = scales(my_tile);
-                    if (more)
-                        base = claim(kRound);
+                    base = claim(kRound);
+                    post(i + 1 + lane, my_tile);
+                    __syncwarp();
                 }
             }
             if (lane == 0 && *abort) {
@@ -1195,6 +1199,17 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
     } else if (warp >= kThreads / 32 - n_conv) {
         // ------------------------------------------------ converters
         const int tid = threadIdx.x - (kThreads - 32 * n_conv), rows = 2 * n_conv;   // rows per step
+        // every scale byte of the head, for the producer (one look-up per tile
+        // in HBM would cost it more than the tile's stream)
+        {
+            const uint8_t *ksc = kc.k_scale + (int64_t)g * (kc.q8_cap / kQ8Block);
+            const uint8_t *vsc = kc.v_scale + (int64_t)g * (kc.q8_cap / kQ8Block);
+            for (int i = tid; i < n_blk; i += 32 * n_conv) {
+                s_scale[i] = __ldg(ksc + i);
+                s_scale[n_blk + i] = __ldg(vsc + i);
+            }
+            named_bar_arrive(kBarScales, 32 * (n_conv + 1));
+        }
         // this thread's share of V's codes: a column chunk and every `rows`-th
         // row, all with the same row mod 8
         const int ch = tid & 15, r0 = tid >> 4;
@@ -1670,7 +1685,9 @@ bool attn_q8_t128_eligible(int n_heads_q, int n_heads_kv, int head_dim, int n_q8
         return false;
     const T128Plan p = q8_plan(n_heads_q, n_heads_kv, n_q8, n_tail, n_tree, num_sms);
     const long long gz = (long long)n_heads_kv * p.node_groups;
-    return gz <= kMaxGz && gz * p.n_split <= num_sms;
+    // the scale bytes of a long head leave room for the rings
+    const Layout lay = q8_layout(n_heads_q / n_heads_kv * p.nodes_per_group, n_q8 / kQ8Block);
+    return gz <= kMaxGz && gz * p.n_split <= num_sms && lay.stages_k >= 2 && lay.stages_v >= 1;
 }
 
 size_t attn_q8_t128_workspace_bytes(int n_heads_q, int n_heads_kv, int n_q8, int n_tail, int n_tree,
