@@ -1240,21 +1240,22 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
             if (!tail) {
                 const unsigned char *src = sV + rv.i * kRawBytes + 8 * tid;
                 unsigned char *dst = vb + c_dst;
-                // four steps' loads before their stores (which could alias them
-                // as far as the compiler knows); 16 steps, or 8, of four each
+                // two steps' loads before their stores (which could alias them as
+                // far as the compiler knows); more at once is slower, as the code
+                // then drives the softmax's out of the instruction cache
 #pragma unroll 1
-                for (int r = r0; r < kTileN; r += 4 * rows) {
-                    uint2 w[4];
+                for (int r = r0; r < kTileN; r += 2 * rows) {
+                    uint2 w[2];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
+                    for (int i = 0; i < 2; ++i)
                         w[i] = *reinterpret_cast<const uint2 *>(src + i * rows * kD);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < 2; ++i) {
                         const uint2 x = codes_to_bf16(w[i].x), y = codes_to_bf16(w[i].y);
                         *reinterpret_cast<uint4 *>(dst + i * rows * 128) = make_uint4(x.x, x.y, y.x, y.y);
                     }
-                    src += 4 * rows * kD;
-                    dst += 4 * rows * 128;
+                    src += 2 * rows * kD;
+                    dst += 2 * rows * 128;
                 }
             } else if (warp >= 16) {
                 tail_values(a, bar, vb, g, nq, tile, t);
@@ -1369,10 +1370,11 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
             Ring rsb(NG == 2 || NB == 2 ? 1 : 2), rps(NG == 2 ? 1 : 2);
             // Part of a half tile in registers (8 J positions, from the half's
             // 32 odd on): weights to P^T
-            auto part = [&](auto &r, auto jc, int odd, int left, int t, int h, float cA, float cB, float ve,
+            auto part = [&](auto &r, auto jc, auto special, int odd, int left, int t, int h, float cA, float cB, float ve,
                             uint64_t &sA, uint64_t &sB, uint32_t atA, uint32_t atB) {
                 constexpr int J = decltype(jc)::value;
-                if (left < 64 || left > kTailMark / 2) {
+                constexpr bool kSpecial = decltype(special)::value != 0;
+                if (kSpecial && (left < 64 || left > kTailMark / 2)) {
                     // masked: the first positions of the half are context, then (a
                     // tail tile) come the tree's, of which a row sees its path
                     const bool tail = left > kTailMark / 2;
@@ -1402,7 +1404,7 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                             lB = __uint_as_float(0x7FC00000u);
                     }
                 }
-                if (fresh) {
+                if (kSpecial && fresh) {
                     // a row that has seen nothing yet takes this part's max,
                     // rounded up to an integer, as its reference
                     float yA = part_max<0, J>(r) * cA, yB = part_max<2, J>(r) * cB;
@@ -1436,6 +1438,61 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                                     pB[4 * w + 1], pB[4 * w + 2], pB[4 * w + 3]);
                 }
             };
+            // One tile's scores to weights.  The halves are its two scale blocks;
+            // one copy of the code serves both (the loop must stay inside the
+            // instruction cache).  With a warp or two per sub-partition a half at
+            // once has the longer independent stretches; with more, quarters, each
+            // on its way while the one before is turned to weights, hide the loads
+            // (T = 13: 66 us against 71, T = 40: 98 against 104).
+            auto pass = [&](auto special, const float4 *scl, uint32_t s0, int t, uint32_t atA, uint32_t atB,
+                            uint32_t bar_free) {
+                uint32_t r0[NG == 2 ? 32 : 16], r1[16];
+                if constexpr (NG == 1) {
+                    tmem_ld16x256_x4(s0, r0);
+                    tmem_ld_wait16(r0);
+                }
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    const float4 sc = scl[h];
+                    if constexpr (NG == 1)
+                        tmem_ld16x256_x4(s0 + 64 * h + 32, r1);
+                    else
+                        tmem_ld16x256_x8(s0 + 64 * h, r0);
+                    // factor of the scores: never zero, as a masked score is -inf
+                    constexpr float kTiny = 1.17549435e-38f;
+                    const float cA = fmaxf(rsA * sc.x, kTiny), cB = fmaxf(rsB * sc.x, kTiny);
+                    const int left = __float_as_int(sc.w);
+                    uint64_t sA = 0ull, sB = 0ull;
+                    if constexpr (NG == 1) {
+                        part(r0, Const<4>(), special, 0, left, t, h, cA, cB, sc.y, sA, sB, atA, atB);
+                        tmem_ld_wait16(r1);
+                    }
+                    if (h == 0) {
+                        if constexpr (NG == 1)
+                            tmem_ld16x256_x4(s0 + 64, r0);
+                    } else {
+                        // S is in registers: QK of a later tile may overwrite it
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(bar_free);
+                    }
+                    if constexpr (NG == 1)
+                        part(r1, Const<4>(), special, 1, left, t, h, cA, cB, sc.y, sA, sB, atA, atB);
+                    else
+                        part(r0, Const<8>(), special, 0, left, t, h, cA, cB, sc.y, sA, sB, atA, atB);
+                    float a0, a1;
+                    unpack2(sA, a0, a1);
+                    lA += (a0 + a1) * sc.z;
+                    unpack2(sB, a0, a1);
+                    lB += (a0 + a1) * sc.z;
+                    atA += p_stepA;
+                    atB += p_stepB;
+                    if constexpr (NG == 1)
+                        if (h == 0)
+                            tmem_ld_wait16(r0);
+                }
+            };
             for (int t = grp; hasA; t += NG, rsb.next(), rps.next()) {
                 const int ps = NG == 2 ? grp : rps.i;
                 const int slot = NB == 2 ? b : (t & 1), sb = NB == 2 ? b : (NG == 2 ? grp : rsb.i);
@@ -1446,65 +1503,16 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     break;
                 }
                 const float4 *scl = aux->scale_of[t & (kTileRing - 1)];
-                float4 sc = scl[0];
-                if (__float_as_int(sc.w) == kEndMark)
+                const int w0 = __float_as_int(scl[0].w), w1 = __float_as_int(scl[1].w);
+                if (w0 == kEndMark)
                     break;
-                uint32_t atA = p_rowA + 2 * ps * p_stepA, atB = p_rowB + 2 * ps * p_stepB;
                 tc_fence_after();
-                const uint32_t s0 = s_addr + 128 * slot;
-                // The halves are the tile's two scale blocks; one copy of the code
-                // serves both (the loop must stay inside the instruction cache).
-                // With a warp or two per sub-partition a half at once has the
-                // longer independent stretches; with more, quarters, each on its
-                // way while the one before is turned to weights, hide the loads
-                // (T = 13: 66 us against 71, T = 40: 98 against 104).
-                uint32_t r0[NG == 2 ? 32 : 16], r1[16];
-                if constexpr (NG == 1) {
-                    tmem_ld16x256_x4(s0, r0);
-                    tmem_ld_wait16(r0);
-                }
-#pragma unroll 1
-                for (int h = 0; h < 2; ++h) {
-                    if constexpr (NG == 1)
-                        tmem_ld16x256_x4(s0 + 64 * h + 32, r1);
-                    else
-                        tmem_ld16x256_x8(s0 + 64 * h, r0);
-                    // factor of the scores: never zero, as a masked score is -inf
-                    constexpr float kTiny = 1.17549435e-38f;
-                    const float cA = fmaxf(rsA * sc.x, kTiny), cB = fmaxf(rsB * sc.x, kTiny);
-                    const int left = __float_as_int(sc.w);
-                    const float ve = sc.y, vi = sc.z;
-                    uint64_t sA = 0ull, sB = 0ull;
-                    if constexpr (NG == 1) {
-                        part(r0, Const<4>(), 0, left, t, h, cA, cB, ve, sA, sB, atA, atB);
-                        tmem_ld_wait16(r1);
-                    }
-                    if (h == 0) {
-                        if constexpr (NG == 1)
-                            tmem_ld16x256_x4(s0 + 64, r0);
-                        sc = scl[1];
-                    } else {
-                        // S is in registers: QK of a later tile may overwrite it
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0)
-                            mbar_arrive(smem_addr(&bar->s_free[sb]));
-                    }
-                    if constexpr (NG == 1)
-                        part(r1, Const<4>(), 1, left, t, h, cA, cB, ve, sA, sB, atA, atB);
-                    else
-                        part(r0, Const<8>(), 0, left, t, h, cA, cB, ve, sA, sB, atA, atB);
-                    float a0, a1;
-                    unpack2(sA, a0, a1);
-                    lA += (a0 + a1) * vi;
-                    unpack2(sB, a0, a1);
-                    lB += (a0 + a1) * vi;
-                    atA += p_stepA;
-                    atB += p_stepB;
-                    if constexpr (NG == 1)
-                        if (h == 0)
-                            tmem_ld_wait16(r0);
-                }
+                const uint32_t atA = p_rowA + 2 * ps * p_stepA, atB = p_rowB + 2 * ps * p_stepB;
+                // masks and references only where a tile asks for them
+                if (fresh || w0 != 64 || w1 != 64)
+                    pass(Const<1>(), scl, s_addr + 128 * slot, t, atA, atB, smem_addr(&bar->s_free[sb]));
+                else
+                    pass(Const<0>(), scl, s_addr + 128 * slot, t, atA, atB, smem_addr(&bar->s_free[sb]));
                 if (!ok)
                     break;
                 fence_proxy_async_smem();
