@@ -472,73 +472,71 @@ struct Q8Sync {
     uint8_t *owner;   // [Hkv * groups][n_tiles]: the split that streamed each tile
 };
 
-// Adds one tile to a row's running exact partial (m, l, acc): fp32 online
-// softmax on CUDA cores, one warp, lane holding head dims 4 lane .. + 3.
-__device__ void tile_exact(const AttnQ8Args &a, unsigned long long anc, int g, const float (&q4)[4],
-                           int tile, int nq, float &m, float &l, float (&acc)[4])
+// Adds one tile to half a row's running exact partial (m, l, acc): fp32
+// online softmax on CUDA cores, one warp; a lane holds dims 4 lane .. + 3 of
+// the products with K, and dims 64 half + 2 lane, + 1 of V.
+__device__ __noinline__ void tile_exact(const AttnQ8Args &a, unsigned long long anc, int row, int half, int g,
+                                        int tile, int nq, float &m, float &l, float (&acc)[2])
 {
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, dv = 64 * half + 2 * lane;
     const Q8Cache &kc = a.c;
+    const uint2 qb = *reinterpret_cast<const uint2 *>(a.q + (size_t)row * kD + 4 * lane);
+    const float2 q0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&qb.x));
+    const float2 q1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&qb.y));
     const bool q8 = tile < nq;
     const int r0 = q8 ? tile * kTileN : (tile - nq) * kTileN;
     const int n = min(kTileN, (q8 ? kc.n_q8 : kc.n_tail + a.n_tree) - r0);
+    auto two = [](uint32_t codes) {
+        return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(codes & 0xFFFFu), __NV_E4M3)));
+    };
     for (int i = 0; i < n; ++i) {
-        float k[4], v[4];
+        float2 k0, k1, v;
+        float sk = 1.f;
         if (q8) {
-            const int64_t row = (int64_t)g * kc.q8_cap + r0 + i;
+            const int64_t at = (int64_t)g * kc.q8_cap + r0 + i;
             const int64_t blk = (int64_t)g * (kc.q8_cap / kQ8Block) + (r0 + i) / kQ8Block;
-            const float sk = q8_factor(kc.k_scale[blk]), sv = q8_factor(kc.v_scale[blk]);
-            const uint32_t kw = *reinterpret_cast<const uint32_t *>(kc.k8 + row * kD + 4 * lane);
-            const uint32_t vw = *reinterpret_cast<const uint32_t *>(kc.v8 + row * kD + 4 * lane);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const float2 x = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(
-                    (__nv_fp8x2_storage_t)((kw >> (16 * h)) & 0xFFFFu), __NV_E4M3)));
-                const float2 y = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(
-                    (__nv_fp8x2_storage_t)((vw >> (16 * h)) & 0xFFFFu), __NV_E4M3)));
-                k[2 * h] = x.x * sk;
-                k[2 * h + 1] = x.y * sk;
-                v[2 * h] = y.x * sv;
-                v[2 * h + 1] = y.y * sv;
-            }
+            const float sv = q8_factor(kc.v_scale[blk]);
+            sk = q8_factor(kc.k_scale[blk]);
+            const uint32_t kw = *reinterpret_cast<const uint32_t *>(kc.k8 + at * kD + 4 * lane);
+            k0 = two(kw);
+            k1 = two(kw >> 16);
+            v = two(*reinterpret_cast<const uint16_t *>(kc.v8 + at * kD + dv));
+            v.x *= sv;
+            v.y *= sv;
         } else {
             const int tp = r0 + i - kc.n_tail;
             if (tp >= 0 && !((anc >> tp) & 1ull))
                 continue;
-            const int64_t row = (int64_t)g * kc.tail_cap + r0 + i;
-            const uint2 kb = *reinterpret_cast<const uint2 *>(kc.k_tail + row * kD + 4 * lane);
-            const uint2 vb = *reinterpret_cast<const uint2 *>(kc.v_tail + row * kD + 4 * lane);
-            const float2 k0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&kb.x));
-            const float2 k1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&kb.y));
-            const float2 v0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&vb.x));
-            const float2 v1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&vb.y));
-            k[0] = k0.x; k[1] = k0.y; k[2] = k1.x; k[3] = k1.y;
-            v[0] = v0.x; v[1] = v0.y; v[2] = v1.x; v[3] = v1.y;
+            const int64_t at = (int64_t)g * kc.tail_cap + r0 + i;
+            const uint2 kb = *reinterpret_cast<const uint2 *>(kc.k_tail + at * kD + 4 * lane);
+            k0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&kb.x));
+            k1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&kb.y));
+            v = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(kc.v_tail + at * kD + dv));
         }
-        float s = q4[0] * k[0] + q4[1] * k[1] + q4[2] * k[2] + q4[3] * k[3];
+        float s = q0.x * k0.x + q0.y * k0.y + q1.x * k1.x + q1.y * k1.y;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             s += __shfl_xor_sync(0xffffffffu, s, o);
-        s *= a.scale_log2;
+        s *= sk * a.scale_log2;
         if (s > m) {
             const float f = m == -INFINITY ? 0.f : exp2f(m - s);
             l *= f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                acc[e] *= f;
+            acc[0] *= f;
+            acc[1] *= f;
             m = s;
         }
         const float p = exp2f(s - m);
         l += p;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            acc[e] += p * v[e];
+        acc[0] += p * v.x;
+        acc[1] += p * v.y;
     }
 }
 
-// One output row, by one warp: out = sum 2^(m - M) acc / sum 2^(m - M) l over
-// the splits, a flagged split recomputed exactly.
-__device__ __forceinline__ void combine_row(const AttnQ8Args &a, const TreeMasks &masks, int row,
+// Half an output row (64 dims from 64 `half` on), by one warp: out = sum
+// 2^(m - M) acc / sum 2^(m - M) l over the splits, a flagged split recomputed
+// exactly.  (Half a row, so that every split's values are in flight at once:
+// the time here is round trips.)
+__device__ __forceinline__ void combine_row(const AttnQ8Args &a, const TreeMasks &masks, int row, int half,
                                             int g, int gz, int n_gz, int n_split, int nq,
                                             int n_tiles_all, const Q8Sync &sy)
 {
@@ -546,95 +544,79 @@ __device__ __forceinline__ void combine_row(const AttnQ8Args &a, const TreeMasks
     const int lane = threadIdx.x & 31;
     const float *ws_o = sy.part;
     const float2 *ws_ml = reinterpret_cast<const float2 *>(ws_o + (size_t)n_split * rows_all * kD);
-    auto ml_of = [&](int p) { return __ldcg(ws_ml + (size_t)p * rows_all + row); };
-    auto acc_of = [&](int p) {
-        return __ldcg(reinterpret_cast<const float4 *>(ws_o + ((size_t)p * rows_all + row) * kD) + lane);
+    auto ml_of = [&](int s) { return __ldcg(ws_ml + (size_t)s * rows_all + row); };
+    auto acc_of = [&](int s) {
+        return __ldcg(reinterpret_cast<const float2 *>(ws_o + ((size_t)s * rows_all + row) * kD) + 32 * half + lane);
     };
-    // the first kB partials' columns are in flight while M is formed
-    constexpr int kB = 9;
-    float4 x[kB];
+    constexpr int kB = 18;
+    float2 x[kB];
+    float2 mine = lane < n_split ? ml_of(lane) : make_float2(-INFINITY, 0.f);
+    bool any = lane < n_split && __ldcg(sy.flags + (size_t)lane * n_gz + gz) != 0;
 #pragma unroll
     for (int u = 0; u < kB; ++u)
-        x[u] = u < n_split ? acc_of(u) : make_float4(0.f, 0.f, 0.f, 0.f);
-    bool any = false;
-    float M = -INFINITY;
-    float2 mine = make_float2(-INFINITY, 0.f);
-    for (int s = lane; s < n_split; s += 32)
+        x[u] = u < n_split ? acc_of(u) : make_float2(0.f, 0.f);
+    float M = mine.x;
+    for (int s = 32 + lane; s < n_split; s += 32) {
         any |= __ldcg(sy.flags + (size_t)s * n_gz + gz) != 0;
-    for (int p = lane; p < n_split; p += 32) {
-        const float2 ml = ml_of(p);
-        if (p == lane)
-            mine = ml;
-        M = fmaxf(M, ml.x);
+        M = fmaxf(M, ml_of(s).x);
     }
     any = __any_sync(0xffffffffu, any);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    float acc[2] = {0.f, 0.f};
     float L = 0.f;
     if (!any) {
-        for (int p0 = 0; p0 < n_split; p0 += kB) {
-            if (p0 > 0) {
+        for (int s0 = 0; s0 < n_split; s0 += kB) {
+            if (s0 > 0) {
 #pragma unroll
                 for (int u = 0; u < kB; ++u)
-                    x[u] = p0 + u < n_split ? acc_of(p0 + u) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    x[u] = s0 + u < n_split ? acc_of(s0 + u) : make_float2(0.f, 0.f);
             }
 #pragma unroll
             for (int u = 0; u < kB; ++u) {
-                const int p = p0 + u;
-                if (p >= n_split)
+                const int s = s0 + u;
+                if (s >= n_split)
                     break;
                 float2 ml;
-                if (p < 32) {
-                    ml.x = __shfl_sync(0xffffffffu, mine.x, p);
-                    ml.y = __shfl_sync(0xffffffffu, mine.y, p);
+                if (s < 32) {
+                    ml.x = __shfl_sync(0xffffffffu, mine.x, s);
+                    ml.y = __shfl_sync(0xffffffffu, mine.y, s);
                 } else {
-                    ml = ml_of(p);
+                    ml = ml_of(s);
                 }
-                // a partial that saw nothing (m = -inf) has l = 0, or NaN, and
-                // its acc may be anything; a NaN reference keeps its NaN
+                // a split that saw nothing (m = -inf) has l = 0, or NaN, and its
+                // acc may be anything; a NaN reference keeps its NaN
                 const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
                 L += w * ml.y;
                 if (w != 0.f) {
                     acc[0] += w * x[u].x;
                     acc[1] += w * x[u].y;
-                    acc[2] += w * x[u].z;
-                    acc[3] += w * x[u].w;
                 }
             }
         }
     } else {
-        const uint2 qb = *reinterpret_cast<const uint2 *>(a.q + (size_t)row * kD + 4 * lane);
-        const float2 q01 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&qb.x));
-        const float2 q23 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&qb.y));
-        const float q4[4] = {q01.x, q01.y, q23.x, q23.y};
         const uint8_t *own = sy.owner + (size_t)gz * n_tiles_all;
         float Mr = -INFINITY;
-        for (int p = 0; p < n_split; ++p) {
-            const int s = p;
-            float ms, ls, as[4];
+        for (int s = 0; s < n_split; ++s) {
+            float ms = -INFINITY, ls = 0.f, as[2] = {0.f, 0.f};
             if (__ldcg(sy.flags + (size_t)s * n_gz + gz) != 0) {
-                ms = -INFINITY;
-                ls = as[0] = as[1] = as[2] = as[3] = 0.f;
                 for (int t0 = 0; t0 < n_tiles_all; t0 += 32) {
                     const int t = t0 + lane;
                     uint32_t bits = __ballot_sync(0xffffffffu, t < n_tiles_all && __ldcg(own + t) == s);
                     while (bits) {
                         const int tt = t0 + __ffs(bits) - 1;
                         bits &= bits - 1;
-                        tile_exact(a, masks.anc[row / a.n_heads_q], g, q4, tt, nq, ms, ls, as);
+                        tile_exact(a, masks.anc[row / a.n_heads_q], row, half, g, tt, nq, ms, ls, as);
                     }
                 }
             } else {
-                const float2 ml = ml_of(p);
-                const float4 y = acc_of(p);
+                const float2 ml = ml_of(s);
+                const float2 y = acc_of(s);
                 ms = ml.x;
                 ls = ml.y;
                 as[0] = y.x;
                 as[1] = y.y;
-                as[2] = y.z;
-                as[3] = y.w;
             }
             if (ms == -INFINITY) {
                 L += ls;   // nothing seen: 0, or NaN
@@ -644,17 +626,14 @@ __device__ __forceinline__ void combine_row(const AttnQ8Args &a, const TreeMasks
             const float fa = Mr == -INFINITY ? 1.f : exp2f(Mr - Mn);   // L may hold a NaN
             const float fb = exp2f(ms - Mn);
             L = L * fa + ls * fb;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                acc[e] = acc[e] * fa + as[e] * fb;
+            acc[0] = acc[0] * fa + as[0] * fb;
+            acc[1] = acc[1] * fa + as[1] * fb;
             Mr = Mn;
         }
     }
     const float inv = 1.f / L;
-    const __nv_bfloat162 o0 = __floats2bfloat162_rn(acc[0] * inv, acc[1] * inv);
-    const __nv_bfloat162 o1 = __floats2bfloat162_rn(acc[2] * inv, acc[3] * inv);
-    *reinterpret_cast<uint2 *>(a.out + (size_t)row * kD + 4 * lane) = make_uint2(
-        *reinterpret_cast<const uint32_t *>(&o0), *reinterpret_cast<const uint32_t *>(&o1));
+    *reinterpret_cast<__nv_bfloat162 *>(a.out + (size_t)row * kD + 64 * half + 2 * lane) =
+        __floats2bfloat162_rn(acc[0] * inv, acc[1] * inv);
 }
 
 // Bounded wait until the int32 at p (written by other CTAs) reaches target.
@@ -906,17 +885,21 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
             // (the query rows first: not behind every CTA's first ring of tiles)
             named_bar_sync(kBarQLoads, kQLoadThreads);
             named_bar_sync(kBarScales, 32 * (n_conv + 1));
-            // Tiles are taken from the end of the cache backwards, four per
-            // claim: lanes 0-3 post a round's tiles (index, scales), lane 0 issues
-            // their loads, and the next round's claim is on its way meanwhile
-            constexpr int kRound = 4;
+            // Tiles are taken from the end of the cache backwards: each split's
+            // first kFirst ones are its own (every n_split-th), then it claims
+            // kRound at a time, one claim ahead of need.  Lanes post a round's
+            // tiles (index, scales), lane 0 issues their loads.  A claim takes up to
+            // 4000 cycles under load, a tile 1600 (one query row) to 3400 (160);
+            // larger rounds leave the splits of a head further apart at the end
+            // (rounds of four: 10000 cycles at T = 40).
+            constexpr int kFirst = 4, kRound = NG == 2 ? 4 : 1;
             auto tile_at = [&](int k) { return n_tiles_all - 1 - k; };
             int32_t *ctr = sy.sync + 4 * gz;
             auto claim = [&](int n) { return lane == 0 ? atomicAdd(&ctr[0], n) : 0; };
             uint8_t *owner = sy.owner + (size_t)gz * n_tiles_all;
-            // tile t of this CTA, from lane t % kRound
-            auto post = [&](int t, int tile) {
-                if (lane >= kRound)
+            // tile t of this CTA, from one of the first n lanes
+            auto post = [&](int t, int tile, int n) {
+                if (lane >= n)
                     return;
                 const int at = t & (kTileRing - 1);
                 const bool tail = tile >= nq;
@@ -939,12 +922,9 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 if (tile >= 0)
                     owner[tile] = (uint8_t)split;
             };
-            // the split's own tile is the first; the round's others are claimed
-            int base = claim(kRound - 1);
-            const int first = __shfl_sync(0xffffffffu, base, 0);
-            int my_tile = lane == 0 ? tile_at(split) : tile_at(n_split + first + lane - 1);
-            base = claim(kRound);
-            post(lane, my_tile);
+            int base = claim(kRound);
+            int my_tile = tile_at(split + lane * n_split);
+            post(lane, my_tile, kFirst);
             __syncwarp();
             const uint64_t pol = l2_evict_first_policy();
             Ring rk(SK), rv(SV);
@@ -969,7 +949,7 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 return true;
             };
             for (int i = 0; ok && more; ++i) {
-                const int tile = max(-1, __shfl_sync(0xffffffffu, my_tile, i % kRound));
+                const int tile = max(-1, __shfl_sync(0xffffffffu, my_tile, i < kFirst ? i : (i - kFirst) % kRound));
                 if (lane == 0) {
                     const bool tail = tile >= nq;
                     if (tail)
@@ -998,10 +978,10 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 }
                 ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
                 more = tile >= 0;
-                if (more && i % kRound == kRound - 1) {
-                    my_tile = tile_at(n_split + __shfl_sync(0xffffffffu, base, 0) + lane);
+                if (more && i >= kFirst - 1 && (i - (kFirst - 1)) % kRound == 0) {
+                    my_tile = tile_at(kFirst * n_split + __shfl_sync(0xffffffffu, base, 0) + lane);
                     base = claim(kRound);
-                    post(i + 1 + lane, my_tile);
+                    post(i + 1 + lane, my_tile, kRound);
                     __syncwarp();
                 }
             }
@@ -1271,58 +1251,77 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
         // ---- query rows of this KV head: row n = node * G + (head - g*G),
         // block 0 into TMEM lanes (warps 4-7), block 1 into the shared-memory
         // A tile (warps 8-11), each split into hi and lo codes
-        if (warp < 8 || (NB == 2 && warp < 12)) {
-            const int b = warp < 8 ? 0 : 1, q = warp & 3;
-            const int rqb = b ? rq1 : rq0, Rb = b ? R1 : R0;
-            const int n = kBlockM * b + q * rqb + lane;
-            const bool valid = lane < rqb && q * rqb + lane < Rb;
-            const uint4 *src = valid ? q_row(q8_row_of(n, R)) : nullptr;
-            uint32_t top = 0;
+        // (rows that are none keep whatever is there: their scores go nowhere).
+        // Sixteen lanes read a row (a thread per row took 8000 cycles at T = 40,
+        // scattered loads and a long chain each); block 0's codes pass through
+        // the P^T tiles, as TMEM wants a row per lane
+        {
+            constexpr int n_sm = 4 * U * NG;   // softmax warps
+            const int l16 = lane & 15;
+            bool first = true;
+            for (int k0 = 2 * (warp - 4); k0 < R || first; k0 += 4 * 2 * n_sm) {
+                uint4 u[4];
 #pragma unroll
-            for (int c = 0; c < 16; ++c)
-                top = __vmaxu2(top, valid ? top_word(__ldg(src + c)) : 0u);
-            named_bar_arrive(kBarQLoads, kQLoadThreads);
-            top = top_of(top);
-            const bool bad = top >= 0x7F80u;
-            const int e = bad ? 0 : split_exp(top);
-            const float f = two_to(-e);
-            if (valid)
-                aux->row_scale[n] = bad ? __uint_as_float(0x7FC00000u) : a.scale_log2 * two_to(e);
-            const int m = q * 32 + lane;   // A-tile row = TMEM lane of S
-#pragma unroll 1
-            for (int h = 0; h < 2; ++h) {   // 64 dims at a time
-                uint32_t hi[16], lo[16];
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    uint2 x, y;
-                    split_16b(valid ? __ldg(src + 8 * h + c) : make_uint4(0u, 0u, 0u, 0u), f, x, y);
-                    hi[2 * c] = x.x;
-                    hi[2 * c + 1] = x.y;
-                    lo[2 * c] = y.x;
-                    lo[2 * c + 1] = y.y;
+                for (int i = 0; i < 4; ++i) {
+                    const int n = k0 + 2 * n_sm * i + (lane >> 4);
+                    u[i] = n < R ? __ldg(q_row(q8_row_of(n, R)) + l16) : make_uint4(0u, 0u, 0u, 0u);
                 }
-                if (b == 0) {
-                    const uint32_t qa = tmem + ((uint32_t)(q * 32) << 16) + kQCol + 16 * h;
-                    __syncwarp();
-                    tmem_st16(qa, hi);
-                    tmem_st16(qa + 32, lo);
-                } else {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const int off = m * 128 + (((4 * h + c) ^ (m & 7)) << 4);
-                        *reinterpret_cast<uint4 *>(sQ1 + off) =
-                            make_uint4(hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
-                        *reinterpret_cast<uint4 *>(sQ1 + kBlockM * kD + off) =
-                            make_uint4(lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
+                for (int i = 0; i < 4; ++i) {
+                    const int n = k0 + 2 * n_sm * i + (lane >> 4);
+                    uint32_t top = top_word(u[i]);
+#pragma unroll
+                    for (int o = 8; o > 0; o >>= 1)
+                        top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    top = top_of(top);
+                    const bool bad = top >= 0x7F80u;
+                    const int e = bad ? 0 : split_exp(top);
+                    uint2 hi, lo;
+                    split_16b(u[i], two_to(-e), hi, lo);
+                    if (n < R) {
+                        if (l16 == 0)
+                            aux->row_scale[n] = bad ? __uint_as_float(0x7FC00000u) : a.scale_log2 * two_to(e);
+                        // row n's codes: hi in chunks 0-7 of 16 bytes, lo in 8-15
+                        if (NB == 1 || n < kBlockM) {
+                            unsigned char *row = sP + n * 256 + 8 * (l16 & 1);
+                            *reinterpret_cast<uint2 *>(row + (((l16 >> 1) ^ (n & 15)) << 4)) = hi;
+                            *reinterpret_cast<uint2 *>(row + (((8 + (l16 >> 1)) ^ (n & 15)) << 4)) = lo;
+                        } else {
+                            const int n1 = n - kBlockM, q1 = n1 / rq1, m = q1 * 32 + n1 - q1 * rq1;
+                            unsigned char *row = sQ1 + m * 128 + (((l16 >> 1) ^ (m & 7)) << 4) + 8 * (l16 & 1);
+                            *reinterpret_cast<uint2 *>(row) = hi;
+                            *reinterpret_cast<uint2 *>(row + kBlockM * kD) = lo;
+                        }
                     }
                 }
+                if (first && warp < 12)
+                    named_bar_arrive(kBarQLoads, kQLoadThreads);
+                first = false;
             }
-            if (b == 0)
-                tmem_st_wait();
-            else
+            if (NB == 2)
                 fence_proxy_async_smem();
-        } else if (warp < 12) {
-            named_bar_arrive(kBarQLoads, kQLoadThreads);   // one block: no rows to load
+            named_bar_sync(kBarOut, 32 * n_sm);
+            if (NB == 1 || warp < 8 || warp >= 12) {
+                // two warps per lane quarter, 64 dims each
+                const int q = warp & 3, h = warp >= 8 ? 1 : 0;
+                const int n = q * rq0 + lane;
+                const bool valid = lane < rq0 && n < R0;
+                uint32_t hi[16], lo[16];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const unsigned char *row = sP + (valid ? n : 0) * 256;
+                    const int x = valid ? n & 15 : 0;
+                    const uint4 a4 = *reinterpret_cast<const uint4 *>(row + (((4 * h + c) ^ x) << 4));
+                    const uint4 b4 = *reinterpret_cast<const uint4 *>(row + (((8 + 4 * h + c) ^ x) << 4));
+                    hi[4 * c] = a4.x; hi[4 * c + 1] = a4.y; hi[4 * c + 2] = a4.z; hi[4 * c + 3] = a4.w;
+                    lo[4 * c] = b4.x; lo[4 * c + 1] = b4.y; lo[4 * c + 2] = b4.z; lo[4 * c + 3] = b4.w;
+                }
+                const uint32_t qa = tmem + ((uint32_t)(q * 32) << 16) + kQCol + 16 * h;
+                __syncwarp();
+                tmem_st16(qa, hi);
+                tmem_st16(qa + 32, lo);
+                tmem_st_wait();
+            }
         }
         tc_fence_before();
         named_bar_sync(kBarQuery, kThreads - 32 * (1 + n_conv));
@@ -1565,10 +1564,16 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + 64 * grp + c, o);
                     const int nv = min(32, R - c);
                     float *dst = reinterpret_cast<float *>(stage) + (size_t)q8_row_of(c, R) * kD + 32 * q + lane;
+                    if (nv == 32) {
 #pragma unroll
-                    for (int jj = 0; jj < 32; ++jj)
-                        if (jj < nv)
+                        for (int jj = 0; jj < 32; ++jj)
                             dst[jj * kD] = __uint_as_float(o[jj]);
+                    } else {
+#pragma unroll
+                        for (int jj = 0; jj < 32; ++jj)
+                            if (jj < nv)
+                                dst[jj * kD] = __uint_as_float(o[jj]);
+                    }
                 }
             }
             fence_proxy_async_smem();
@@ -1615,7 +1620,7 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
     }
 
     // ---- combine: once every split of this (head, group) has arrived, each
-    // folds rows split, split + n_split, ... (one warp each)
+    // folds half rows split, split + n_split, ... (one warp each)
     const int n_gz = a.n_heads_kv * gridDim.z;
     int32_t *ctr = sy.sync + 4 * gz;
     if (threadIdx.x == 0) {
@@ -1626,9 +1631,11 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
     }
     __syncthreads();
     if (!*abort) {
-        for (int m = split + warp * n_split; m < R; m += (kThreads / 32) * n_split)
-            combine_row(a, masks, (node0 + m / G) * a.n_heads_q + g * G + m % G, g, gz, n_gz,
+        for (int u = split + warp * n_split; u < 2 * R; u += (kThreads / 32) * n_split) {
+            const int m = u >> 1;
+            combine_row(a, masks, (node0 + m / G) * a.n_heads_q + g * G + m % G, u & 1, g, gz, n_gz,
                         n_split, nq, n_tiles_all, sy);
+        }
     }
     __syncthreads();
     if (threadIdx.x == 0 && atomicAdd(&ctr[2], 1) == n_split - 1) {
