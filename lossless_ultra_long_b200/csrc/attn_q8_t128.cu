@@ -313,6 +313,17 @@ __device__ __forceinline__ void tmem_ld_wait16(uint32_t (&r)[16])
                  : "memory");
 }
 
+// 8 consecutive 32-bit TMEM columns of this thread's lane; waits.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+        "tcgen05.wait::ld.sync.aligned;\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+        : "r"(taddr)
+        : "memory");
+}
+
 // 16 consecutive 32-bit TMEM columns of this thread's lane; not waited.
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16])
 {
@@ -567,34 +578,31 @@ __device__ __forceinline__ void combine_row(const AttnQ8Args &a, const TreeMasks
     float acc[2] = {0.f, 0.f};
     float L = 0.f;
     if (!any) {
-        for (int s0 = 0; s0 < n_split; s0 += kB) {
-            if (s0 > 0) {
+        // lane s holds split s's weight.  A split that saw nothing (m = -inf)
+        // has l = 0 and acc = 0, or l = NaN; a NaN reference keeps its NaN
+        for (int s0 = 0; s0 < n_split; s0 += 32) {
+            const float2 ml = s0 == 0 ? mine
+                              : s0 + lane < n_split ? ml_of(s0 + lane) : make_float2(-INFINITY, 0.f);
+            const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
+            L += w * ml.y;
+            for (int u0 = 0; u0 < 32 && s0 + u0 < n_split; u0 += kB) {
+                if (s0 + u0 > 0) {
 #pragma unroll
-                for (int u = 0; u < kB; ++u)
-                    x[u] = s0 + u < n_split ? acc_of(s0 + u) : make_float2(0.f, 0.f);
-            }
-#pragma unroll
-            for (int u = 0; u < kB; ++u) {
-                const int s = s0 + u;
-                if (s >= n_split)
-                    break;
-                float2 ml;
-                if (s < 32) {
-                    ml.x = __shfl_sync(0xffffffffu, mine.x, s);
-                    ml.y = __shfl_sync(0xffffffffu, mine.y, s);
-                } else {
-                    ml = ml_of(s);
+                    for (int u = 0; u < kB; ++u)
+                        x[u] = u0 + u < 32 && s0 + u0 + u < n_split ? acc_of(s0 + u0 + u) : make_float2(0.f, 0.f);
                 }
-                // a split that saw nothing (m = -inf) has l = 0, or NaN, and its
-                // acc may be anything; a NaN reference keeps its NaN
-                const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
-                L += w * ml.y;
-                if (w != 0.f) {
-                    acc[0] += w * x[u].x;
-                    acc[1] += w * x[u].y;
+#pragma unroll
+                for (int u = 0; u < kB; ++u) {
+                    // (past the last: a zero, times some weight that is not used)
+                    const float wu = __shfl_sync(0xffffffffu, w, (u0 + u) & 31);
+                    acc[0] += wu * x[u].x;
+                    acc[1] += wu * x[u].y;
                 }
             }
         }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            L += __shfl_xor_sync(0xffffffffu, L, o);
     } else {
         const uint8_t *own = sy.owner + (size_t)gz * n_tiles_all;
         float Mr = -INFINITY;
@@ -866,10 +874,15 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
     grid_dependency_wait();
     const uint32_t tmem = bar->tmem_base;
 
-    auto q_row = [&](int n) {
-        return reinterpret_cast<const uint4 *>(
-            a.q + ((int64_t)(node0 + n / G) * a.n_heads_q + g * G + n % G) * kD);
+    // node of row m (m < 192, G <= 128: half a unit off any border is far more
+    // than the product's rounding), and its row of q and out
+    const float inv_G = 1.f / (float)G;
+    auto node_of = [&](int m) { return (int)(((float)m + 0.5f) * inv_G); };
+    auto orow = [&](int m) {
+        const int node = node_of(m);
+        return (node0 + node) * a.n_heads_q + g * G + (m - node * G);
     };
+    auto q_row = [&](int m) { return reinterpret_cast<const uint4 *>(a.q + (int64_t)orow(m) * kD); };
 
     if (warp < 4) {
         if (warp == 0)
@@ -1356,8 +1369,8 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
             const uint32_t p_stepA = okA ? p_half : 0u, p_stepB = okB ? p_half : 0u;
             const int rxA = okA ? pnA & 7 : 0, rxB = okB ? pnB & 7 : 0;
             const float rsA = vA ? aux->row_scale[nA] : 1.f, rsB = vB ? aux->row_scale[nB] : 1.f;
-            const unsigned long long ancA = aux->anc[node0 + (vA ? q8_row_of(nA, R) / G : 0)];
-            const unsigned long long ancB = aux->anc[node0 + (vB ? q8_row_of(nB, R) / G : 0)];
+            const unsigned long long ancA = aux->anc[node0 + (vA ? node_of(q8_row_of(nA, R)) : 0)];
+            const unsigned long long ancB = aux->anc[node0 + (vB ? node_of(q8_row_of(nB, R)) : 0)];
             // references, negated (2^(x + n)); sums, NaN from the start for a
             // query row that is none (its scale is NaN)
             float mA = -INFINITY, mB = -INFINITY, nmA = 0.f, nmB = 0.f;
@@ -1534,10 +1547,7 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
             float *ws_o = sy.part;
             float2 *ws_ml = reinterpret_cast<float2 *>(ws_o + (size_t)n_split * rows_all * kD);
             const size_t part_row = (size_t)split * rows_all;
-            auto orow_of = [&](int n) {
-                const int m = q8_row_of(n, R);
-                return (node0 + m / G) * a.n_heads_q + g * G + m % G;
-            };
+            auto orow_of = [&](int n) { return orow(q8_row_of(n, R)); };
             if (ok && (lane & 3) == 0) {
                 if (vA) {
                     if (NG == 2)
@@ -1560,17 +1570,15 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
             if (have_o) {
                 tc_fence_after();
                 for (int c = 32 * j; c < r_pad; c += 32 * U) {
-                    uint32_t o[32];
-                    tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + 64 * grp + c, o);
-                    const int nv = min(32, R - c);
+                    // (steps of eight columns: short code, run once)
                     float *dst = reinterpret_cast<float *>(stage) + (size_t)q8_row_of(c, R) * kD + 32 * q + lane;
-                    if (nv == 32) {
+#pragma unroll 1
+                    for (int c8 = 0; c8 < 32 && c + c8 < R; c8 += 8, dst += 8 * kD) {
+                        uint32_t o[8];
+                        tmem_ld8(tmem + ((uint32_t)(32 * q) << 16) + 64 * grp + c + c8, o);
+                        const int nv = R - c - c8;   // query rows among these
 #pragma unroll
-                        for (int jj = 0; jj < 32; ++jj)
-                            dst[jj * kD] = __uint_as_float(o[jj]);
-                    } else {
-#pragma unroll
-                        for (int jj = 0; jj < 32; ++jj)
+                        for (int jj = 0; jj < 8; ++jj)
                             if (jj < nv)
                                 dst[jj * kD] = __uint_as_float(o[jj]);
                     }
@@ -1633,7 +1641,7 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
     if (!*abort) {
         for (int u = split + warp * n_split; u < 2 * R; u += (kThreads / 32) * n_split) {
             const int m = u >> 1;
-            combine_row(a, masks, (node0 + m / G) * a.n_heads_q + g * G + m % G, u & 1, g, gz, n_gz,
+            combine_row(a, masks, orow(m), u & 1, g, gz, n_gz,
                         n_split, nq, n_tiles_all, sy);
         }
     }
