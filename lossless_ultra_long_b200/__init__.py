@@ -148,12 +148,19 @@ def library():
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+# the current stream's handle without a Stream object around it (2 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(stream):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _check_dev(name, t, dtype, device=None):
@@ -195,6 +202,18 @@ def _host_i32(a):
     arr = np.ascontiguousarray(a.cpu().numpy() if isinstance(a, torch.Tensor) else a,
                                dtype=np.int32)
     return arr, arr.ctypes.data_as(ctypes.c_void_p)
+
+
+def _parent_arg(parent, n):
+    """(keep-alive, address) of a host int32 parent array of n entries."""
+    import numpy as np
+    if isinstance(parent, torch.Tensor):
+        parent = parent.cpu().numpy()
+    arr = (parent if isinstance(parent, np.ndarray) and parent.dtype == np.int32 and
+           parent.flags.c_contiguous else np.array(parent, dtype=np.int32))
+    if arr.shape != (n,):
+        raise ValueError("parent must have one entry per tree node")
+    return arr, arr.__array_interface__["data"][0]
 
 
 def _raise(rc, where):
@@ -490,18 +509,21 @@ def rope_inv_freq(rot_dim: int, base: float, kind: str = "plain", *params):
 
 
 def _check_rows(name, t, heads, d, device):
-    """A bf16 [tokens, heads, D] tensor whose tokens may lie apart."""
+    """A bf16 [tokens, heads, D] tensor whose tokens may lie apart: the
+    elements from one token to the next."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != torch.bfloat16:
         raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the call's other tensors on {device}")
-    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or t.shape[2] != d:
+    shape = t.shape
+    if len(shape) != 3 or (heads is not None and shape[1] != heads) or shape[2] != d:
         raise ValueError(f"{name} must be [tokens, heads, {d}]")
-    if (t.shape[2] > 1 and t.stride(2) != 1) or (t.shape[1] > 1 and t.stride(1) != d):
+    st = t.stride()
+    if (st[2] != 1 and d > 1) or (st[1] != d and shape[1] > 1):
         raise ValueError(f"{name}: the heads and elements of a token must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * d
+    return st[0] if shape[0] > 1 else shape[1] * d
 
 
 def rope_append(q, k, v, k_cache, v_cache, row0: int, pos0: int, inv_freq, parent=None,
@@ -537,11 +559,7 @@ def rope_append(q, k, v, k_cache, v_cache, row0: int, pos0: int, inv_freq, paren
     if inv_freq is not None:
         _check_dev("inv_freq", inv_freq, torch.float32, dev)
         rot = 2 * inv_freq.numel()
-    par_p = None
-    if parent is not None:
-        par, par_p = _host_i32(parent)
-        if len(par) != n:
-            raise ValueError("parent must have one entry per tree node")
+    par, par_p = (None, None) if parent is None else _parent_arg(parent, n)
     _raise(_lib().ts_rope_append(
         _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, hq, hkv, d, n, par_p, int(pos0),
         _ptr(inv_freq) if rot else None, rot, int(bool(interleaved)), float(mscale),
@@ -604,9 +622,20 @@ class KvCacheQ8:
             raise ValueError("n_q8 must be a multiple of 64 within the 8-bit rows")
         if n_tail < 0 or tail_row0 < 0 or tail_row0 + n_tail > k_tail.shape[1]:
             raise ValueError("n_tail rows from tail_row0 must lie in the tail")
-        self.k8, self.v8, self.k_scale, self.v_scale = k8, v8, k_scale, v_scale
-        self.k_tail, self.v_tail, self.device = k_tail, v_tail, dev
+        self._tensors = (k8, v8, k_scale, v_scale, k_tail, v_tail)   # the struct's, for good
+        self.device = dev
         self.n_q8, self.n_tail, self.tail_row0 = int(n_q8), int(n_tail), int(tail_row0)
+        hkv, cap, d = k8.shape
+        self._struct = _Q8Cache(k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(),
+                                v_scale.data_ptr(), cap, k_tail.data_ptr(), v_tail.data_ptr(),
+                                k_tail.shape[1], self.tail_row0, hkv, d, self.n_q8, self.n_tail)
+
+    k8 = property(lambda self: self._tensors[0])
+    v8 = property(lambda self: self._tensors[1])
+    k_scale = property(lambda self: self._tensors[2])
+    v_scale = property(lambda self: self._tensors[3])
+    k_tail = property(lambda self: self._tensors[4])
+    v_tail = property(lambda self: self._tensors[5])
 
     @classmethod
     def empty(cls, n_heads_kv: int, head_dim: int, capacity: int, tail_rows: int = 256,
@@ -632,11 +661,9 @@ class KvCacheQ8:
 
     def struct(self):
         """The ``ts_q8_cache`` of the cache as it stands."""
-        hkv, cap, d = self.k8.shape
-        return _Q8Cache(self.k8.data_ptr(), self.v8.data_ptr(), self.k_scale.data_ptr(),
-                        self.v_scale.data_ptr(), cap, self.k_tail.data_ptr(),
-                        self.v_tail.data_ptr(), self.k_tail.shape[1], self.tail_row0, hkv, d,
-                        self.n_q8, self.n_tail)
+        st = self._struct
+        st.n_q8, st.n_tail, st.tail_row0 = self.n_q8, self.n_tail, self.tail_row0
+        return st
 
     def append(self, q, k, v, inv_freq, parent=None, stream=None, **kw):
         """:func:`rope_append` behind the context, at its positions.  With
@@ -695,7 +722,10 @@ class KvCacheQ8:
 def _call_cache(cache):
     if not isinstance(cache, KvCacheQ8):
         raise ValueError("cache must be a KvCacheQ8")
-    return _call_device("cache", cache.k_tail), cache.struct()
+    cur = torch.cuda.current_device()
+    if cache.device.index != cur:
+        raise ValueError(f"cache is on {cache.device} but the current device is cuda:{cur}")
+    return cache.device, cache.struct()
 
 
 def tree_verify_attn_q8_workspace_size(n_heads_q, n_heads_kv, head_dim, n_q8, n_tail,
@@ -729,9 +759,7 @@ def tree_verify_attn_q8(q, cache: KvCacheQ8, parent, out=None, workspace=None,
     if workspace is None:
         workspace = new_workspace(tree_verify_attn_q8_workspace_size(
             hq, st.n_heads_kv, d, st.n_q8, st.n_tail, t), dev)
-    par, par_p = _host_i32(parent)
-    if len(par) != t:
-        raise ValueError("parent must have one entry per tree node")
+    par, par_p = _parent_arg(parent, t)
     scale = float(d) ** -0.5 if softmax_scale is None else float(softmax_scale)
     rc = _lib().ts_tree_verify_attn_q8(
         ctypes.byref(st), _ptr(q), hq, t, par_p, scale, _ptr(out), _ptr(root_scores_out),

@@ -22,6 +22,7 @@
 #include <math.h>
 
 #include "attn_q8.cuh"
+#include "sm100.cuh"
 
 namespace ts {
 namespace {
@@ -29,6 +30,8 @@ namespace {
 constexpr int kTile = kQ8Block;
 constexpr int kStages = 3;
 constexpr int kMaxWarps = 12;    // 192 query rows per CTA
+// contexts of at most so many tiles are one split, without a combine
+constexpr int kOneSplit = 2;
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p)
 {
@@ -105,6 +108,8 @@ attn_q8_kernel(AttnQ8Args a, TreeMasks masks, int tiles_per_split, int n_split)
     constexpr int TB = Shape<D>::kTileBytes;
     const Q8Cache &kc = a.c;
 
+    if (threadIdx.x == 0)
+        sm100::launch_dependents();   // the combine may take its place and wait
     const int split = blockIdx.x, g = blockIdx.y;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int nthreads = blockDim.x;
@@ -397,6 +402,8 @@ attn_q8_combine_kernel(const float *__restrict__ ws_o, const float *__restrict__
 {
     const int row = blockIdx.x * 8 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
+    sm100::launch_dependents();
+    sm100::grid_dependency_wait();   // the split kernel's partials
     if (row >= rows_all)
         return;
     float M = -INFINITY;
@@ -405,26 +412,39 @@ attn_q8_combine_kernel(const float *__restrict__ ws_o, const float *__restrict__
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    constexpr int PER = D / 32;
+    constexpr int PER = D / 32, kB = 12;   // splits whose loads are in flight together
     float acc[PER] = {};
     float L = 0.f;
-#pragma unroll 4
-    for (int s = 0; s < n_split; ++s) {
-        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(ws_ml + ((size_t)s * rows_all + row) * 2));
-        const float *src = ws_o + ((size_t)s * rows_all + row) * D + lane * PER;
-        float x[PER];
-        if constexpr (PER == 4) {
-            const float4 v = __ldcg(reinterpret_cast<const float4 *>(src));
-            x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-        } else {
-            const float2 v = __ldcg(reinterpret_cast<const float2 *>(src));
-            x[0] = v.x; x[1] = v.y;
-        }
-        const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
-        L += w * ml.y;
+    for (int s0 = 0; s0 < n_split; s0 += kB) {
+        float2 ml[kB];
+        float x[kB][PER];
 #pragma unroll
-        for (int e = 0; e < PER; ++e)
-            acc[e] += w * x[e];
+        for (int u = 0; u < kB; ++u) {
+            ml[u] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+            for (int e = 0; e < PER; ++e)
+                x[u][e] = 0.f;
+            if (s0 + u < n_split) {
+                const size_t at = (size_t)(s0 + u) * rows_all + row;
+                ml[u] = __ldcg(reinterpret_cast<const float2 *>(ws_ml + at * 2));
+                const float *src = ws_o + at * D + lane * PER;
+                if constexpr (PER == 4) {
+                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(src));
+                    x[u][0] = v.x; x[u][1] = v.y; x[u][2] = v.z; x[u][3] = v.w;
+                } else {
+                    const float2 v = __ldcg(reinterpret_cast<const float2 *>(src));
+                    x[u][0] = v.x; x[u][1] = v.y;
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kB; ++u) {
+            const float w = ml[u].x == -INFINITY ? 0.f : exp2f(ml[u].x - M);
+            L += w * ml[u].y;
+#pragma unroll
+            for (int e = 0; e < PER; ++e)
+                acc[e] += w * x[u][e];
+        }
     }
     const float inv = 1.f / L;
     __nv_bfloat162 *dst = reinterpret_cast<__nv_bfloat162 *>(out + (size_t)row * D + lane * PER);
@@ -447,6 +467,8 @@ SplitPlan make_plan(int n_heads_q, int n_heads_kv, int n_q8, int n_tail, int n_t
     const int n_tiles = n_q8 / kTile + (n_tail + n_tree + kTile - 1) / kTile;
     int want = num_sms / (n_heads_kv * p.row_blocks);
     want = want < 1 ? 1 : (want > n_tiles ? n_tiles : want);
+    if (n_tiles <= kOneSplit)
+        want = 1;
     p.tiles_per_split = (n_tiles + want - 1) / want;
     p.n_split = (n_tiles + p.tiles_per_split - 1) / p.tiles_per_split;
     return p;
@@ -475,12 +497,8 @@ cudaError_t launch_d(const AttnQ8Args &a, const TreeMasks &masks, const SplitPla
     const float *ws_o = reinterpret_cast<const float *>(
         reinterpret_cast<const char *>(a.workspace) + kHeaderBytes + kQ8SyncBytes);
     const float *ws_ml = ws_o + (size_t)p.n_split * rows_all * D;
-    attn_q8_combine_kernel<D><<<(rows_all + 7) / 8, 256, 0, stream>>>(ws_o, ws_ml, a.out, rows_all,
-                                                                     p.n_split);
-    e = cudaGetLastError();
-    if (e == cudaSuccess)
-        count_launches(1);
-    return e;
+    return launch_pdl(attn_q8_combine_kernel<D>, dim3((rows_all + 7) / 8), dim3(256), 0, stream, ws_o,
+                      ws_ml, a.out, rows_all, p.n_split);
 }
 
 }  // namespace

@@ -74,82 +74,122 @@ __device__ __forceinline__ void turn8(uint4 &a, uint4 &b, const float *cs, const
     }
 }
 
-// Grid (token, head group).  The token's angles are formed once per CTA;
-// then each thread moves units of 16 bytes (two of them where a pair's
-// halves lie apart).  VEC: interleaved pairs, or halves that start on a
-// 16-byte boundary; otherwise one pair or one element per unit.
-template <bool VEC>
-__global__ void __launch_bounds__(kThreads)
-rope_append_kernel(RopeArgs a, Depths depths, int heads_per_cta)
+// Cosines and sines (times mscale) of tokens tok0 .. tok0 + n_tok - 1 into
+// shared memory, [token][rot / 2], a pair per thread and round.
+__device__ __forceinline__ void form_angles(const RopeArgs &a, const Depths &depths, int tok0, int n_tok,
+                                            float *cs, float *sn)
 {
-    __shared__ __align__(16) float cs[64], sn[64];
-    const int tok = blockIdx.x;
-    const int half = a.rot_dim / 2, D = a.head_dim;
-    if (threadIdx.x < half) {
-        const int64_t pos = a.pos0 + (a.tree ? depths.depth[tok] : tok);
-        const double turns = (double)pos * (double)a.inv_freq[threadIdx.x] * 0.15915494309189535;
+    const int half = a.rot_dim / 2;
+    for (int i = threadIdx.x; i < n_tok * half; i += kThreads) {
+        const int t = i / half;
+        const int64_t pos = a.pos0 + (a.tree ? depths.depth[tok0 + t] : tok0 + t);
+        const double turns = (double)pos * (double)__ldg(a.inv_freq + (i - t * half)) * 0.15915494309189535;
         float s, c;
         sincospif((float)(2.0 * (turns - rint(turns))), &s, &c);
-        cs[threadIdx.x] = c * a.mscale;
-        sn[threadIdx.x] = s * a.mscale;
+        cs[i] = c * a.mscale;
+        sn[i] = s * a.mscale;
     }
     __syncthreads();
-    const int heads = a.n_heads_q + 2 * a.n_heads_kv;
-    const int h0 = blockIdx.y * heads_per_cta, h1 = min(h0 + heads_per_cta, heads);
-    if (VEC) {
-        // a row is D/8 chunks of 8 elements.  Half layout: chunk c < half/8
-        // also takes chunk c + half/8; those partners are no unit of their own
-        const int chunks = D / 8;
-        const int hc = a.interleaved ? 0 : half / 8;
-        for (int u = threadIdx.x; u < (h1 - h0) * chunks; u += kThreads) {
-            const int c = u % chunks;
-            const RowPtr r = row_ptr(a, tok, h0 + u / chunks);
-            const uint4 *src = reinterpret_cast<const uint4 *>(r.src);
-            uint4 *dst = reinterpret_cast<uint4 *>(r.dst);
-            if (!r.turn) {
-                dst[c] = src[c];
-            } else if (!a.interleaved) {
-                if (c < hc) {
-                    uint4 x = src[c], y = src[c + hc];
-                    turn8(x, y, cs + 8 * c, sn + 8 * c);
-                    dst[c] = x;
-                    dst[c + hc] = y;
-                } else if (c >= 2 * hc) {
-                    dst[c] = src[c];
-                }
-            } else {
-                uint4 x = src[c];
-                uint32_t *p = reinterpret_cast<uint32_t *>(&x);
+}
+
+// Grid (run of tokens, head group): 16-byte chunks, for interleaved pairs, or
+// halves that start on a chunk.  A row is D / 8 chunks; with halves apart,
+// unit c < hc = rot / 16 is the chunks c and c + hc (a turned row's pairs),
+// unit c >= hc the chunk c + hc.  A thread has kUnits units' loads in flight,
+// the first of them while the run's angles are formed.
+// HBM-bound on a prompt: on 8190 tokens of 56 heads of 128 (235 MB) a CTA per
+// token took 86-95 us, each waiting for its own angles; runs of tokens NN us.
+constexpr int kUnits = 4, kMaxAngles = 512;
+template <int D, bool INTER>
+__global__ void __launch_bounds__(kThreads)
+rope_append_kernel(RopeArgs a, Depths depths, int toks_per_cta, int heads_per_cta)
+{
+    __shared__ __align__(16) float cs[kMaxAngles], sn[kMaxAngles];
+    constexpr int kChunks = D / 8;
+    const int half = a.rot_dim / 2;
+    const int hc = INTER ? 0 : half / 8, upr = kChunks - hc;   // units per row
+    const int tok0 = blockIdx.x * toks_per_cta, n_tok = min(toks_per_cta, a.n_tok - tok0);
+    const int h0 = blockIdx.y * heads_per_cta;
+    const int n_heads = min(heads_per_cta, a.n_heads_q + 2 * a.n_heads_kv - h0);
+    const int units = n_tok * n_heads * upr;
+    // quotients by products: half a unit off any border is more than their rounding
+    const float inv_upr = 1.f / (float)upr, inv_heads = 1.f / (float)n_heads;
+    bool angles = false;
+    for (int u0 = threadIdx.x; u0 < units || !angles; u0 += kUnits * kThreads) {
+        uint4 x[kUnits], y[kUnits];
+        __nv_bfloat16 *dst[kUnits];
+        int c[kUnits], at[kUnits];   // at: the token's angles, or -1
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int j = 4 * c + i;
-                    if (j < half) {
-                        const float2 v = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162 *>(p + i));
-                        float y0, y1;
-                        turn2(v.x, v.y, cs[j], sn[j], y0, y1);
-                        *reinterpret_cast<__nv_bfloat162 *>(p + i) = __floats2bfloat162_rn(y0, y1);
-                    }
-                }
-                dst[c] = x;
+        for (int i = 0; i < kUnits; ++i) {
+            const int u = u0 + i * kThreads;
+            if (u < units) {
+                const int row = (int)(((float)u + 0.5f) * inv_upr);
+                const int t = (int)(((float)row + 0.5f) * inv_heads);
+                c[i] = u - row * upr;
+                const RowPtr r = row_ptr(a, tok0 + t, h0 + row - t * n_heads);
+                const uint4 *src = reinterpret_cast<const uint4 *>(r.src);
+                dst[i] = r.dst;
+                at[i] = r.turn ? t * half : -1;
+                if (c[i] < hc)
+                    x[i] = __ldcs(src + c[i]);
+                y[i] = __ldcs(src + c[i] + hc);
             }
         }
-    } else {
-        // half layout whose halves start anywhere: unit j < half is a pair,
-        // the rest single elements from rot on
-        const int units = D - half;
-        for (int u = threadIdx.x; u < (h1 - h0) * units; u += kThreads) {
-            const int j = u % units;
-            const RowPtr r = row_ptr(a, tok, h0 + u / units);
-            if (j < half) {
-                const float x = __bfloat162float(r.src[j]), w = __bfloat162float(r.src[j + half]);
-                float y0 = x, y1 = w;
-                if (r.turn)
-                    turn2(x, w, cs[j], sn[j], y0, y1);
-                r.dst[j] = __float2bfloat16_rn(y0);
-                r.dst[j + half] = __float2bfloat16_rn(y1);
-            } else {
-                r.dst[j + half] = r.src[j + half];
+        if (!angles)
+            form_angles(a, depths, tok0, n_tok, cs, sn);
+        angles = true;
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i) {
+            if (u0 + i * kThreads >= units)
+                continue;
+            uint4 *out = reinterpret_cast<uint4 *>(dst[i]);
+            if (INTER) {
+                if (at[i] >= 0) {
+                    uint32_t *p = reinterpret_cast<uint32_t *>(&y[i]);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int j = 4 * c[i] + k;
+                        if (j < half) {
+                            const float2 v = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162 *>(p + k));
+                            float y0, y1;
+                            turn2(v.x, v.y, cs[at[i] + j], sn[at[i] + j], y0, y1);
+                            *reinterpret_cast<__nv_bfloat162 *>(p + k) = __floats2bfloat162_rn(y0, y1);
+                        }
+                    }
+                }
+            } else if (c[i] < hc) {
+                if (at[i] >= 0)
+                    turn8(x[i], y[i], cs + at[i] + 8 * c[i], sn + at[i] + 8 * c[i]);
+                out[c[i]] = x[i];
             }
+            out[c[i] + hc] = y[i];
+        }
+    }
+}
+
+// Halves that start anywhere: unit j < half is a pair, the rest single
+// elements from rot on.
+__global__ void __launch_bounds__(kThreads)
+rope_append_any_kernel(RopeArgs a, Depths depths, int heads_per_cta)
+{
+    __shared__ float cs[64], sn[64];
+    const int tok = blockIdx.x, half = a.rot_dim / 2;
+    form_angles(a, depths, tok, 1, cs, sn);
+    const int heads = a.n_heads_q + 2 * a.n_heads_kv;
+    const int h0 = blockIdx.y * heads_per_cta, h1 = min(h0 + heads_per_cta, heads);
+    const int units = a.head_dim - half;
+    for (int u = threadIdx.x; u < (h1 - h0) * units; u += kThreads) {
+        const int j = u % units;
+        const RowPtr r = row_ptr(a, tok, h0 + u / units);
+        if (j < half) {
+            const float x = __bfloat162float(r.src[j]), w = __bfloat162float(r.src[j + half]);
+            float y0 = x, y1 = w;
+            if (r.turn)
+                turn2(x, w, cs[j], sn[j], y0, y1);
+            r.dst[j] = __float2bfloat16_rn(y0);
+            r.dst[j + half] = __float2bfloat16_rn(y1);
+        } else {
+            r.dst[j + half] = r.src[j + half];
         }
     }
 }
@@ -168,12 +208,25 @@ cudaError_t rope_append_launch(const RopeArgs &a, const int32_t *parent, int num
     int groups = (2 * num_sms + a.n_tok - 1) / a.n_tok;
     groups = groups > heads ? heads : groups;
     const int per = (heads + groups - 1) / groups;
-    const dim3 grid(a.n_tok, (heads + per - 1) / per);
-    const bool vec = a.interleaved || (a.rot_dim / 2) % 8 == 0;
-    if (vec)
-        rope_append_kernel<true><<<grid, kThreads, 0, stream>>>(a, d, per);
-    else
-        rope_append_kernel<false><<<grid, kThreads, 0, stream>>>(a, d, per);
+    if (!a.interleaved && (a.rot_dim / 2) % 8 != 0) {
+        rope_append_any_kernel<<<dim3(a.n_tok, (heads + per - 1) / per), kThreads, 0, stream>>>(a, d, per);
+    } else {
+        // runs of tokens as long as their angles fit and every SM keeps four CTAs
+        const int half = a.rot_dim / 2;
+        int run = half > 0 ? kMaxAngles / half : 8;
+        run = run > 8 ? 8 : run;
+        const int fit = a.n_tok / (4 * num_sms);
+        run = fit < run ? (fit < 1 ? 1 : fit) : run;
+        const dim3 grid((a.n_tok + run - 1) / run, (heads + per - 1) / per);
+        if (a.head_dim == 128 && a.interleaved)
+            rope_append_kernel<128, true><<<grid, kThreads, 0, stream>>>(a, d, run, per);
+        else if (a.head_dim == 128)
+            rope_append_kernel<128, false><<<grid, kThreads, 0, stream>>>(a, d, run, per);
+        else if (a.interleaved)
+            rope_append_kernel<64, true><<<grid, kThreads, 0, stream>>>(a, d, run, per);
+        else
+            rope_append_kernel<64, false><<<grid, kThreads, 0, stream>>>(a, d, run, per);
+    }
     const cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess)
         count_launches(1);
