@@ -33,7 +33,7 @@
 //
 // CTA = (split, KV head, node group), 20 warps, one CTA per SM:
 //   warp 0      root scores out of S        warp 1  QK issuer, TMEM
-//   warp 2      PV issuer                   warp 3  TMA producer
+//   warp 2      PV issuer                   warp 3  takes tiles, TMA producer
 //   warps 4-15  softmax, as many as the rows need; the others and
 //   warps 16-19 V's codes to bf16
 // P^T is double-buffered, and with one query block (R <= 128) S too, so a
@@ -82,9 +82,10 @@ constexpr int kBarQuery = 1;                 // named barrier: query rows in pla
 constexpr int kBarOut = 2;                   // named barrier: O^T staged, or merged, in shared memory
 constexpr int kTileRing = 16;                // entries of the tile rings (> any role's lead)
 static_assert(kTileRing == 1 << 4, "indexed by shifts");
+constexpr int kBarRows = 5;                  // named barrier: row_scale is written (for warp 0)
 constexpr int kBarQLoads = 3;                // named barrier: the query rows are read
 constexpr int kBarScales = 4;                // named barrier: the scale bytes are in shared memory
-constexpr int kQLoadThreads = 32 * 9;        // warps 4-11 arrive, the producer warp waits
+constexpr int kQLoadThreads = 32 * 9;        // warps 4-11 arrive, K's producer waits
 constexpr int kMaxGz = 256;                  // (KV head, node group) pairs: counters in the workspace
 static_assert(kMaxGz * 16 <= (int)kQ8SyncBytes, "counters fit their region");
 
@@ -104,9 +105,9 @@ struct Bars {
     uint64_t drain[2];
     uint64_t conv;                  // the converter warps meet (tail tiles)
     uint64_t info[kTileRing];       // tile_of, scale_of of that tile are written
-    // per tile, at [t & (kTileRing - 1)]: its index (-1 after the last) and its
-    // first K ring entry.  Written by the producer before the arrival that
-    // the readers wait for.
+    uint64_t tail_slots[kTileRing]; // a tail tile's K slots are free, entry_of is written
+    // per tile, at [t & (kTileRing - 1)]: its index (-1 after the last), and a
+    // tail tile's first K ring entry
     volatile int32_t tile_of[kTileRing];
     volatile int32_t entry_of[kTileRing];
     uint32_t bad[4][4];             // tail tile t % 4: rows with a value that is no number
@@ -119,7 +120,7 @@ struct Bars {
 
 struct Aux {
     Bars bar;
-    // per tile and half, written like tile_of (a tail tile's k by a converter):
+    // per tile and half, posted with tile_of (a tail tile's k by a converter):
     // K's scale, V's as an exponent, V's inverse, and (as an int) how many of
     // the half's positions are context, kTailMark added on a tail tile, or
     // kEndMark.  A block that is NaN, in K or V, has a NaN exponent and
@@ -700,6 +701,8 @@ __device__ __noinline__ bool tail_keys(const AttnQ8Args &a, Aux *aux, unsigned c
     }
     if (!warp_wait(smem_addr(&bar->conv), met++ & 1, abort, hdr))
         return false;
+    if (!warp_wait(smem_addr(&bar->tail_slots[t & (kTileRing - 1)]), (t >> 4) & 1, abort, hdr))
+        return false;
     volatile uint32_t *top = bar->top;
     const int e = split_exp(max(top[w & 2], top[(w & 2) + 1]));
     if (tid == 0) {
@@ -778,6 +781,11 @@ struct Form {
     static constexpr int U = MODE + 1;               // softmax warps per lane quarter and group
     static constexpr int U0 = MODE == 0 ? 1 : 2;     // of these in block 0
     static constexpr int SVB = MODE == 2 ? 1 : 2;    // bf16 V slots
+    // K's loads from warp 0 instead of warp 3, when it has no root scores to
+    // read: with V's they cost their warp 1500 cycles a tile, about what a tile
+    // takes up to 64 rows (T = 13: 58 us against 65; with the root scores in the
+    // same warp 84 against 67)
+    static constexpr bool kSplit = MODE == 0;
     static constexpr int n_conv = kThreads / 32 - 4 - 4 * U * NG;   // converter warps, the last ones
 };
 
@@ -803,6 +811,7 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
     // (quarter, unit) pairs with query rows: their warps arrive on the barriers
     const int act0 = active_units(R0, rq0), act1 = active_units(R1, rq1);
     const bool rs_warp0 = a.root_scores != nullptr && node0 == 0;
+    const bool k_split = F::kSplit && !rs_warp0;
     const int n_blk = kc.n_q8 / kQ8Block;
     const Layout lay = q8_layout(R, n_blk);
     const int SK = lay.stages_k, SV = lay.stages_v, r_pad = lay.r_pad;
@@ -845,8 +854,10 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
         mbar_init(smem_addr(&bar->vb_full[1]), n_conv);
         mbar_init(smem_addr(&bar->drain[0]), 1);
         mbar_init(smem_addr(&bar->drain[1]), 1);
-        for (int i = 0; i < kTileRing; ++i)
+        for (int i = 0; i < kTileRing; ++i) {
             mbar_init(smem_addr(&bar->info[i]), 1);
+            mbar_init(smem_addr(&bar->tail_slots[i]), 1);
+        }
         for (int i = 0; i < 3; ++i) {
             mbar_init(smem_addr(&bar->s_full[i]), 1);
             mbar_init(smem_addr(&bar->s_free[i]), NB == 1 ? act0 + rs : (i == 0 ? act0 : act1 + rs));
@@ -885,24 +896,62 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
     auto q_row = [&](int m) { return reinterpret_cast<const uint4 *>(a.q + (int64_t)orow(m) * kD); };
 
     if (warp < 4) {
-        if (warp == 0)
+        if (warp == 2)
             for (int i = lane; i < a.n_tree; i += 32)
                 aux->anc[i] = masks.anc[i];
-        if (warp != 3) {
+        if (warp == 1 || warp == 2) {
             tc_fence_before();
-            named_bar_sync(kBarQuery, kThreads - 32 * (1 + n_conv));
+            named_bar_sync(kBarQuery, 32 * (2 + 4 * U * NG));
             tc_fence_after();
         }
+        // K's loads: step t issues tile t's (a tail tile takes two slots, which the
+        // converters fill)
+        const uint64_t pol = l2_evict_first_policy();
+        Ring rk(SK);
+        int ke = 0, k_tma = -1;   // K ring entries used; the last that was a TMA load
+        bool k_end = false;       // the end marker is on its way
+        auto k_step = [&](int t) {
+            const int at = t & (kTileRing - 1);
+            if (k_split && !warp_wait(smem_addr(&bar->info[at]), (t >> 4) & 1, abort, hdr))
+                return false;
+            const int tile = bar->tile_of[at];
+            const bool tail = tile >= nq;
+            for (int part = 0; part < (tail ? 2 : 1); ++part, ++ke, rk.next()) {
+                const int s = rk.i;
+                if (ke >= SK && !warp_wait(smem_addr(&bar->empty_k[s]), rk.ph ^ 1, abort, hdr))
+                    return false;
+                if (lane == 0) {
+                    const uint32_t fb = smem_addr(&bar->full_k[s]);
+                    if (tile < 0) {
+                        mbar_arrive(fb);   // no tile left: the QK issuer passes it on
+                    } else if (!tail) {
+                        mbar_arrive_expect_tx(fb, kRawBytes);
+                        tma_load_3d_hint(smem_addr(sK + s * kRawBytes), &tmap_k, 0, tile * kTileN, g, fb, pol);
+                        k_tma = ke;
+                    } else if (part == 1) {
+                        bar->entry_of[at] = ke - 1;
+                        mbar_arrive(smem_addr(&bar->tail_slots[at]));
+                    }
+                }
+            }
+            k_end = __any_sync(0xffffffffu, tile < 0);
+            return true;
+        };
+        auto k_drain = [&]() {   // our own copies land before the CTA exits
+            if (lane == 0 && *abort)
+                for (int t = max(0, k_tma - SK + 1); t <= k_tma; ++t)
+                    wait_drain(smem_addr(&bar->full_k[t % SK]), (t / SK) & 1);
+        };
         if (warp == 3) {
-            // ------------------------------------------------ TMA producer
-            // (the query rows first: not behind every CTA's first ring of tiles)
-            named_bar_sync(kBarQLoads, kQLoadThreads);
+            // ------------------------------------------------ tiles, TMA producer
+            if (!k_split)   // (the query rows first, as below)
+                named_bar_sync(kBarQLoads, kQLoadThreads);
             named_bar_sync(kBarScales, 32 * (n_conv + 1));
             // Tiles are taken from the end of the cache backwards: each split's
             // first kFirst ones are its own (every n_split-th), then it claims
             // kRound at a time, one claim ahead of need.  Lanes post a round's
-            // tiles (index, scales), lane 0 issues their loads.  A claim takes up to
-            // 4000 cycles under load, a tile 1600 (one query row) to 3400 (160);
+            // tiles (index, scales), a few ahead of the loads.  A claim takes up to
+            // 4000 cycles under load, a tile 1400 (one query row) to 3400 (160);
             // larger rounds leave the splits of a head further apart at the end
             // (rounds of four: 10000 cycles at T = 40).
             constexpr int kFirst = 4, kRound = NG == 2 ? 4 : 1;
@@ -934,138 +983,139 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 }
                 if (tile >= 0)
                     owner[tile] = (uint8_t)split;
+                else   // (the second group's end)
+                    aux->scale_of[(t + 1) & (kTileRing - 1)][0].w = __int_as_float(kEndMark);
             };
             int base = claim(kRound);
             int my_tile = tile_at(split + lane * n_split);
             post(lane, my_tile, kFirst);
             __syncwarp();
-            const uint64_t pol = l2_evict_first_policy();
-            Ring rk(SK), rv(SV);
-            int ke = 0;             // K ring entries used
-            int vn = 0;             // V ring entries used
-            int k_tma = -1, v_tma = -1;   // last entries that were TMA loads
-            bool ok = true, more = true;
-            auto issue_v = [&](int t) {
-                const int s = rv.i;
-                if (t >= SV && !lane_wait(smem_addr(&bar->empty_v[s]), rv.ph ^ 1, abort, hdr))
-                    return false;
-                rv.next();
-                const uint32_t fb = smem_addr(&bar->full_v[s]);
-                const int tile = bar->tile_of[t & (kTileRing - 1)];
-                if (tile < 0 || tile >= nq) {
-                    mbar_arrive(fb);   // the end, or a tail tile: the converters read it themselves
-                } else {
-                    mbar_arrive_expect_tx(fb, kRawBytes);
-                    tma_load_3d_hint(smem_addr(sV + s * kRawBytes), &tmap_v, 0, tile * kTileN, g, fb, pol);
-                    v_tma = t;
-                }
-                return true;
-            };
-            for (int i = 0; ok && more; ++i) {
-                const int tile = max(-1, __shfl_sync(0xffffffffu, my_tile, i < kFirst ? i : (i - kFirst) % kRound));
-                if (lane == 0) {
-                    const bool tail = tile >= nq;
-                    if (tail)
-                        bar->entry_of[i & (kTileRing - 1)] = ke;
-                    for (int part = 0; part < (tail ? 2 : 1); ++part, ++ke, rk.next()) {
-                        const int s = rk.i;
-                        if (ke >= SK && !lane_wait(smem_addr(&bar->empty_k[s]), rk.ph ^ 1, abort, hdr)) {
-                            ok = false;
-                            break;
-                        }
-                        const uint32_t fb = smem_addr(&bar->full_k[s]);
-                        if (tile < 0) {
-                            // (the second group's end may lie in a round of its own)
-                            aux->scale_of[(i + 1) & (kTileRing - 1)][0].w = __int_as_float(kEndMark);
-                            mbar_arrive(fb);   // no tile left: the QK issuer passes it on
-                        } else if (!tail) {
-                            mbar_arrive_expect_tx(fb, kRawBytes);
-                            tma_load_3d_hint(smem_addr(sK + s * kRawBytes), &tmap_k, 0, tile * kTileN, g,
-                                             fb, pol);
-                            k_tma = ke;
-                        }   // a tail tile's slots, free now, are filled by the converters
-                    }
-                    mbar_arrive(smem_addr(&bar->info[i & (kTileRing - 1)]));
-                    while (ok && (vn < i || (vn == i && tile < 0)))   // V one tile behind K
-                        ok = issue_v(vn++);
-                }
-                ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
-                more = tile >= 0;
-                if (more && i >= kFirst - 1 && (i - (kFirst - 1)) % kRound == 0) {
+            if (lane == 0)
+                for (int i = 0; i < kFirst; ++i)
+                    mbar_arrive(smem_addr(&bar->info[i]));
+            int posted = kFirst;
+            bool more = __shfl_sync(0xffffffffu, my_tile, kFirst - 1) >= 0;
+            Ring rv(SV);
+            int v_tma = -1;
+            for (int step = 0;; ++step) {
+                // V one tile behind K where both are this warp's
+                const int t = k_split ? step : step - 1;
+                if (more && posted - t <= 2) {
                     my_tile = tile_at(kFirst * n_split + __shfl_sync(0xffffffffu, base, 0) + lane);
-                    base = claim(kRound);
-                    post(i + 1 + lane, my_tile, kRound);
-                    __syncwarp();
-                }
-            }
-            if (lane == 0 && *abort) {
-                // our own copies land before the CTA exits
-                for (int t = max(0, k_tma - SK + 1); t <= k_tma; ++t)
-                    wait_drain(smem_addr(&bar->full_k[t % SK]), (t / SK) & 1);
-                for (int t = max(0, v_tma - SV + 1); t <= v_tma; ++t)
-                    wait_drain(smem_addr(&bar->full_v[t % SV]), (t / SV) & 1);
-            }
-        } else if (warp == 0) {
-            // ------------------------------------ root node's scores out of S
-            if (rs_warp0) {
-                const int r = lane >> 2;
-                const bool mine = r < G;
-                const int c0 = 2 * (lane & 3);
-                const float rsc = aux->row_scale[NB == 2 ? kBlockM + (mine ? r : 0) : (mine ? r : 0)];
-                float *dst_row = a.root_scores + (size_t)(g * G + (mine ? r : 0)) * n_ctx;
-                const bool vec = ((reinterpret_cast<uintptr_t>(a.root_scores) | (uintptr_t)n_ctx * 4) & 7) == 0;
-                Ring rs(SI);
-                for (int t = 0;; ++t, rs.next()) {
-                    const int slot = NB == 2 ? 1 : (t & 1), sb = NB == 2 ? 1 : rs.i;
-                    if (!warp_wait(smem_addr(&bar->s_full[sb]), rs.ph, abort, hdr))
-                        break;
-                    const int tile = bar->tile_of[t & (kTileRing - 1)];
-                    if (tile < 0)
-                        break;
-                    tc_fence_after();
-                    const bool q8 = tile < nq;
-                    const int r0 = (q8 ? tile : tile - nq) * kTileN;
-                    const int left = (q8 ? kc.n_q8 : kc.n_tail) - r0;   // context positions here
-                    const int pos0 = q8 ? r0 : kc.n_q8 + r0;
-#pragma unroll 1
-                    for (int h = 0; h < 2; ++h) {
-                        const int lh = left - 64 * h;
-                        if (lh <= 0)
-                            break;   // uniform: nothing of the context from here on
-                        uint32_t rr[32];
-                        tmem_ld16x256_x8(tmem + kSCol + 128 * slot + 64 * h, rr);
-                        if (mine) {
-                            const float f = rsc * aux->scale_of[t & (kTileRing - 1)][h].x;
-                            float *dst = dst_row + pos0 + 64 * h + c0;
-                            unsigned long long nan = 0ull;
-                            if (!q8)
-                                nan = bar->bad_k[t & 3][2 * h] |
-                                      ((unsigned long long)bar->bad_k[t & 3][2 * h + 1] << 32);
-                            if (vec && lh >= 64 && nan == 0ull) {
-#pragma unroll
-                                for (int j = 0; j < 8; ++j)
-                                    *reinterpret_cast<float2 *>(dst + 8 * j) =
-                                        make_float2(__uint_as_float(rr[4 * j]) * f,
-                                                    __uint_as_float(rr[4 * j + 1]) * f);
-                            } else {
-#pragma unroll
-                                for (int k = 0; k < 16; ++k) {
-                                    const int p = 8 * (k >> 1) + c0 + (k & 1);
-                                    if (p < lh)
-                                        dst[8 * (k >> 1) + (k & 1)] =
-                                            (nan >> p) & 1ull ? __uint_as_float(0x7FC00000u)
-                                                              : __uint_as_float(rr[4 * (k >> 1) + (k & 1)]) * f;
-                                }
-                            }
-                        }
-                        __syncwarp();   // the next TMEM load is the whole warp's
-                    }
-                    tc_fence_before();
+                    more = __shfl_sync(0xffffffffu, my_tile, kRound - 1) >= 0;
+                    if (more)
+                        base = claim(kRound);
+                    post(posted + lane, my_tile, kRound);
                     __syncwarp();
                     if (lane == 0)
-                        mbar_arrive(smem_addr(&bar->s_free[sb]));
+                        for (int i = 0; i < kRound; ++i)
+                            mbar_arrive(smem_addr(&bar->info[(posted + i) & (kTileRing - 1)]));
+                    posted += kRound;
                 }
+                if (!k_split && !k_end && !k_step(step))
+                    break;
+                if (t < 0)
+                    continue;
+                const int tile = bar->tile_of[t & (kTileRing - 1)];
+                int ok = 1;
+                if (lane == 0) {
+                    if (t >= SV)
+                        ok = lane_wait(smem_addr(&bar->empty_v[rv.i]), rv.ph ^ 1, abort, hdr);
+                    if (ok) {
+                        const uint32_t fb = smem_addr(&bar->full_v[rv.i]);
+                        if (tile < 0 || tile >= nq) {
+                            mbar_arrive(fb);   // the end, or a tail tile: the converters read it themselves
+                        } else {
+                            mbar_arrive_expect_tx(fb, kRawBytes);
+                            tma_load_3d_hint(smem_addr(sV + rv.i * kRawBytes), &tmap_v, 0, tile * kTileN, g, fb,
+                                             pol);
+                            v_tma = t;
+                        }
+                    }
+                }
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (!ok || tile < 0)
+                    break;
+                rv.next();
             }
+            if (!k_split)
+                k_drain();
+            if (lane == 0 && *abort)   // our own copies land before the CTA exits
+                for (int t = max(0, v_tma - SV + 1); t <= v_tma; ++t)
+                    wait_drain(smem_addr(&bar->full_v[t % SV]), (t / SV) & 1);
+            __syncwarp();
+        } else if (warp == 0) {
+            if (k_split) {
+                // -------------------------------------------- TMA producer of K
+                // (the query rows first: not behind every CTA's first ring)
+                named_bar_sync(kBarQLoads, kQLoadThreads);
+                for (int t = 0; !k_end && k_step(t); ++t) {
+                }
+                k_drain();
+            }
+            // ------------------------------------------------ root node's scores out of S
+            const int r = lane >> 2;
+            const bool mine = r < G;
+            const int c0 = 2 * (lane & 3);
+            float rsc = 0.f;
+            float *dst_row = a.root_scores + (size_t)(g * G + (mine ? r : 0)) * n_ctx;
+            const bool vec = ((reinterpret_cast<uintptr_t>(a.root_scores) | (uintptr_t)n_ctx * 4) & 7) == 0;
+            if (rs_warp0) {
+                named_bar_sync(kBarRows, 32 * (1 + 4 * U * NG));
+                rsc = aux->row_scale[NB == 2 ? kBlockM + (mine ? r : 0) : (mine ? r : 0)];
+            }
+            Ring rs(SI);
+            for (int t = 0; rs_warp0; ++t, rs.next()) {
+                const int slot = NB == 2 ? 1 : (t & 1), sb = NB == 2 ? 1 : rs.i;
+                if (!warp_wait(smem_addr(&bar->s_full[sb]), rs.ph, abort, hdr))
+                    break;
+                const int tile = bar->tile_of[t & (kTileRing - 1)];
+                if (tile < 0)
+                    break;
+                tc_fence_after();
+                const bool q8 = tile < nq;
+                const int r0 = (q8 ? tile : tile - nq) * kTileN;
+                const int left = (q8 ? kc.n_q8 : kc.n_tail) - r0;   // context positions here
+                const int pos0 = q8 ? r0 : kc.n_q8 + r0;
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    const int lh = left - 64 * h;
+                    if (lh <= 0)
+                        break;   // uniform: nothing of the context from here on
+                    uint32_t rr[32];
+                    tmem_ld16x256_x8(tmem + kSCol + 128 * slot + 64 * h, rr);
+                    if (mine) {
+                        const float f = rsc * aux->scale_of[t & (kTileRing - 1)][h].x;
+                        float *dst = dst_row + pos0 + 64 * h + c0;
+                        unsigned long long nan = 0ull;
+                        if (!q8)
+                            nan = bar->bad_k[t & 3][2 * h] |
+                                  ((unsigned long long)bar->bad_k[t & 3][2 * h + 1] << 32);
+                        if (vec && lh >= 64 && nan == 0ull) {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                *reinterpret_cast<float2 *>(dst + 8 * j) =
+                                    make_float2(__uint_as_float(rr[4 * j]) * f,
+                                                __uint_as_float(rr[4 * j + 1]) * f);
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) {
+                                const int p = 8 * (k >> 1) + c0 + (k & 1);
+                                if (p < lh)
+                                    dst[8 * (k >> 1) + (k & 1)] =
+                                        (nan >> p) & 1ull ? __uint_as_float(0x7FC00000u)
+                                                          : __uint_as_float(rr[4 * (k >> 1) + (k & 1)]) * f;
+                            }
+                        }
+                    }
+                    __syncwarp();   // the next TMEM load is the whole warp's
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_addr(&bar->s_free[sb]));
+            }
+            __syncwarp();
         } else if (warp == 1) {
             // ------------------------------------------------ QK issuer
             // (the whole warp keeps the loop, so that descriptors stay uniform;
@@ -1191,7 +1241,7 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
         }
     } else if (warp >= kThreads / 32 - n_conv) {
         // ------------------------------------------------ converters
-        const int tid = threadIdx.x - (kThreads - 32 * n_conv), rows = 2 * n_conv;   // rows per step
+        const int tid = threadIdx.x - 32 * (kThreads / 32 - n_conv), rows = 2 * n_conv;   // rows per step
         // every scale byte of the head, for the producer (one look-up per tile
         // in HBM would cost it more than the tile's stream)
         {
@@ -1337,7 +1387,9 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
             }
         }
         tc_fence_before();
-        named_bar_sync(kBarQuery, kThreads - 32 * (1 + n_conv));
+        if (rs_warp0)
+            named_bar_arrive(kBarRows, 32 * (1 + 4 * U * NG));
+        named_bar_sync(kBarQuery, 32 * (2 + 4 * U * NG));
         tc_fence_after();
         if ((warp - 4) / 4 < U * NG) {
             // ------------------------------------------------ softmax
@@ -1458,7 +1510,8 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
             // (T = 13: 66 us against 71, T = 40: 98 against 104).
             auto pass = [&](auto special, const float4 *scl, uint32_t s0, int t, uint32_t atA, uint32_t atB,
                             uint32_t bar_free) {
-                uint32_t r0[NG == 2 ? 32 : 16], r1[16];
+                uint32_t r0[NG == 2 ? 32 : 16];
+                [[maybe_unused]] uint32_t r1[16];
                 if constexpr (NG == 1) {
                     tmem_ld16x256_x4(s0, r0);
                     tmem_ld_wait16(r0);
