@@ -98,7 +98,7 @@ __device__ __forceinline__ void form_angles(const RopeArgs &a, const Depths &dep
 // unit c >= hc the chunk c + hc.  A thread has kUnits units' loads in flight,
 // the first of them while the run's angles are formed.
 // HBM-bound on a prompt: on 8190 tokens of 56 heads of 128 (235 MB) a CTA per
-// token took 86-95 us, each waiting for its own angles; runs of tokens NN us.
+// token took 86-95 us, each waiting for its own angles; runs of tokens 53 us.
 constexpr int kUnits = 4, kMaxAngles = 512;
 template <int D, bool INTER>
 __global__ void __launch_bounds__(kThreads)

@@ -449,3 +449,123 @@ def test_a_cache_on_another_device_is_refused():
     with pytest.raises(ValueError):
         L.tree_verify_attn_q8(torch.zeros(4, 8, 128, dtype=torch.bfloat16, device="cuda"), cache,
                               [-1, 0, 1, 2])
+
+
+# ------------------------------------------- both attention kernels' borders
+BORDERS = [
+    (16, 4, 128, 704, 60, 3, "bfs"),      # 767 positions: the last of the short kernel's
+    (16, 4, 128, 704, 60, 4, "bfs"),      # 768
+    (32, 8, 128, 768, 0, 1, "chain"),
+    (4, 4, 128, 0, 900, 5, "random"),     # bf16 rows alone: up to 64 query rows a head,
+    (24, 8, 128, 0, 777, 40, "random"),   # up to 128,
+    (32, 8, 128, 0, 1500, 40, "bfs"),     # up to 192
+    (24, 8, 128, 832, 130, 40, "random"),
+    (16, 1, 128, 1024, 63, 4, "star"),    # 64 rows a head
+    (13, 1, 128, 1024, 63, 5, "star"),    # 65
+    (32, 1, 128, 1024, 63, 6, "random"),  # 192
+    (50, 1, 128, 1024, 10, 5, "bfs"),     # whole nodes of 50 rows: groups of 2, 2 and 1
+    (130, 1, 128, 1024, 10, 2, "bfs"),    # a node's rows fit no block
+    (10, 1, 128, 1024, 10, 13, "random"),   # root scores of more than 8 heads
+    (160, 160, 128, 832, 10, 3, "bfs"),   # more KV heads than SMs
+    (74, 74, 128, 832, 10, 3, "bfs"),
+]
+
+
+@pytest.mark.parametrize("root", [False, True])
+@pytest.mark.parametrize("shape", BORDERS, ids=lambda s: "-".join(map(str, s)))
+def test_attention_borders(shape, root):
+    check_attention(sum(map(len, map(str, shape))), *shape, root=root)
+
+
+def test_attention_of_a_million_positions():
+    """A head's scale bytes in shared memory (2 x 16 KB), 8-bit tiles numbered
+    past 2^13; the plain form takes one head."""
+    check_attention(80, 1, 1, 128, 1 << 20, 5, 2, "chain")
+
+
+@pytest.mark.parametrize("n_q8", [128, 1024])
+def test_attention_past_32_bits_of_elements(n_q8):
+    """A head's rows start past element 2^31 of the codes and of the tail."""
+    hkv, d, cap, n_tail, t = 18, 128, 1 << 20, 9, 4
+    c = P8.cache_inputs(81, hkv, d, n_q8, n_tail, t)
+    k8, v8 = (torch.zeros(hkv, cap, d, dtype=torch.uint8, device="cuda") for _ in range(2))
+    scales = [torch.zeros(hkv, cap // 64, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    k_tail, v_tail = (torch.zeros(hkv, cap, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    for dst, name in ((k8, "k8"), (v8, "v8")):
+        dst[:, :n_q8] = c[name].view(torch.uint8).cuda()[:, :n_q8]
+    for dst, name in zip(scales, ("k_scale", "v_scale")):
+        dst[:, :n_q8 // 64] = c[name].cuda()[:, :n_q8 // 64]
+    row0 = cap - n_tail - t
+    for dst, name in ((k_tail, "k_tail"), (v_tail, "v_tail")):
+        dst[:, row0:] = c[name].cuda()
+    cache = L.KvCacheQ8(k8.view(torch.float8_e4m3fn), v8.view(torch.float8_e4m3fn), *scales, k_tail,
+                        v_tail, n_q8=n_q8, n_tail=n_tail, tail_row0=row0)
+    q, parent = queries(81, t, 2 * hkv, d), P8.parents("bfs", t)
+    out = L.tree_verify_attn_q8(q.cuda(), cache, parent)
+    k, v = (P8.cache_rows(c, x, n_q8, 0, n_tail + t) for x in "kv")
+    want, bound, _, _ = P8.attention(q, k, v, n_q8 + n_tail, parent, d ** -0.5)
+    assert bool(((out.double().cpu() - want).abs() <= bound).all())
+
+    # the same rows gathered, and the tail's last 64 quantised behind the codes
+    idx = torch.arange(n_q8 + n_tail, dtype=torch.int32, device="cuda").expand(hkv, -1).contiguous()
+    kp, vp = L.kv_gather_q8(cache, idx)
+    assert torch.equal(kp.double().cpu(), k[:, :n_q8 + n_tail])
+    assert torch.equal(vp.double().cpu(), v[:, :n_q8 + n_tail])
+    L.kv_quantize_q8(k_tail, v_tail, cap - 64, 64, cache.k8, cache.v8, *scales, cap - 64)
+    for rows, codes, byte in ((k_tail, cache.k8, scales[0]), (v_tail, cache.v8, scales[1])):
+        wc, wb = P8.quantize(rows[:, cap - 64:].cpu())
+        assert torch.equal(codes[:, cap - 64:].float().double().cpu(), wc)
+        assert torch.equal(byte[:, -1:].cpu(), wb)
+
+
+def test_attention_on_two_streams_at_once():
+    """Calls on two streams, each with its workspace, in no order between them."""
+    jobs = []
+    for seed, (hq, hkv, d, n_q8, n_tail, t) in ((82, (16, 4, 128, 8192, 9, 13)),
+                                               (83, (16, 4, 128, 4096, 63, 40)),
+                                               (84, (8, 2, 64, 2048, 9, 5))):
+        c, cache = make(seed, hkv, d, n_q8, n_tail, t)
+        q, parent = queries(seed, t, hq, d), P8.parents("bfs", t)
+        k, v = (P8.cache_rows(c, n, n_q8, 0, n_tail + t) for n in "kv")
+        want, bound, _, _ = P8.attention(q, k, v, n_q8 + n_tail, parent, d ** -0.5)
+        ws = L.new_workspace(L.tree_verify_attn_q8_workspace_size(hq, hkv, d, n_q8, n_tail, t))
+        jobs.append((torch.cuda.Stream(), q.cuda(), cache, parent, ws, want, bound))
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(20):
+        for s, q, cache, parent, ws, _, _ in jobs:
+            out = torch.empty_like(q)
+            L.tree_verify_attn_q8(q, cache, parent, out=out, workspace=ws, stream=s)
+            outs.append(out)
+    torch.cuda.synchronize()
+    for i, out in enumerate(outs):
+        _, _, _, _, ws, want, bound = jobs[i % len(jobs)]
+        assert L.workspace_status(ws) == 0
+        assert bool(((out.double().cpu() - want).abs() <= bound).all()), i
+
+
+def test_a_cache_keeps_its_rows_in_bounds():
+    cache = L.KvCacheQ8.empty(2, 64, 64, tail_rows=140)
+    assert cache.n_ctx == 0 and cache.fold() == 0
+    fused = torch.zeros(140, 6, 64, dtype=torch.bfloat16, device="cuda")
+    q, k, v = fused.split([2, 2, 2], 1)
+    freq = L.rope_inv_freq(64, 1e4)[0].cuda()
+    with pytest.raises(L.TsError):           # one row more than the tail has
+        cache.append(torch.cat([q, q[:1]]), torch.cat([k, k[:1]]), torch.cat([v, v[:1]]), freq)
+    cache.append(q, k, v, freq)
+    assert (cache.n_q8, cache.n_tail) == (0, 140)
+    with pytest.raises(L.TsError):           # two blocks, room for one
+        cache.fold()
+    assert (cache.n_q8, cache.n_tail, cache.tail_row0) == (0, 140, 0)
+    accept = torch.zeros(8, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):          # a tree behind the tail's end
+        cache.commit(accept, 1, 0)
+    cache = L.KvCacheQ8.empty(2, 64, 64, tail_rows=140)
+    for n_tree, n_accepted in ((4, 4), (4, -1), (0, 0)):
+        with pytest.raises(ValueError):
+            cache.commit(accept, n_tree, n_accepted)
+    for kw in ({"n_q8": 63}, {"n_q8": 128}, {"n_q8": -64}, {"n_tail": 141}, {"n_tail": -1},
+               {"tail_row0": -1}, {"n_tail": 100, "tail_row0": 41}):
+        with pytest.raises(ValueError):
+            L.KvCacheQ8(cache.k8, cache.v8, cache.k_scale, cache.v_scale, cache.k_tail, cache.v_tail,
+                        **kw)
