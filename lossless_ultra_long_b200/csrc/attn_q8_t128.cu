@@ -452,11 +452,20 @@ __device__ __forceinline__ unsigned long long row_vis(unsigned long long anc, in
     return d > 0 ? ((1ull << d) - 1ull) | (anc << d) : (d > -64 ? anc >> -d : 0ull);
 }
 
+// s0 += the low bf16 value of w, s1 += the high one.
+__device__ __forceinline__ void add_pair(float &s0, float &s1, uint32_t w)
+{
+    asm("{.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tadd.rn.f32.bf16 %0, l, %0;\n\tadd.rn.f32.bf16 %1, h, %1;}"
+        : "+f"(s0), "+f"(s1) : "r"(w));
+}
+
 // Weights 2^(x * c + n) of the 2 J scores a thread holds of row E / 2 (E = 0:
-// row A, E = 2: row B) of 8 J positions, packed to bf16 pairs; adds them to sum.
+// row A, E = 2: row B) of 8 J positions, packed to bf16 pairs; adds the rounded
+// weights to sum0 and sum1, so that a rounding moves the result only by how far its
+// position's value lies from the result.
 template <int E, int J>
 __device__ __forceinline__ void exp_row(const uint32_t (&r)[4 * J], float c, float n, uint32_t (&p)[J],
-                                        uint64_t &sum)
+                                        float &sum0, float &sum1)
 {
     const uint64_t c2 = pack2(c, c), n2 = pack2(n, n);
 #pragma unroll
@@ -468,7 +477,7 @@ __device__ __forceinline__ void exp_row(const uint32_t (&r)[4 * J], float c, flo
         const float x0 = ex2(y0), x1 = ex2(y1);
         const __nv_bfloat162 hv = __floats2bfloat162_rn(x0, x1);
         p[j] = *reinterpret_cast<const uint32_t *>(&hv);
-        sum = add2(sum, pack2(x0, x1));
+        add_pair(sum0, sum1, p[j]);
     }
 }
 
@@ -1443,7 +1452,7 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
             // Part of a half tile in registers (8 J positions, from the half's
             // 32 odd on): weights to P^T
             auto part = [&](auto &r, auto jc, auto special, int odd, int left, int t, int h, float cA, float cB, float ve,
-                            uint64_t &sA, uint64_t &sB, uint32_t atA, uint32_t atB) {
+                            float (&sum)[4], uint32_t atA, uint32_t atB) {
                 constexpr int J = decltype(jc)::value;
                 constexpr bool kSpecial = decltype(special)::value != 0;
                 if (kSpecial && (left < 64 || left > kTailMark / 2)) {
@@ -1493,9 +1502,9 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     fresh = __any_sync(0xffffffffu, (vA && mA == -INFINITY) || (vB && mB == -INFINITY));
                 }
                 uint32_t pA[J], pB[J];
-                exp_row<0, J>(r, cA, nmA + ve, pA, sA);
+                exp_row<0, J>(r, cA, nmA + ve, pA, sum[0], sum[1]);
                 if (hasB)
-                    exp_row<2, J>(r, cB, nmB + ve, pB, sB);
+                    exp_row<2, J>(r, cB, nmB + ve, pB, sum[2], sum[3]);
                 if (NG == 2 && h == 0 && t >= 2 &&
                     !warp_wait(smem_addr(&bar->pv_done[grp]), rps.ph ^ 1, abort, hdr))
                     ok = false;
@@ -1535,9 +1544,9 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     constexpr float kTiny = 1.17549435e-38f;
                     const float cA = fmaxf(rsA * sc.x, kTiny), cB = fmaxf(rsB * sc.x, kTiny);
                     const int left = __float_as_int(sc.w);
-                    uint64_t sA = 0ull, sB = 0ull;
+                    float sum[4] = {};
                     if constexpr (NG == 1) {
-                        part(r0, Const<4>(), special, 0, left, t, h, cA, cB, sc.y, sA, sB, atA, atB);
+                        part(r0, Const<4>(), special, 0, left, t, h, cA, cB, sc.y, sum, atA, atB);
                         tmem_ld_wait16(r1);
                     }
                     if (h == 0) {
@@ -1551,14 +1560,11 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                             mbar_arrive(bar_free);
                     }
                     if constexpr (NG == 1)
-                        part(r1, Const<4>(), special, 1, left, t, h, cA, cB, sc.y, sA, sB, atA, atB);
+                        part(r1, Const<4>(), special, 1, left, t, h, cA, cB, sc.y, sum, atA, atB);
                     else
-                        part(r0, Const<8>(), special, 0, left, t, h, cA, cB, sc.y, sA, sB, atA, atB);
-                    float a0, a1;
-                    unpack2(sA, a0, a1);
-                    lA += (a0 + a1) * sc.z;
-                    unpack2(sB, a0, a1);
-                    lB += (a0 + a1) * sc.z;
+                        part(r0, Const<8>(), special, 0, left, t, h, cA, cB, sc.y, sum, atA, atB);
+                    lA += (sum[0] + sum[1]) * sc.z;
+                    lB += (sum[2] + sum[3]) * sc.z;
                     atA += p_stepA;
                     atB += p_stepB;
                     if constexpr (NG == 1)

@@ -79,8 +79,11 @@ def attention(q, k, v, n_ctx, parent, scale):
     float64 [Hkv, n_ctx + T, D].
 
     bound: how far a kernel's bf16 output may be.  Its weights carry one
-    rounding to bf16 (2^-8 of each; their sum is taken in 32 bits), its result
-    another.  A score sums D products in 32 bits, where each addition (the
+    rounding to bf16, its result another (2^-8 of each).  With the weights' sum
+    taken before their rounding, w_j (1 + e_j) in place of w_j moves the result
+    by sum w_j e_j v_j, at most 2^-8 sum w_j |v_j|; with the rounded weights'
+    own sum by sum w_j e_j (v_j - out) / (1 + sum w_j e_j), at most
+    2^-8 sum w_j |v_j - out| (1 + 2^-7).  Sums are taken in 32 bits.  A score sums D products in 32 bits, where each addition (the
     tensor core may cut instead of round) loses at most 2^-23 of the sum of
     magnitudes, and 2^-20 of it for the query's split into 8-bit parts; a
     score's error e changes a weight by the factor exp(e), and the weights'
@@ -106,9 +109,10 @@ def attention(q, k, v, n_ctx, parent, scale):
             at = torch.cat([torch.arange(n_ctx), n_ctx + vis[i].nonzero()[:, 0]])
             w = torch.softmax(x[i, at], 0)
             o, a = w @ vh[at], w @ vh[at].abs()
+            move = torch.maximum(a, w @ (vh[at] - o).abs())
             out[i, h] = o
             eta = 2 * float(mag[i, at].max()) * per + 2.0 ** -18
-            bound[i, h] = 2.0 ** -8 * (a + o.abs()) * (1 + 2.0 ** -7) + a * eta + 1e-30
+            bound[i, h] = 2.0 ** -8 * (move + o.abs()) * (1 + 2.0 ** -7) + a * eta + 1e-30
     return out, bound, root, root_bound
 
 
