@@ -9,6 +9,7 @@ call raises.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 
@@ -151,19 +152,27 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+_Tensor, _BF16, _I32 = torch.Tensor, torch.bfloat16, torch.int32
+
 # the current stream's handle without a Stream object around it (2 us a call)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream):
+def _stream(stream, device=None):
+    """A stream's handle; without one, the current stream's of ``device`` (the
+    current device where that is None)."""
     if stream is not None:
         return stream.cuda_stream
     if _raw_stream is not None:
-        return _raw_stream(torch.cuda.current_device())
-    return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(torch.cuda.current_device() if device is None else device.index)
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 def _check_dev(name, t, dtype, device=None):
+    # what every right call passes, in one test (checks are most of its host time)
+    if (type(t) is _Tensor and t.dtype is dtype and t.is_contiguous() and
+            (t.is_cuda if device is None else t.device == device and t.is_cuda)):
+        return
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
@@ -194,7 +203,7 @@ def _ws_bytes(workspace, device):
         raise ValueError(f"workspace is on {workspace.device}, the call's tensors on {device}")
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    return workspace.numel() * workspace.element_size()
+    return workspace.nbytes
 
 
 def _host_i32(a):
@@ -206,6 +215,14 @@ def _host_i32(a):
 
 def _parent_arg(parent, n):
     """(keep-alive, address) of a host int32 parent array of n entries."""
+    if type(parent) is list:
+        try:   # a third of numpy's time for a list of integers
+            ints = array.array("i", parent)
+            if len(ints) != n:
+                raise ValueError("parent must have one entry per tree node")
+            return ints, ints.buffer_info()[0]
+        except (TypeError, OverflowError):
+            pass
     import numpy as np
     if isinstance(parent, torch.Tensor):
         parent = parent.cpu().numpy()
@@ -511,10 +528,10 @@ def rope_inv_freq(rot_dim: int, base: float, kind: str = "plain", *params):
 def _check_rows(name, t, heads, d, device):
     """A bf16 [tokens, heads, D] tensor whose tokens may lie apart: the
     elements from one token to the next."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not isinstance(t, _Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
-        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dtype is not _BF16:
+        raise ValueError(f"{name} must be {_BF16}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the call's other tensors on {device}")
     shape = t.shape
@@ -538,8 +555,8 @@ def rope_append(q, k, v, k_cache, v_cache, row0: int, pos0: int, inv_freq, paren
     (positions pos0 + i).  Returns the turned queries, bf16 [n, Hq, D].
     """
     dev = _call_device("k", k)
-    _check_dev("k_cache", k_cache, torch.bfloat16, dev)
-    _check_dev("v_cache", v_cache, torch.bfloat16, dev)
+    _check_dev("k_cache", k_cache, _BF16, dev)
+    _check_dev("v_cache", v_cache, _BF16, dev)
     if k_cache.dim() != 3 or v_cache.shape != k_cache.shape:
         raise ValueError("k_cache and v_cache must be [Hkv, kv_cap, D]")
     hkv, cap, d = k_cache.shape
@@ -549,9 +566,9 @@ def rope_append(q, k, v, k_cache, v_cache, row0: int, pos0: int, inv_freq, paren
     if q is not None:
         qs, hq = _check_rows("q", q, None, d, dev), q.shape[1]
         if q_out is None:
-            q_out = torch.empty((n, hq, d), dtype=torch.bfloat16, device=dev)
-        _check_dev("q_out", q_out, torch.bfloat16, dev)
-        if tuple(q_out.shape) != (n, hq, d):
+            q_out = torch.empty((n, hq, d), dtype=_BF16, device=dev)
+        _check_dev("q_out", q_out, _BF16, dev)
+        if q_out.shape != q.shape:
             raise ValueError("q_out must have q's shape")
     if v.shape[0] != n or (q is not None and q.shape[0] != n):
         raise ValueError("q, k and v must have as many tokens")
@@ -564,7 +581,7 @@ def rope_append(q, k, v, k_cache, v_cache, row0: int, pos0: int, inv_freq, paren
         _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, hq, hkv, d, n, par_p, int(pos0),
         _ptr(inv_freq) if rot else None, rot, int(bool(interleaved)), float(mscale),
         _ptr(q_out) if hq else None, _ptr(k_cache), _ptr(v_cache), cap, int(row0),
-        _stream(stream)), "ts_rope_append")
+        _stream(stream, dev)), "ts_rope_append")
     return q_out
 
 
@@ -585,16 +602,16 @@ def kv_quantize_q8(k, v, row0: int, n_rows: int, k8, v8, k_scale, v_scale, dst_r
     """Rows [row0, row0 + n_rows) of bf16 k and v [Hkv, cap, D] into 8-bit rows
     [dst_row, dst_row + n_rows) and their blocks' scales
     (``ts_kv_quantize_q8``); n_rows and dst_row multiples of 64."""
-    _check_dev("k", k, torch.bfloat16)
+    _check_dev("k", k, _BF16)
     dev = _call_device("k", k)
-    _check_dev("v", v, torch.bfloat16, dev)
+    _check_dev("v", v, _BF16, dev)
     _check_q8(k8, v8, k_scale, v_scale, dev)
     if k.dim() != 3 or v.shape != k.shape or k.shape[0] != k8.shape[0] or k.shape[2] != k8.shape[2]:
         raise ValueError("k / v / k8 / v8 shapes disagree")
     hkv, cap, d = k.shape
     _raise(_lib().ts_kv_quantize_q8(_ptr(k), _ptr(v), cap, hkv, d, int(row0), int(n_rows), _ptr(k8),
                                     _ptr(v8), _ptr(k_scale), _ptr(v_scale), k8.shape[1],
-                                    int(dst_row), _stream(stream)), "ts_kv_quantize_q8")
+                                    int(dst_row), _stream(stream, dev)), "ts_kv_quantize_q8")
     return k8, v8, k_scale, v_scale
 
 
@@ -613,8 +630,8 @@ class KvCacheQ8:
                  tail_row0: int = 0):
         dev = _call_device("k_tail", k_tail)
         _check_q8(k8, v8, k_scale, v_scale, dev)
-        _check_dev("k_tail", k_tail, torch.bfloat16, dev)
-        _check_dev("v_tail", v_tail, torch.bfloat16, dev)
+        _check_dev("k_tail", k_tail, _BF16, dev)
+        _check_dev("v_tail", v_tail, _BF16, dev)
         if (k_tail.dim() != 3 or v_tail.shape != k_tail.shape or
                 k_tail.shape[0] != k8.shape[0] or k_tail.shape[2] != k8.shape[2]):
             raise ValueError("k_tail and v_tail must be [Hkv, rows, D] as k8")
@@ -653,7 +670,7 @@ class KvCacheQ8:
         scales = [torch.zeros((n_heads_kv, cap // TS_Q8_BLOCK), dtype=torch.uint8, device=device)
                   for _ in range(2)]
         return cls(new(cap, None).view(torch.float8_e4m3fn), new(cap, None).view(torch.float8_e4m3fn),
-                   *scales, new(int(tail_rows), torch.bfloat16), new(int(tail_rows), torch.bfloat16))
+                   *scales, new(int(tail_rows), _BF16), new(int(tail_rows), _BF16))
 
     @property
     def n_ctx(self) -> int:
@@ -682,7 +699,7 @@ class KvCacheQ8:
         caller."""
         if not 0 <= int(n_accepted) < int(n_tree):
             raise ValueError("n_accepted must lie in [0, n_tree)")
-        _check_dev("accept", accept, torch.int32, self.device)
+        _check_dev("accept", accept, _I32, self.device)
         dev = _call_device("k_tail", self.k_tail)
         if workspace is None:
             workspace = new_workspace(256, dev)
@@ -693,7 +710,7 @@ class KvCacheQ8:
         _raise(_lib().ts_kv_commit_path(
             ctypes.c_void_p(self.k_tail.data_ptr() + off),
             ctypes.c_void_p(self.v_tail.data_ptr() + off), cap, hkv, d, self.n_tail, int(n_tree),
-            _ptr(accept), _ptr(workspace), _ws_bytes(workspace, dev), _stream(stream)),
+            _ptr(accept), _ptr(workspace), _ws_bytes(workspace, dev), _stream(stream, dev)),
             "ts_kv_commit_path")
         self.n_tail += int(n_accepted) + 1
 
@@ -740,7 +757,7 @@ def tree_verify_attn_q8(q, cache: KvCacheQ8, parent, out=None, workspace=None,
     the tree's rows lie in the tail behind the context.  q: bf16 [T, Hq, D];
     returns bf16 [T, Hq, D].  ``root_scores_out``: fp32 [Hq, n_ctx], as for
     :func:`tree_verify_attn`."""
-    _check_dev("q", q, torch.bfloat16)
+    _check_dev("q", q, _BF16)
     dev, st = _call_cache(cache)
     if q.device != dev:
         raise ValueError(f"q is on {q.device}, the call's other tensors on {dev}")
@@ -748,9 +765,9 @@ def tree_verify_attn_q8(q, cache: KvCacheQ8, parent, out=None, workspace=None,
     if d != st.head_dim:
         raise ValueError("q and the cache must have the same head_dim")
     if out is None:
-        out = torch.empty((t, hq, d), dtype=torch.bfloat16, device=dev)
-    _check_dev("out", out, torch.bfloat16, dev)
-    if tuple(out.shape) != (t, hq, d):
+        out = torch.empty((t, hq, d), dtype=_BF16, device=dev)
+    _check_dev("out", out, _BF16, dev)
+    if out.shape != q.shape:
         raise ValueError("out must have q's shape")
     if root_scores_out is not None:
         _check_dev("root_scores_out", root_scores_out, torch.float32, dev)
@@ -763,7 +780,7 @@ def tree_verify_attn_q8(q, cache: KvCacheQ8, parent, out=None, workspace=None,
     scale = float(d) ** -0.5 if softmax_scale is None else float(softmax_scale)
     rc = _lib().ts_tree_verify_attn_q8(
         ctypes.byref(st), _ptr(q), hq, t, par_p, scale, _ptr(out), _ptr(root_scores_out),
-        _ptr(workspace), _ws_bytes(workspace, dev), _stream(stream))
+        _ptr(workspace), _ws_bytes(workspace, dev), _stream(stream, dev))
     _raise(rc, "ts_tree_verify_attn_q8")
     return out
 
@@ -771,11 +788,11 @@ def tree_verify_attn_q8(q, cache: KvCacheQ8, parent, out=None, workspace=None,
 def _q8_partials(cache, n_keep, k_partial, v_partial, dev):
     hkv, _, d = cache.k8.shape
     if k_partial is None:
-        k_partial = torch.empty((hkv, n_keep, d), dtype=torch.bfloat16, device=dev)
+        k_partial = torch.empty((hkv, n_keep, d), dtype=_BF16, device=dev)
     if v_partial is None:
         v_partial = torch.empty_like(k_partial)
-    _check_dev("k_partial", k_partial, torch.bfloat16, dev)
-    _check_dev("v_partial", v_partial, torch.bfloat16, dev)
+    _check_dev("k_partial", k_partial, _BF16, dev)
+    _check_dev("v_partial", v_partial, _BF16, dev)
     if (k_partial.dim() != 3 or k_partial.shape[0] != hkv or k_partial.shape[2] != d or
             v_partial.shape != k_partial.shape):
         raise ValueError("k_partial and v_partial must be [Hkv, rows, D]")
@@ -787,7 +804,7 @@ def kv_gather_q8(cache: KvCacheQ8, idx, k_partial=None, v_partial=None, workspac
     """Context rows ``idx`` (int32 [Hkv, n_keep]) of an 8-bit cache as bf16 rows
     (``ts_kv_gather_q8``).  Returns ``(k_partial, v_partial)``."""
     dev, st = _call_cache(cache)
-    _check_dev("idx", idx, torch.int32, dev)
+    _check_dev("idx", idx, _I32, dev)
     if idx.dim() != 2 or idx.shape[0] != st.n_heads_kv:
         raise ValueError("idx must be [Hkv, n_keep]")
     k_partial, v_partial = _q8_partials(cache, idx.shape[1], k_partial, v_partial, dev)
@@ -795,7 +812,7 @@ def kv_gather_q8(cache: KvCacheQ8, idx, k_partial=None, v_partial=None, workspac
         workspace = new_workspace(256, dev)
     _raise(_lib().ts_kv_gather_q8(
         ctypes.byref(st), _ptr(idx), idx.shape[1], _ptr(k_partial), _ptr(v_partial),
-        k_partial.shape[1], _ptr(workspace), _ws_bytes(workspace, dev), _stream(stream)),
+        k_partial.shape[1], _ptr(workspace), _ws_bytes(workspace, dev), _stream(stream, dev)),
         "ts_kv_gather_q8")
     return k_partial, v_partial
 
@@ -818,8 +835,8 @@ def kv_select_from_scores_q8(root_scores, cache: KvCacheQ8, n_sink: int, budget:
     n_keep = min(n_ctx, int(n_sink) + int(budget))
     k_partial, v_partial = _q8_partials(cache, n_keep, k_partial, v_partial, dev)
     if idx_out is None:
-        idx_out = torch.empty((hkv, n_keep), dtype=torch.int32, device=dev)
-    _check_dev("idx_out", idx_out, torch.int32, dev)
+        idx_out = torch.empty((hkv, n_keep), dtype=_I32, device=dev)
+    _check_dev("idx_out", idx_out, _I32, dev)
     if idx_out.numel() != hkv * n_keep:
         raise ValueError("idx_out must be [Hkv, n_keep]")
     if want_scores and scores_out is None:
@@ -833,7 +850,7 @@ def kv_select_from_scores_q8(root_scores, cache: KvCacheQ8, n_sink: int, budget:
     _raise(_lib().ts_kv_select_from_scores_q8(
         _ptr(root_scores), ctypes.byref(st), hq, int(n_sink), int(budget), _ptr(scores_out),
         _ptr(idx_out), _ptr(k_partial), _ptr(v_partial), k_partial.shape[1], _ptr(workspace),
-        _ws_bytes(workspace, dev), _stream(stream)), "ts_kv_select_from_scores_q8")
+        _ws_bytes(workspace, dev), _stream(stream, dev)), "ts_kv_select_from_scores_q8")
     return idx_out, k_partial, v_partial, scores_out
 
 
