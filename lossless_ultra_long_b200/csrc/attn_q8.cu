@@ -22,7 +22,6 @@
 #include <math.h>
 
 #include "attn_q8.cuh"
-#include "sm100.cuh"
 
 namespace ts {
 namespace {
@@ -31,7 +30,7 @@ constexpr int kTile = kQ8Block;
 constexpr int kStages = 3;
 constexpr int kMaxWarps = 12;    // 192 query rows per CTA
 // Contexts of at most so many tiles are one split: two tiles in turn cost less
-// than a second launch for the combine.  Four tiles (212 positions, D = 64) are
+// than the meeting of two splits.  Four tiles (212 positions, D = 64) are
 // 6.2 us as four splits with their combine and 10.2 us as one split.
 constexpr int kOneSplit = 2;
 
@@ -100,18 +99,91 @@ struct Shape {
     static constexpr int kSmem = (kStages + 1) * 2 * kTileBytes;
 };
 
+// Output row: out = sum_s 2^(m_s - M) acc_s / sum_s 2^(m_s - M) l_s.  A split
+// whose row saw nothing has m = -inf; its l is 0, or NaN where the row saw a
+// value that is no number there.
+constexpr int kB = 12;   // splits whose loads a warp has in flight together
+
+__device__ __forceinline__ float row_max(const float *ws_ml, int row, int rows_all, int n_split)
+{
+    float M = -INFINITY;
+    for (int s = threadIdx.x & 31; s < n_split; s += 32)
+        M = fmaxf(M, __ldcg(ws_ml + ((size_t)s * rows_all + row) * 2));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    return M;
+}
+
+// Adds splits s0, s0 + step, ... of a row to a warp's acc (D / 32 elements a
+// lane) and L.
+template <int D>
+__device__ __forceinline__ void add_splits(const float *ws_o, const float *ws_ml, int row, int rows_all,
+                                           int s0, int step, int n_split, float M, float (&acc)[D / 32],
+                                           float &L)
+{
+    constexpr int PER = D / 32;
+    const int lane = threadIdx.x & 31;
+    for (; s0 < n_split; s0 += kB * step) {
+        float2 ml[kB];
+        float x[kB][PER];
+#pragma unroll
+        for (int u = 0; u < kB; ++u) {
+            ml[u] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+            for (int e = 0; e < PER; ++e)
+                x[u][e] = 0.f;
+            if (s0 + u * step < n_split) {
+                const size_t at = (size_t)(s0 + u * step) * rows_all + row;
+                ml[u] = __ldcg(reinterpret_cast<const float2 *>(ws_ml + at * 2));
+                const float *src = ws_o + at * D + lane * PER;
+                if constexpr (PER == 4) {
+                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(src));
+                    x[u][0] = v.x; x[u][1] = v.y; x[u][2] = v.z; x[u][3] = v.w;
+                } else {
+                    const float2 v = __ldcg(reinterpret_cast<const float2 *>(src));
+                    x[u][0] = v.x; x[u][1] = v.y;
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kB; ++u) {
+            const float w = ml[u].x == -INFINITY ? 0.f : exp2f(ml[u].x - M);
+            L += w * ml[u].y;
+#pragma unroll
+            for (int e = 0; e < PER; ++e)
+                acc[e] += w * x[u][e];
+        }
+    }
+}
+
+template <int D>
+__device__ __forceinline__ void write_row(__nv_bfloat16 *out, int row, const float (&acc)[D / 32], float L)
+{
+    const float inv = 1.f / L;
+    __nv_bfloat162 *dst = reinterpret_cast<__nv_bfloat162 *>(out + (size_t)row * D +
+                                                             (threadIdx.x & 31) * (D / 32));
+#pragma unroll
+    for (int e = 0; e < D / 64; ++e)
+        dst[e] = __floats2bfloat162_rn(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+}
+
 template <int D>
 __global__ void __launch_bounds__(kMaxWarps * 32, 1)
-attn_q8_kernel(AttnQ8Args a, TreeMasks masks, int tiles_per_split, int n_split)
+attn_q8_kernel(AttnQ8Args a, TreeMasks masks, int tiles_per_split, int n_split, int meet)
 {
     extern __shared__ __align__(128) unsigned char smem[];
     // tail tile: rows with a value that is no number, and those of K among them
     __shared__ unsigned long long odd_rows, odd_keys;
+    __shared__ uint32_t gave_up;
     constexpr int TB = Shape<D>::kTileBytes;
     const Q8Cache &kc = a.c;
 
-    if (threadIdx.x == 0)
-        sm100::launch_dependents();   // the combine may take its place and wait
+    if (threadIdx.x == 0) {
+        gave_up = 0u;
+        sm100::launch_dependents();
+    }
+    sm100::grid_dependency_wait();   // what the previous kernel wrote
     const int split = blockIdx.x, g = blockIdx.y;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int nthreads = blockDim.x;
@@ -392,71 +464,76 @@ attn_q8_kernel(AttnQ8Args a, TreeMasks masks, int tiles_per_split, int n_split)
                     make_float2(m_run[hi], l_run[hi]);
         }
     }
+    if (!meet)
+        return;
+
+    // ---- few splits and rows (a cooperative launch): once every split of
+    // these rows has arrived, each folds every n_split-th row
+    WorkspaceHeader *hdr = reinterpret_cast<WorkspaceHeader *>(a.workspace);
+    int32_t *ctr = reinterpret_cast<int32_t *>(reinterpret_cast<char *>(a.workspace) + kHeaderBytes) +
+                   4 * (g * gridDim.z + blockIdx.z);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        __threadfence();   // the partials before the arrival
+        atomicAdd(&ctr[1], 1);
+        wait_count_bounded(&ctr[1], n_split, &gave_up, hdr);
+    }
+    __syncthreads();
+    const int row0 = blockIdx.z * nthreads / 2, row1 = min(R, row0 + nthreads / 2);
+    if (!*(volatile uint32_t *)&gave_up) {
+        for (int r = row0 + split + warp * n_split; r < row1; r += (nthreads / 32) * n_split) {
+            const int row = (r / G) * a.n_heads_q + g * G + r % G;
+            float acc[D / 32] = {}, L = 0.f;
+            add_splits<D>(ws_o, ws_ml, row, rows_all, 0, 1, n_split,
+                          row_max(ws_ml, row, rows_all, n_split), acc, L);
+            write_row<D>(a.out, row, acc, L);
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x == 0 && atomicAdd(&ctr[2], 1) == n_split - 1) {
+        atomicExch(&ctr[1], 0);
+        atomicExch(&ctr[2], 0);
+    }
 }
 
-// One warp per output row: out = sum_s 2^(m_s - M) acc_s / sum_s 2^(m_s - M) l_s.
-// A split whose row saw nothing has m = -inf; its l is 0, or NaN where the
-// row saw a value that is no number there.
+// The combine as a launch of its own (dependent: it starts while the splits
+// run), `per_row` warps to a row.
 template <int D>
 __global__ void __launch_bounds__(256)
 attn_q8_combine_kernel(const float *__restrict__ ws_o, const float *__restrict__ ws_ml,
-                       __nv_bfloat16 *out, int rows_all, int n_split)
+                       __nv_bfloat16 *out, int rows_all, int n_split, int per_row)
 {
-    const int row = blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
+    constexpr int PER = D / 32;
+    __shared__ float part[8][32][PER + 1];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w = warp % per_row;
+    const int row = blockIdx.x * (8 / per_row) + warp / per_row;
     sm100::launch_dependents();
-    sm100::grid_dependency_wait();   // the split kernel's partials
-    if (row >= rows_all)
-        return;
-    float M = -INFINITY;
-    for (int s = lane; s < n_split; s += 32)
-        M = fmaxf(M, __ldcg(ws_ml + ((size_t)s * rows_all + row) * 2));
+    sm100::grid_dependency_wait();   // the splits' partials
+    float acc[PER] = {}, L = 0.f;
+    if (row < rows_all)
+        add_splits<D>(ws_o, ws_ml, row, rows_all, w, per_row, n_split,
+                      row_max(ws_ml, row, rows_all, n_split), acc, L);
+    if (per_row > 1) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    constexpr int PER = D / 32, kB = 12;   // splits whose loads are in flight together
-    float acc[PER] = {};
-    float L = 0.f;
-    for (int s0 = 0; s0 < n_split; s0 += kB) {
-        float2 ml[kB];
-        float x[kB][PER];
+        for (int e = 0; e < PER; ++e)
+            part[warp][lane][e] = acc[e];
+        part[warp][lane][PER] = L;
+        __syncthreads();
+        if (w == 0)
+            for (int v = 1; v < per_row; ++v) {
 #pragma unroll
-        for (int u = 0; u < kB; ++u) {
-            ml[u] = make_float2(-INFINITY, 0.f);
-#pragma unroll
-            for (int e = 0; e < PER; ++e)
-                x[u][e] = 0.f;
-            if (s0 + u < n_split) {
-                const size_t at = (size_t)(s0 + u) * rows_all + row;
-                ml[u] = __ldcg(reinterpret_cast<const float2 *>(ws_ml + at * 2));
-                const float *src = ws_o + at * D + lane * PER;
-                if constexpr (PER == 4) {
-                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(src));
-                    x[u][0] = v.x; x[u][1] = v.y; x[u][2] = v.z; x[u][3] = v.w;
-                } else {
-                    const float2 v = __ldcg(reinterpret_cast<const float2 *>(src));
-                    x[u][0] = v.x; x[u][1] = v.y;
-                }
+                for (int e = 0; e < PER; ++e)
+                    acc[e] += part[warp + v][lane][e];
+                L += part[warp + v][lane][PER];
             }
-        }
-#pragma unroll
-        for (int u = 0; u < kB; ++u) {
-            const float w = ml[u].x == -INFINITY ? 0.f : exp2f(ml[u].x - M);
-            L += w * ml[u].y;
-#pragma unroll
-            for (int e = 0; e < PER; ++e)
-                acc[e] += w * x[u][e];
-        }
     }
-    const float inv = 1.f / L;
-    __nv_bfloat162 *dst = reinterpret_cast<__nv_bfloat162 *>(out + (size_t)row * D + lane * PER);
-#pragma unroll
-    for (int e = 0; e < PER / 2; ++e)
-        dst[e] = __floats2bfloat162_rn(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    if (row < rows_all && w == 0)
+        write_row<D>(out, row, acc, L);
 }
 
 struct SplitPlan {
     int warps, row_blocks, n_split, tiles_per_split;
+    bool meet;   // the splits combine their rows themselves
 };
 
 SplitPlan make_plan(int n_heads_q, int n_heads_kv, int n_q8, int n_tail, int n_tree, int num_sms)
@@ -473,6 +550,13 @@ SplitPlan make_plan(int n_heads_q, int n_heads_kv, int n_q8, int n_tail, int n_t
         want = 1;
     p.tiles_per_split = (n_tiles + want - 1) / want;
     p.n_split = (n_tiles + p.tiles_per_split - 1) / p.tiles_per_split;
+    // One launch, without a combine of its own, where a warp has no more than
+    // one row to fold, of no more splits than it loads at once: 8 heads of 64
+    // over 2, T = 1, 212 positions 7.7 us a call against 9.6 (the host's time
+    // of two launches); T = 13 there, four rows a warp, 13.4 against 10.9.
+    const int warps = p.warps < 4 ? 4 : p.warps;
+    p.meet = p.n_split > 1 && p.n_split <= kB && R <= p.n_split * warps * p.row_blocks &&
+             n_heads_kv * p.row_blocks <= kQ8MaxSets;
     return p;
 }
 
@@ -485,22 +569,37 @@ cudaError_t launch_d(const AttnQ8Args &a, const TreeMasks &masks, const SplitPla
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess)
         return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.n_split, a.n_heads_kv, p.row_blocks);
     // at least 4 warps: they also turn the codes into bf16
-    const int warps = p.warps < 4 ? 4 : p.warps;
-    attn_q8_kernel<D><<<dim3(p.n_split, a.n_heads_kv, p.row_blocks), warps * 32, smem, stream>>>(
-        a, masks, p.tiles_per_split, p.n_split);
-    e = cudaGetLastError();
+    cfg.blockDim = dim3((p.warps < 4 ? 4 : p.warps) * 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    // cooperative where the splits wait for one another (at most one CTA per SM)
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeCooperative;
+    at[1].val.cooperative = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = p.meet ? 2 : 1;
+    e = cudaLaunchKernelEx(&cfg, attn_q8_kernel<D>, a, masks, p.tiles_per_split, p.n_split, (int)p.meet);
+    if (e == cudaSuccess)
+        e = cudaGetLastError();
     if (e != cudaSuccess)
         return e;
     count_launches(1);
-    if (p.n_split == 1)
+    if (p.meet || p.n_split == 1)
         return e;
     const int rows_all = a.n_tree * a.n_heads_q;
     const float *ws_o = reinterpret_cast<const float *>(
         reinterpret_cast<const char *>(a.workspace) + kHeaderBytes + kQ8SyncBytes);
     const float *ws_ml = ws_o + (size_t)p.n_split * rows_all * D;
-    return launch_pdl(attn_q8_combine_kernel<D>, dim3((rows_all + 7) / 8), dim3(256), 0, stream, ws_o,
-                      ws_ml, a.out, rows_all, p.n_split);
+    // warps to a row: a round of loads each
+    const int per_row = p.n_split <= kB ? 1 : p.n_split <= 2 * kB ? 2 : p.n_split <= 4 * kB ? 4 : 8;
+    const int rows_cta = 8 / per_row;
+    return launch_pdl(attn_q8_combine_kernel<D>, dim3((rows_all + rows_cta - 1) / rows_cta), dim3(256), 0,
+                      stream, ws_o, ws_ml, a.out, rows_all, p.n_split, per_row);
 }
 
 }  // namespace

@@ -6,6 +6,7 @@
 
 #include <cuda_fp8.h>
 
+#include "sm100.cuh"
 #include "ts_internal.cuh"
 
 namespace ts {
@@ -67,10 +68,30 @@ size_t attn_q8_t128_workspace_bytes(int n_heads_q, int n_heads_kv, int n_q8, int
 cudaError_t attn_q8_t128_launch(const AttnQ8Args &a, const TreeMasks &masks, int num_sms,
                                 cudaStream_t stream);
 
-// Both attention kernels' workspaces: header, this region (the tcgen05
-// kernel's counters, zero between calls, so that one workspace serves calls
-// of any shape), then scratch.
+// Both attention kernels' workspaces: header, this region (four counters per
+// set of splits that meet, zero between calls, so that one workspace serves
+// calls of any shape), then scratch.
 constexpr size_t kQ8SyncBytes = 4096;
+constexpr int kQ8MaxSets = (int)kQ8SyncBytes / 16;
+
+// Bounded wait until the int32 at p (written by other CTAs) reaches target.
+__device__ __forceinline__ bool wait_count_bounded(const int32_t *p, int target,
+                                                   volatile uint32_t *abort, WorkspaceHeader *ws)
+{
+    const long long t0 = clock64();
+    for (;;) {
+        int32_t v;
+        asm volatile("ld.acquire.gpu.global.b32 %0, [%1];\n" : "=r"(v) : "l"(p) : "memory");
+        if (v >= target)
+            return true;
+        if (clock64() - t0 > sm100::kWaitCycles) {
+            *abort = 1u;
+            record_status(ws, TS_ERR_TIMEOUT);
+            return false;
+        }
+        __nanosleep(64);
+    }
+}
 
 // the factor a scale byte stands for (bytes below the least scale read as
 // it), its exponent, and its inverse; 255 is NaN

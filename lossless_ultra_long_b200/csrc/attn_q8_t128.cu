@@ -94,8 +94,7 @@ constexpr int kBarRows = 5;                  // named barrier: row_scale is writ
 constexpr int kBarQLoads = 3;                // named barrier: the query rows are read
 constexpr int kBarScales = 4;                // named barrier: the scale bytes are in shared memory
 constexpr int kQLoadThreads = 32 * 9;        // warps 4-11 arrive, K's producer waits
-constexpr int kMaxGz = 256;                  // (KV head, node group) pairs: counters in the workspace
-static_assert(kMaxGz * 16 <= (int)kQ8SyncBytes, "counters fit their region");
+constexpr int kMaxGz = kQ8MaxSets;           // (KV head, node group) pairs: counters in the workspace
 
 constexpr int kTailMark = 1 << 20, kEndMark = -(1 << 30);
 
@@ -660,25 +659,6 @@ __device__ __forceinline__ void combine_row(const AttnQ8Args &a, const TreeMasks
     const float inv = 1.f / L;
     *reinterpret_cast<__nv_bfloat162 *>(a.out + (size_t)row * kD + 64 * half + 2 * lane) =
         __floats2bfloat162_rn(acc[0] * inv, acc[1] * inv);
-}
-
-// Bounded wait until the int32 at p (written by other CTAs) reaches target.
-__device__ __forceinline__ bool wait_count_bounded(const int32_t *p, int target,
-                                                   volatile uint32_t *abort, WorkspaceHeader *ws)
-{
-    const long long t0 = clock64();
-    for (;;) {
-        int32_t v;
-        asm volatile("ld.acquire.gpu.global.b32 %0, [%1];\n" : "=r"(v) : "l"(p) : "memory");
-        if (v >= target)
-            return true;
-        if (clock64() - t0 > kWaitCycles) {
-            *abort = 1u;
-            record_status(ws, TS_ERR_TIMEOUT);
-            return false;
-        }
-        __nanosleep(64);
-    }
 }
 
 // The keys of tail tile t into its two K slots, by the converters' 128 threads,
