@@ -459,7 +459,11 @@ TS_API int ts_kv_quantize_q8(const void *k, const void *v, int64_t src_cap, int 
  *               tail_row0 + n_tail + n_tree <= tail_cap.
  *  out          device bf16 [n_tree, Hq, D], written entirely.
  *  root_scores_out  device fp32 [Hq, n_q8 + n_tail], or NULL.
- *  workspace    device, >= ts_tree_verify_attn_q8_workspace_size(...) bytes.
+ *  workspace    device, >= ts_tree_verify_attn_q8_workspace_size(...) bytes;
+ *               its counters lie where other entry points keep scratch, so
+ *               it serves this one alone.
+ * The result is formed in 32 bits before its rounding: weights times values
+ * of V past 2^60 may overflow.
  * Other arguments as for ts_tree_verify_attn.  A position that a row does
  * not see does not affect it, whatever its K and V hold; a row that sees a
  * key or value row with an infinity or a NaN comes out as NaN.

@@ -560,6 +560,16 @@ SplitPlan make_plan(int n_heads_q, int n_heads_kv, int n_q8, int n_tail, int n_t
     return p;
 }
 
+// Whether the tcgen05 kernel is the faster one.  This one's time grows with the
+// tiles a split takes in turn, from a short start; the other's start (TMEM,
+// barriers, the tail's keys, the meeting of the splits) costs 13 us or more
+// whatever the length.  Heads of 128, this kernel against the other: up to two
+// tiles in turn, 32 heads over 8 at 2048 positions T = 1 14.0 and 15.9 us,
+// T = 40 20.8 and 22.7; 8 over 1 at 16K T = 1 17.4 and 20.6; three, 32 over 8
+// at 2.5K T = 40 24.8 and 24.7, 32 over 32 at 768 T = 1 17.0 and 16.3, 8 over 1
+// at 12K T = 40 26.7 and 24.4.
+bool long_enough(const SplitPlan &p) { return p.tiles_per_split > 2; }
+
 template <int D>
 cudaError_t launch_d(const AttnQ8Args &a, const TreeMasks &masks, const SplitPlan &p,
                      cudaStream_t stream)
@@ -611,7 +621,8 @@ size_t attn_q8_workspace_bytes(int n_heads_q, int n_heads_kv, int head_dim, int 
     size_t bytes = kHeaderBytes + kQ8SyncBytes +
                    align_up((size_t)p.n_split * n_tree * n_heads_q * (head_dim + 2) * sizeof(float), 256);
     // large enough for whichever kernel the launch picks
-    if (attn_q8_t128_eligible(n_heads_q, n_heads_kv, head_dim, n_q8, n_tail, n_tree, num_sms)) {
+    if (long_enough(p) &&
+        attn_q8_t128_eligible(n_heads_q, n_heads_kv, head_dim, n_q8, n_tail, n_tree, num_sms)) {
         const size_t t = attn_q8_t128_workspace_bytes(n_heads_q, n_heads_kv, n_q8, n_tail, n_tree, num_sms);
         bytes = t > bytes ? t : bytes;
     }
@@ -621,13 +632,13 @@ size_t attn_q8_workspace_bytes(int n_heads_q, int n_heads_kv, int head_dim, int 
 cudaError_t attn_q8_launch(const AttnQ8Args &a, const TreeMasks &masks, int num_sms,
                            cudaStream_t stream)
 {
+    const SplitPlan p = make_plan(a.n_heads_q, a.n_heads_kv, a.c.n_q8, a.c.n_tail, a.n_tree, num_sms);
     // the tcgen05 kernel needs scores that grow with the products, and leaves
     // root scores for groups of up to 8 heads
-    if (a.scale_log2 > 0.f && (!a.root_scores || a.n_heads_q / a.n_heads_kv <= 8) &&
+    if (long_enough(p) && a.scale_log2 > 0.f && (!a.root_scores || a.n_heads_q / a.n_heads_kv <= 8) &&
         attn_q8_t128_eligible(a.n_heads_q, a.n_heads_kv, a.head_dim, a.c.n_q8, a.c.n_tail, a.n_tree,
                               num_sms))
         return attn_q8_t128_launch(a, masks, num_sms, stream);
-    const SplitPlan p = make_plan(a.n_heads_q, a.n_heads_kv, a.c.n_q8, a.c.n_tail, a.n_tree, num_sms);
     return a.head_dim == 128 ? launch_d<128>(a, masks, p, stream)
                              : launch_d<64>(a, masks, p, stream);
 }

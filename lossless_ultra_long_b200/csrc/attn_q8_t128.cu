@@ -77,14 +77,6 @@ constexpr int kTmemCols = 512;
 constexpr int kQ1Bytes = 2 * kBlockM * kD;   // Q of block 1 in shared memory: hi, lo
 constexpr float kMaxRowSum = 9.223372036854775808e18f;   // 2^63
 constexpr int kTailWarps = 4;                // warps 16-19, which also turn the tail tiles
-// Fewer positions than this are the general kernel's.  Its time grows with the
-// tiles a split takes in turn, from a short start; this one's start (TMEM,
-// barriers, the tail's keys, the meeting of the splits) costs 13 us or more,
-// whatever the length.  32 heads over 8, here against the general kernel: T = 1
-// at 485 positions 14.2 against 11.8 us, at 764 15.1 and 14.1, at 997 14.6 and
-// 15.5; T = 40 at 740 24.1 and 18.3, at 1037 22.7 and 21.9, at 2061 22.7 and
-// 27.3; 32 KV heads, T = 13, at 777 18.0 and 20.9.
-constexpr int kShort = 768;
 constexpr size_t kSmemLimit = 232448;        // dynamic shared memory per CTA
 constexpr int kBarQuery = 1;                 // named barrier: query rows in place
 constexpr int kBarOut = 2;                   // named barrier: O^T staged, or merged, in shared memory
@@ -1709,7 +1701,10 @@ T128Plan q8_plan(int n_heads_q, int n_heads_kv, int n_q8, int n_tail, int n_tree
 {
     T128Plan p;
     const int G = n_heads_q / n_heads_kv, rows = G * n_tree;
-    p.node_groups = rows <= kMaxRows ? 1 : (rows + kBlockM - 1) / kBlockM;
+    // (warp 0 reads the root node's G rows out of the last block: where they
+    // would lie in both, two groups)
+    const bool one = rows <= kMaxRows && !(G <= 8 && rows > kBlockM && rows < kBlockM + G);
+    p.node_groups = one ? 1 : (rows + kBlockM - 1) / kBlockM;
     p.nodes_per_group = (n_tree + p.node_groups - 1) / p.node_groups;
     // whole nodes per CTA: a group's rows must fit one block
     if (p.node_groups > 1 && p.nodes_per_group * G > kBlockM)
@@ -1752,8 +1747,6 @@ bool attn_q8_t128_eligible(int n_heads_q, int n_heads_kv, int head_dim, int n_q8
     // a CTA takes whole tree nodes: one node's G rows must fit one block;
     // one CTA per SM, all resident
     if (head_dim != kD || n_heads_q / n_heads_kv > kBlockM)
-        return false;
-    if (n_q8 + (long long)n_tail + n_tree < kShort)
         return false;
     const T128Plan p = q8_plan(n_heads_q, n_heads_kv, n_q8, n_tail, n_tree, num_sms);
     const long long gz = (long long)n_heads_kv * p.node_groups;

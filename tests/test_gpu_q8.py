@@ -73,15 +73,17 @@ def test_attention(shape):
 def test_attention_rows_outside_the_cache_are_not_read():
     check_attention(3, 8, 2, 64, 320, 17, 9, "random", cap=512, tail_cap=200, tail_row0=70)
     check_attention(4, 16, 4, 128, 2240, 17, 9, "random", cap=2560, tail_cap=200, tail_row0=70)
+    check_attention(4, 148, 74, 128, 704, 17, 9, "random", cap=768, tail_cap=200, tail_row0=70)
 
 
 @pytest.mark.parametrize("scale", [0.0, -0.05, 0.3])
 def test_attention_scales(scale):
     check_attention(5, 8, 2, 64, 128, 9, 5, "bfs", scale=scale)
     check_attention(6, 8, 2, 128, 2176, 9, 5, "bfs", scale=scale)
+    check_attention(6, 74, 74, 128, 640, 9, 5, "bfs", scale=scale)
 
 
-@pytest.mark.parametrize("hq,hkv,d,n_q8", [(8, 2, 64, 128), (16, 4, 128, 2176)])
+@pytest.mark.parametrize("hq,hkv,d,n_q8", [(8, 2, 64, 128), (16, 4, 128, 2176), (148, 74, 128, 640)])
 def test_unseen_rows_may_hold_anything(hq, hkv, d, n_q8):
     """NaN and infinities in a branch reach its own nodes alone."""
     t, n_tail = 13, 30
@@ -105,7 +107,7 @@ def test_unseen_rows_may_hold_anything(hq, hkv, d, n_q8):
     assert bool(torch.isfinite(clean).all())
 
 
-@pytest.mark.parametrize("hq,hkv,d,n_q8", [(8, 2, 64, 128), (16, 4, 128, 2176)])
+@pytest.mark.parametrize("hq,hkv,d,n_q8", [(8, 2, 64, 128), (16, 4, 128, 2176), (148, 74, 128, 640)])
 @pytest.mark.parametrize("which", ["k_scale", "v_scale"])
 def test_a_block_that_is_not_a_number_reaches_its_head(hq, hkv, d, n_q8, which):
     c, _ = make(8, hkv, d, n_q8, 9, 4)
@@ -116,7 +118,7 @@ def test_a_block_that_is_not_a_number_reaches_its_head(hq, hkv, d, n_q8, which):
     assert bool(nan[:, 1].all()) and not bool(nan[:, [0] + list(range(2, hkv))].any())
 
 
-@pytest.mark.parametrize("hq,hkv,d,n_q8", [(8, 2, 64, 192), (16, 4, 128, 2176)])
+@pytest.mark.parametrize("hq,hkv,d,n_q8", [(8, 2, 64, 192), (16, 4, 128, 2176), (148, 74, 128, 640)])
 def test_extreme_scales(hq, hkv, d, n_q8):
     """Values far apart: tiny values of V in one block, large ones in another; small keys."""
     c, _ = make(9, hkv, d, n_q8, 9, 4)
@@ -132,7 +134,8 @@ def test_extreme_scales(hq, hkv, d, n_q8):
 
 
 @pytest.mark.parametrize("hq,hkv,d,n_q8,n_tail", [(8, 2, 64, 2048, 9), (16, 4, 128, 4096, 9),
-                                                  (32, 8, 128, 2176, 150)])
+                                                  (32, 8, 128, 2176, 150), (74, 74, 128, 1024, 9),
+                                                  (37, 37, 128, 2048, 150)])
 @pytest.mark.parametrize("rise", [30.0, 200.0])
 def test_scores_that_rise_along_the_context(hq, hkv, d, n_q8, n_tail, rise):
     """Keys whose score grows by `rise` nats towards either end: the first
@@ -159,10 +162,13 @@ def test_scores_that_rise_along_the_context(hq, hkv, d, n_q8, n_tail, rise):
         assert bool((err <= bound).all()), (flip, float((err / bound).max()))
 
 
-def test_attention_reuses_a_workspace_and_a_graph():
+@pytest.mark.parametrize("shapes", [
+    [(16, 4, 128, 2176, 9, 13), (8, 2, 64, 320, 20, 5), (16, 4, 128, 4096, 63, 40)],
+    [(74, 74, 128, 640, 9, 13), (8, 2, 64, 320, 20, 5), (120, 40, 128, 1024, 63, 60)],
+], ids=["short", "long"])
+def test_attention_reuses_a_workspace_and_a_graph(shapes):
     """One workspace over calls of other shapes; a captured call replayed with
     new contents of the same buffers, while a second graph has its own."""
-    shapes = [(16, 4, 128, 2176, 9, 13), (8, 2, 64, 320, 20, 5), (16, 4, 128, 4096, 63, 40)]
     ws = L.new_workspace(max(L.tree_verify_attn_q8_workspace_size(*s) for s in shapes))
     for i, (hq, hkv, d, n_q8, n_tail, t) in enumerate(shapes + shapes):
         c, cache = make(20 + i, hkv, d, n_q8, n_tail, t)
@@ -182,13 +188,14 @@ def test_attention_reuses_a_workspace_and_a_graph():
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
             L.tree_verify_attn_q8(q, cache, P8.parents("bfs", t), out=out, workspace=own)
-        graphs.append((g, q, cache, out, t, d, n_q8, n_tail))
+        # (the graph's replays use the workspace, too: it must live as long)
+        graphs.append((g, q, cache, out, own, t))
     for rep in range(3):
-        for j, (g, q, cache, out, t, d, n_q8, n_tail) in enumerate(graphs):
-            q.copy_(queries(40 + rep, t, q.shape[1], d))
+        for j, (g, q, cache, out, own, t) in enumerate(graphs):
+            q.copy_(queries(40 + rep, t, q.shape[1], q.shape[2]))
             g.replay()
         torch.cuda.synchronize()
-        for j, (g, q, cache, out, t, d, n_q8, n_tail) in enumerate(graphs):
+        for j, (g, q, cache, out, own, t) in enumerate(graphs):
             eager = L.tree_verify_attn_q8(q, cache, P8.parents("bfs", t))
             # both within one bound of the truth; they differ by summation order
             assert float((out.float() - eager.float()).abs().max()) <= 2.0 ** -6 * float(
@@ -351,7 +358,7 @@ def test_rope_far_positions_past_32_bits_of_elements():
 
 
 # ------------------------------------------------------------- a run of them together
-@pytest.mark.parametrize("hq,hkv,d,prompt", [(8, 2, 64, 500), (16, 4, 128, 2300)])
+@pytest.mark.parametrize("hq,hkv,d,prompt", [(8, 2, 64, 500), (16, 4, 128, 2300), (80, 40, 128, 900)])
 def test_steps(hq, hkv, d, prompt):
     """A prompt, then steps of a drafted tree: append, verify, select, gather,
     accept, commit, fold; every step's attention against the cache that the
@@ -471,6 +478,29 @@ BORDERS = [
 ]
 
 
+# the tcgen05 kernel: more than two tiles of 64 positions in turn per split,
+# which many KV heads make of a short context
+BORDERS += [
+    (74, 74, 128, 192, 60, 4, "bfs"),       # 256 positions are four tiles of 64, two in turn:
+    (74, 74, 128, 192, 61, 4, "bfs"),       # the general kernel's; one more
+    (74, 74, 128, 320, 0, 1, "chain"),
+    (148, 148, 128, 192, 0, 1, "chain"),    # a head is one CTA's
+    (74, 74, 128, 0, 400, 5, "random"),     # bf16 rows alone: up to 64 query rows a head,
+    (111, 37, 128, 0, 600, 40, "random"),   # up to 128,
+    (148, 37, 128, 0, 800, 40, "bfs"),      # up to 192
+    (111, 37, 128, 576, 130, 40, "random"),
+    (592, 37, 128, 640, 63, 4, "star"),     # 64 rows a head
+    (481, 37, 128, 640, 63, 5, "star"),     # 65
+    (74, 37, 128, 640, 63, 64, "random"),   # 128
+    (222, 74, 128, 448, 63, 43, "random"),  # 129: too few for a second block with the root's
+    (259, 37, 128, 640, 63, 19, "random"),  # 133, the same
+    (370, 74, 128, 448, 63, 27, "random"),  # 135: enough
+    (185, 37, 128, 640, 63, 40, "random"),  # 200: two groups of nodes
+    (1000, 20, 128, 640, 10, 5, "bfs"),     # whole nodes of 50 rows: groups of 2, 2 and 1
+    (74, 74, 128, 704, 300, 64, "chain"),   # a tail of several tiles
+]
+
+
 @pytest.mark.parametrize("root", [False, True])
 @pytest.mark.parametrize("shape", BORDERS, ids=lambda s: "-".join(map(str, s)))
 def test_attention_borders(shape, root):
@@ -523,7 +553,9 @@ def test_attention_on_two_streams_at_once():
     jobs = []
     for seed, (hq, hkv, d, n_q8, n_tail, t) in ((82, (16, 4, 128, 8192, 9, 13)),
                                                (83, (16, 4, 128, 4096, 63, 40)),
-                                               (84, (8, 2, 64, 2048, 9, 5))):
+                                               (84, (8, 2, 64, 2048, 9, 5)),
+                                               (85, (74, 74, 128, 640, 9, 13)),
+                                               (86, (80, 40, 128, 1024, 9, 40))):
         c, cache = make(seed, hkv, d, n_q8, n_tail, t)
         q, parent = queries(seed, t, hq, d), P8.parents("bfs", t)
         k, v = (P8.cache_rows(c, n, n_q8, 0, n_tail + t) for n in "kv")
