@@ -11,6 +11,10 @@
 // bf16 numbers (4 significant bits), so both products are exact up to their
 // fp32 accumulation and, for PV, the two bf16 parts of P.
 //
+// Bound: short contexts, where a call is a chain of latencies (the launch, one
+// or two tiles, the combine): 8 heads of 64 over 2, 13 nodes, 2048 positions
+// 8.6 us; one node, 212 positions 6.2 to 8 us.
+//
 // Work split: grid (splits, Hkv, row blocks).  A CTA streams a contiguous
 // range of tiles: a tile is one 64-row block of the 8-bit cache or 64 rows
 // of the bf16 tail (context, then the tree).  cp.async brings the bytes into

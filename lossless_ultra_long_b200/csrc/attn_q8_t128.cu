@@ -44,6 +44,14 @@
 // O^T and P^T, and their partials are merged before they leave.
 // TMEM: O^T in [0, 192), Q_0 (hi, lo) in [192, 256), S in [256, 512).
 //
+// What bounds it, at 102400 positions (8 KV heads, 210 MB: 32 us of HBM time):
+// up to 16 query rows a head 51 us, the conversion of V the largest part (8 us
+// without it) and shared memory, of which a tile moves some 150 KB; 52 rows 58
+// us; 160 rows 96 us, the exponentials and the order of the tiles' steps (two
+// query blocks leave room for one bf16 V tile).  32 KV heads of 4 rows (839 MB)
+// 190 us, on the 128 SMs that 32 heads divide into.  Under calls without a pause
+// the clock falls to 1.65 GHz at the power limit (57, 110 and 222 us).
+//
 // Every wait is bounded (about a second): on expiry the kernel records
 // TS_ERR_TIMEOUT in the workspace status word, all roles leave their loops,
 // and TMEM is freed before the CTA exits.
@@ -1496,7 +1504,8 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
             // instruction cache).  With a warp or two per sub-partition a half at
             // once has the longer independent stretches; with more, quarters, each
             // on its way while the one before is turned to weights, hide the loads
-            // (T = 13: 66 us against 71, T = 40: 98 against 104).
+            // (measured with fewer other gains: T = 13 66 us against 71, T = 40 98
+            // against 104).
             auto pass = [&](auto special, const float4 *scl, uint32_t s0, int t, uint32_t atA, uint32_t atB,
                             uint32_t bar_free) {
                 uint32_t r0[NG == 2 ? 32 : 16];
