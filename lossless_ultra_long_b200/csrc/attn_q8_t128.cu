@@ -426,7 +426,7 @@ __device__ __forceinline__ float two_to(int e) { return __uint_as_float((uint32_
 // Four codes -> two bf16 pairs (low codes first).  The seven low bits of a
 // code, shifted to bf16's exponent and mantissa, are its magnitude times
 // 2^-120 (subnormals included); NaN codes read as 480.  With a code in the
-// low byte of each half word, code * 16 + sign * 30720 puts the magnitude at
+// low byte of each half word, code * 16 + sign * 0x7800 puts the magnitude at
 // bit 4 and the sign at bit 15: two multiply-adds a pair, which leave the
 // integer pipe, the busiest one, to the softmax.
 __device__ __forceinline__ uint32_t code_pair(uint32_t two)
