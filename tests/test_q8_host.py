@@ -225,3 +225,17 @@ def test_cache_refuses_host_tensors():
         L.KvCacheQ8(**c, n_q8=64, n_tail=3)
     with pytest.raises(ValueError):
         L.tree_verify_attn_q8(torch.zeros(4, 8, 64, dtype=torch.bfloat16), None, [-1, 0, 1, 2])
+
+
+@pytest.mark.parametrize("form", [list, tuple, lambda p: np.array(p, dtype=np.int32),
+                                  lambda p: np.array(p, dtype=np.int64), torch.tensor])
+def test_a_tree_in_any_form_is_the_same_tree(form):
+    parent = [-1, 0, 0, 1, 1]
+    keep, address = L._parent_arg(form(parent), 5)
+    assert list((ctypes.c_int32 * 5).from_address(address)) == parent
+    del keep
+    for n in (4, 6):
+        with pytest.raises(ValueError):
+            L._parent_arg(form(parent), n)
+    with pytest.raises((OverflowError, ValueError)):
+        L._parent_arg([-1, 1 << 40], 2)
