@@ -23,13 +23,17 @@
 // and copy V.  Rows with an infinity or a NaN are zeroed there and noted;
 // a query row that sees one gets a NaN sum.
 //
-// Softmax layout, reference maximum (fixed at a row's first tile), run-time
-// hand-out of tiles from the end of the cache backwards, partials, and the
-// combine by the splits themselves follow the bf16 kernel in attn_t128.cu;
-// a split whose row sum outgrows the reference by 2^63 is recomputed exactly
-// from the owner map.  The result is rounded to bf16, as coarse as the
-// weights' own rounding, so rows that rest on few positions need no second
-// look.
+// Softmax layout, reference maximum (fixed at a row's first tile), partials, and
+// the combine by the splits themselves follow the bf16 kernel in attn_t128.cu;
+// a split whose row sum outgrows the reference by 2^63 is recomputed exactly.
+// The result is rounded to bf16, as coarse as the weights' own rounding, so rows
+// that rest on few positions need no second look.
+//
+// Which split takes a tile depends on its index alone (HandOut), from the end
+// of the cache backwards: a row's reference and the order of its sums are the
+// same in every call, and so is the result, bit for bit.  (Tiles handed out at
+// run time move the result by the order of the sums and the rounding of a weight
+// to bf16, up to 2^-8 of it from call to call.)
 //
 // CTA = (split, KV head, node group), 20 warps, one CTA per SM:
 //   warp 0      root scores out of S        warp 1  QK issuer, TMEM
@@ -84,6 +88,10 @@ constexpr int kSCol = 256;                   // S slots: 128 columns each
 constexpr int kTmemCols = 512;
 constexpr int kQ1Bytes = 2 * kBlockM * kD;   // Q of block 1 in shared memory: hi, lo
 constexpr float kMaxRowSum = 9.223372036854775808e18f;   // 2^63
+// 8-bit tiles that the others stream while a split makes its tail tile ready.
+// 102400 positions of 8 heads, 1, 4, 6 of them: one query row a head 56.0, 53.0,
+// 51.3 us, 40 nodes 103, 97.8, 97.7 us (run-time hand-out: 51.9 and 96.1)
+constexpr int kTailCost = 6;
 constexpr int kTailWarps = 4;                // warps 16-19, which also turn the tail tiles
 constexpr size_t kSmemLimit = 232448;        // dynamic shared memory per CTA
 constexpr int kBarQuery = 1;                 // named barrier: query rows in place
@@ -493,11 +501,57 @@ __device__ __forceinline__ float part_max(const uint32_t (&r)[4 * J])
 
 // The kernel's workspace, after the header and the counters.
 struct Q8Sync {
-    int32_t *sync;    // [Hkv * groups][4]: tile counter, arrivals, finished combines, unused;
+    int32_t *sync;    // [Hkv * groups][4]: unused, arrivals, finished combines, unused;
                       // zero when a call starts, and again when it ends
     float *part;      // acc fp32 [n_split][T*Hq][128], then (m, l) fp32 [n_split][T*Hq][2]
     int32_t *flags;   // [n_split][Hkv * groups]: some row's sum outgrew its reference
-    uint8_t *owner;   // [Hkv * groups][n_tiles]: the split that streamed each tile
+};
+
+// Which split streams which tile of a head, by counting alone.  The nt tail tiles
+// come first, one per split and round; the `busy` splits of the last such round are
+// kTailCost 8-bit tiles behind the others (the tail's keys are split and its masks
+// evaluated), so the others take so many rounds ahead of them.  The rest
+// goes round all splits, what is left of the last round to the last ones.  Tiles
+// are taken from the end of the cache backwards.  Every split has a tile as long as
+// there are no more splits than tiles.
+struct HandOut {
+    int n_split, nq, n_tiles, tail_rounds, busy, ahead, full, left;
+    __device__ __forceinline__ HandOut(int n_split_, int nq_, int n_tiles_) : n_split(n_split_), nq(nq_), n_tiles(n_tiles_)
+    {
+        const int nt = n_tiles - nq;
+        tail_rounds = (nt + n_split - 1) / n_split;
+        busy = nt - (tail_rounds - 1) * n_split;
+        ahead = min(nq, kTailCost * (n_split - busy));
+        full = (nq - ahead) / n_split;
+        left = nq - ahead - full * n_split;
+    }
+    // the r-th tile of a split, negative from its end on
+    __device__ __forceinline__ int tile(int split, int r) const
+    {
+        const bool late = split < busy;
+        int i = r - tail_rounds + (late ? 0 : 1);
+        if (i < 0)
+            return n_tiles - 1 - (r * n_split + split);
+        if (!late) {
+            const int k = i * (n_split - busy) + split - busy;
+            if (i < kTailCost)
+                return k < ahead ? nq - 1 - k : -1;
+            i -= kTailCost;
+        }
+        const int s = i < full ? split : split - (n_split - left);
+        return i > full || s < 0 ? -1 : nq - 1 - (ahead + i * n_split + s);
+    }
+    // the split that has tile t
+    __device__ __forceinline__ int split_of(int t) const
+    {
+        if (t >= nq)
+            return (n_tiles - 1 - t) % n_split;
+        int k = nq - 1 - t;
+        if (k < ahead)
+            return busy + k % (n_split - busy);
+        k -= ahead;
+        return k < full * n_split ? k % n_split : k - full * n_split + n_split - left;
+    }
 };
 
 // Adds one tile to half a row's running exact partial (m, l, acc): fp32
@@ -621,14 +675,14 @@ __device__ __forceinline__ void combine_row(const AttnQ8Args &a, const TreeMasks
         for (int o = 16; o > 0; o >>= 1)
             L += __shfl_xor_sync(0xffffffffu, L, o);
     } else {
-        const uint8_t *own = sy.owner + (size_t)gz * n_tiles_all;
+        const HandOut hand(n_split, nq, n_tiles_all);
         float Mr = -INFINITY;
         for (int s = 0; s < n_split; ++s) {
             float ms = -INFINITY, ls = 0.f, as[2] = {0.f, 0.f};
             if (__ldcg(sy.flags + (size_t)s * n_gz + gz) != 0) {
                 for (int t0 = 0; t0 < n_tiles_all; t0 += 32) {
                     const int t = t0 + lane;
-                    uint32_t bits = __ballot_sync(0xffffffffu, t < n_tiles_all && __ldcg(own + t) == s);
+                    uint32_t bits = __ballot_sync(0xffffffffu, t < n_tiles_all && hand.split_of(t) == s);
                     while (bits) {
                         const int tt = t0 + __ffs(bits) - 1;
                         bits &= bits - 1;
@@ -944,21 +998,12 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
             if (!k_split)   // (the query rows first, as below)
                 named_bar_sync(kBarQLoads, kQLoadThreads);
             named_bar_sync(kBarScales, 32 * (n_conv + 1));
-            // Tiles are taken from the end of the cache backwards: each split's
-            // first kFirst ones are its own (every n_split-th), then it claims
-            // kRound at a time, one claim ahead of need.  Lanes post a round's
-            // tiles (index, scales), a few ahead of the loads.  A claim takes up to
-            // 4000 cycles under load, a tile 1400 (one query row) to 3400 (160);
-            // larger rounds leave the splits of a head further apart at the end
-            // (rounds of four: 10000 cycles at T = 40).
-            constexpr int kFirst = 4, kRound = NG == 2 ? 4 : 1;
-            auto tile_at = [&](int k) { return n_tiles_all - 1 - k; };
-            int32_t *ctr = sy.sync + 4 * gz;
-            auto claim = [&](int n) { return lane == 0 ? atomicAdd(&ctr[0], n) : 0; };
-            uint8_t *owner = sy.owner + (size_t)gz * n_tiles_all;
-            // tile t of this CTA, from one of the first n lanes
-            auto post = [&](int t, int tile, int n) {
-                if (lane >= n)
+            // Four lanes post a tile each (index, scales), a few tiles ahead of the
+            // loads
+            constexpr int kRound = 4;
+            // tile t of this CTA
+            auto post = [&](int t, int tile) {
+                if (lane >= kRound)
                     return;
                 const int at = t & (kTileRing - 1);
                 const bool tail = tile >= nq;
@@ -978,37 +1023,30 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                                                             : min(max(left - 64 * h, -kTileN), 64) +
                                                                   (tail ? kTailMark : 0)));
                 }
-                if (tile >= 0)
-                    owner[tile] = (uint8_t)split;
-                else   // (the second group's end)
+                if (tile < 0)   // (the second group's end)
                     aux->scale_of[(t + 1) & (kTileRing - 1)][0].w = __int_as_float(kEndMark);
             };
-            int base = claim(kRound);
-            int my_tile = tile_at(split + lane * n_split);
-            post(lane, my_tile, kFirst);
-            __syncwarp();
-            if (lane == 0)
-                for (int i = 0; i < kFirst; ++i)
-                    mbar_arrive(smem_addr(&bar->info[i]));
-            int posted = kFirst;
-            bool more = __shfl_sync(0xffffffffu, my_tile, kFirst - 1) >= 0;
+            const HandOut hand(n_split, nq, n_tiles_all);
+            int posted = 0;
+            bool more = true;
+            auto post_round = [&]() {
+                const int tile = hand.tile(split, posted + (lane & (kRound - 1)));
+                more = __shfl_sync(0xffffffffu, tile, kRound - 1) >= 0;
+                post(posted + lane, tile);
+                __syncwarp();
+                if (lane == 0)
+                    for (int i = 0; i < kRound; ++i)
+                        mbar_arrive(smem_addr(&bar->info[(posted + i) & (kTileRing - 1)]));
+                posted += kRound;
+            };
+            post_round();
             Ring rv(SV);
             int v_tma = -1;
             for (int step = 0;; ++step) {
                 // V one tile behind K where both are this warp's
                 const int t = k_split ? step : step - 1;
-                if (more && posted - t <= 2) {
-                    my_tile = tile_at(kFirst * n_split + __shfl_sync(0xffffffffu, base, 0) + lane);
-                    more = __shfl_sync(0xffffffffu, my_tile, kRound - 1) >= 0;
-                    if (more)
-                        base = claim(kRound);
-                    post(posted + lane, my_tile, kRound);
-                    __syncwarp();
-                    if (lane == 0)
-                        for (int i = 0; i < kRound; ++i)
-                            mbar_arrive(smem_addr(&bar->info[(posted + i) & (kTileRing - 1)]));
-                    posted += kRound;
-                }
+                if (more && posted - t <= 2)
+                    post_round();
                 if (!k_split && !k_end && !k_step(step))
                     break;
                 if (t < 0)
@@ -1681,7 +1719,7 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
     int32_t *ctr = sy.sync + 4 * gz;
     if (threadIdx.x == 0) {
         sy.flags[(size_t)split * n_gz + gz] = bar->overflow;
-        __threadfence();   // partials, flag and owner entries before the arrival
+        __threadfence();   // partials and flag before the arrival
         atomicAdd(&ctr[1], 1);
         wait_count_bounded(&ctr[1], n_split, abort, hdr);
     }
@@ -1695,7 +1733,6 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
     }
     __syncthreads();
     if (threadIdx.x == 0 && atomicAdd(&ctr[2], 1) == n_split - 1) {
-        atomicExch(&ctr[0], 0);
         atomicExch(&ctr[1], 0);
         atomicExch(&ctr[2], 0);
     }
@@ -1703,7 +1740,7 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
 
 struct T128Plan {
     int n_split, node_groups, nodes_per_group;
-    size_t part, flags, owner, total;
+    size_t part, flags, total;
 };
 
 T128Plan q8_plan(int n_heads_q, int n_heads_kv, int n_q8, int n_tail, int n_tree, int num_sms)
@@ -1723,12 +1760,11 @@ T128Plan q8_plan(int n_heads_q, int n_heads_kv, int n_q8, int n_tail, int n_tree
     int want = num_sms / (n_heads_kv * p.node_groups);
     want = want < 1 ? 1 : want;
     want = want > n_tiles ? n_tiles : want;
-    p.n_split = want > 255 ? 255 : want;
+    p.n_split = want;
     const size_t n_gz = (size_t)n_heads_kv * p.node_groups;
     p.part = kHeaderBytes + kQ8SyncBytes;
     p.flags = p.part + align_up((size_t)p.n_split * n_tree * n_heads_q * (kD + 2) * sizeof(float), 256);
-    p.owner = p.flags + align_up((size_t)p.n_split * n_gz * sizeof(int32_t), 256);
-    p.total = p.owner + align_up(n_gz * n_tiles, 256);
+    p.total = p.flags + align_up((size_t)p.n_split * n_gz * sizeof(int32_t), 256);
     return p;
 }
 
@@ -1793,7 +1829,6 @@ cudaError_t attn_q8_t128_launch(const AttnQ8Args &a, const TreeMasks &masks, int
     sy.sync = reinterpret_cast<int32_t *>(ws + kHeaderBytes);
     sy.part = reinterpret_cast<float *>(ws + p.part);
     sy.flags = reinterpret_cast<int32_t *>(ws + p.flags);
-    sy.owner = reinterpret_cast<uint8_t *>(ws + p.owner);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(p.n_split, a.n_heads_kv, p.node_groups);
     cfg.blockDim = dim3(kThreads);
