@@ -745,8 +745,6 @@ __device__ __noinline__ bool tail_keys(const AttnQ8Args &a, Aux *aux, unsigned c
     const uint32_t wk = __ballot_sync(0xffffffffu, bad_k), wb = __ballot_sync(0xffffffffu, bad);
     const uint32_t wtop = __reduce_max_sync(0xffffffffu, bad ? 0u : tk);
     if (lane == 0) {
-        bar->bad_k[t & 3][w] = wk;
-        bar->bad[t & 3][w] = wb;
         bar->top[w] = wtop;
         mbar_arrive(smem_addr(&bar->conv));
     }
@@ -754,6 +752,16 @@ __device__ __noinline__ bool tail_keys(const AttnQ8Args &a, Aux *aux, unsigned c
         return false;
     if (!warp_wait(smem_addr(&bar->tail_slots[t & (kTileRing - 1)]), (t >> 4) & 1, abort, hdr))
         return false;
+    // Tile t - 4's notes are read until now at the latest.  These two K slots are
+    // free: with at most five, QK of tile t - 2 is complete, and it waited until
+    // tile t - 4's S was read, by warp 0 too, which reads bad_k before it says so.
+    // bad of t - 4 has its last reader before PV of that tile, and this warp waited
+    // for PV of a later one.
+    static_assert(kMaxStages <= 5, "a later QK than tile t - 4's successor in its S slot");
+    if (lane == 0) {
+        bar->bad_k[t & 3][w] = wk;
+        bar->bad[t & 3][w] = wb;
+    }
     volatile uint32_t *top = bar->top;
     const int e = split_exp(max(top[w & 2], top[(w & 2) + 1]));
     if (tid == 0) {

@@ -1,5 +1,8 @@
 """The 8-bit cache's attention on the GPU, beyond the plain forms' sizes: the same
-call twice."""
+call twice, long tails with keys that are no numbers."""
+import math
+
+import numpy as np
 import pytest
 import torch
 
@@ -56,3 +59,30 @@ def test_the_same_call_gives_the_same_bits(hq, hkv, d, n_q8, n_tail, t, root):
         assert not root or torch.equal(rs, first[1]), rep
     assert L.workspace_status(ws) == 0
     torch.cuda.synchronize()
+
+
+# --------------------------------------------------- values that are no numbers
+@pytest.mark.parametrize("hq,hkv,n_tail,t", [(74, 74, 2500, 3), (592, 74, 2000, 12), (592, 74, 1900, 16),
+                                             (296, 74, 1500, 40)])
+def test_many_tail_tiles_with_keys_that_are_no_numbers(hq, hkv, n_tail, t):
+    """Each CTA takes more tail tiles than it has places for their notes."""
+    d = 128
+    c = P8.cache_inputs(96, hkv, d, 0, n_tail, t)
+    rng = np.random.default_rng(97)
+    bad = torch.from_numpy(rng.random((hkv, n_tail)) < 0.02)
+    c["k_tail"][:, :n_tail][bad] = math.nan
+    q, parent = P8.bf16(rng, t, hq * d).reshape(t, hq, d), P8.parents("random", t, 2)
+    cache = L.KvCacheQ8(**{k: x.cuda() for k, x in c.items()}, n_q8=0, n_tail=n_tail)
+    g = hq // hkv
+    k = torch.where(bad[..., None], 0.0, c["k_tail"][:, :n_tail].double())
+    mask = bad.repeat_interleave(g, 0)
+    want = torch.einsum("hgd,hnd->hgn", q[0].double().reshape(hkv, g, d), k).reshape(hq, -1) * d ** -0.5 / math.log(2)
+    mag = torch.einsum("hgd,hnd->hgn", q[0].double().abs().reshape(hkv, g, d), k.abs()).reshape(hq, -1)
+    bound = mag * d ** -0.5 / math.log(2) * ((d + 8) * 2.0 ** -23 + 2.0 ** -20) + 1e-30
+    for _ in range(8):
+        rs = torch.zeros(hq, n_tail, device="cuda")
+        out = L.tree_verify_attn_q8(q.cuda(), cache, parent, root_scores_out=rs)
+        got = rs.double().cpu()
+        assert torch.equal(torch.isnan(got), mask)
+        assert bool(((got - want).abs() <= bound)[~mask].all())
+        assert bool(torch.isnan(out).all())
