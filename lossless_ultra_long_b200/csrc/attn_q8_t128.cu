@@ -18,9 +18,10 @@
 // and each block's sum is multiplied back by 1 / s_v.
 //
 // A tail tile (bf16 rows: newest context, tree) goes through the same
-// products: the converter warps scale its keys by block and splits them like
-// the queries into an e4m3 and an e5m2 tile (two K slots, four products),
-// and copy V.  Rows with an infinity or a NaN are zeroed there and noted;
+// products: the converter warps scale its keys, each row by a power of two of its
+// own (no row takes another's bits, whatever its size), split them like the
+// queries into an e4m3 and an e5m2 tile (two K slots, four products), and copy V;
+// the scores take the keys' scales where the masks are evaluated.  Rows with an infinity or a NaN are zeroed there and noted;
 // a query row that sees one gets a NaN sum.
 //
 // Softmax layout, reference maximum (fixed at a row's first tile), partials, and
@@ -111,23 +112,22 @@ struct Bars {
     uint64_t empty_k[kMaxStages];
     uint64_t full_v[kMaxStages];    // codes of V landed (or: a tail tile)
     uint64_t empty_v[kMaxStages];
-    uint64_t s_full[3];             // QK landed: by block, or (one block) by tile in turn
-    uint64_t s_free[3];             // its readers hold S in registers
+    uint64_t s_full[2];             // QK landed: by block, or (one block) by tile in turn
+    uint64_t s_free[2];             // its readers hold S in registers
     uint64_t vb_full[2];            // V in bf16
-    uint64_t sm_done[3];            // per P^T slot: P^T is written
-    uint64_t pv_done[3];            // per P^T slot: PV is complete
+    uint64_t sm_done[2];            // per P^T slot: P^T is written
+    uint64_t pv_done[2];            // per P^T slot: PV is complete
     uint64_t o_final;
     uint64_t drain[2];
     uint64_t conv;                  // the converter warps meet (tail tiles)
     uint64_t info[kTileRing];       // tile_of, scale_of of that tile are written
     uint64_t tail_slots[kTileRing]; // a tail tile's K slots are free, entry_of is written
-    // per tile, at [t & (kTileRing - 1)]: its index (-1 after the last), and a
-    // tail tile's first K ring entry
+    // per tile, at [t & (kTileRing - 1)]: its index (-1 after the last); a tail
+    // tile's first K ring entry, at [t & 3]
     volatile int32_t tile_of[kTileRing];
-    volatile int32_t entry_of[kTileRing];
+    volatile int32_t entry_of[4];
     uint32_t bad[4][4];             // tail tile t % 4: rows with a value that is no number
     uint32_t bad_k[4][4];
-    uint32_t top[4];                // tail tile: largest key magnitude of each 32 rows
     uint32_t tmem_base;
     uint32_t abort;
     int32_t overflow;
@@ -135,17 +135,17 @@ struct Bars {
 
 struct Aux {
     Bars bar;
-    // per tile and half, posted with tile_of (a tail tile's k by a converter):
-    // K's scale, V's as an exponent, V's inverse, and (as an int) how many of
-    // the half's positions are context, kTailMark added on a tail tile, or
-    // kEndMark.  A block that is NaN, in K or V, has a NaN exponent and
+    // per tile and half, posted with tile_of: K's scale (1 on a tail tile), V's
+    // as an exponent, V's inverse, and (as an int) how many of the half's positions
+    // are context, kTailMark added on a tail tile, or kEndMark.  A block that is NaN, in K or V, has a NaN exponent and
     // inverse: its weights and sums are NaN.
     float4 scale_of[kTileRing][2];
     unsigned long long anc[TS_MAX_TREE];
     float2 ml[2][64];               // (m, l) of each group's rows, to be merged
-    float row_scale[2 * kBlockM];   // softmax scale * log2 e * the query row's scale
+    float row_scale[kMaxRows];      // softmax scale * log2 e * the query row's scale
+    uint8_t key_exp[4][kTileN];     // tail tile t % 4: the keys' scales 2^(byte - 127)
 };
-constexpr size_t kAuxBytes = (sizeof(Aux) + 1023) / 1024 * 1024;
+constexpr size_t kAuxBytes = (sizeof(Aux) + 15) / 16 * 16;
 
 struct Layout {
     int r_pad, stages_k, stages_v, stages_vb;
@@ -168,7 +168,7 @@ __host__ __device__ inline Layout q8_layout(int rows, int n_blk)
     L.stages_vb = rows > kBlockM ? 1 : 2;
     L.k_off = L.vb_off + (size_t)L.stages_vb * kVbBytes;
     // the scale bytes of every block of the head, K's then V's
-    const size_t sc_bytes = ((size_t)2 * n_blk + 127) / 128 * 128;
+    const size_t sc_bytes = ((size_t)2 * n_blk + 15) / 16 * 16;
     const size_t fixed = 1024 + L.k_off + sc_bytes + kAuxBytes;
     int stages = fixed > kSmemLimit ? 0 : (int)((kSmemLimit - fixed) / kRawBytes);
     stages = stages > 2 * kMaxStages ? 2 * kMaxStages : stages;
@@ -427,7 +427,7 @@ __device__ __forceinline__ uint32_t top_word(const uint4 &u)
 __device__ __forceinline__ int split_exp(uint32_t top)
 {
     const int e = (int)(top >> 7) - 127 - 8 + ((top & 0x7Fu) > 0x60u ? 1 : 0);
-    return top == 0 ? 0 : max(e, kQ8MinExp);
+    return top == 0 ? 0 : max(e, -126);
 }
 __device__ __forceinline__ float two_to(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
@@ -716,9 +716,9 @@ __device__ __forceinline__ void combine_row(const AttnQ8Args &a, const TreeMasks
 }
 
 // The keys of tail tile t into its two K slots, by the converters' 128 threads,
-// a row each: scaled by block of 64 rows, split into e4m3 and e5m2
-// codes; notes the rows with an infinity or a NaN (and zeroes them).  False
-// when a wait ran out.
+// a row each: scaled to at most 448 by a power of two (noted in key_exp), split
+// into e4m3 and e5m2 codes; notes the rows with an infinity or a NaN (and zeroes
+// them).  False when a wait ran out.
 __device__ __noinline__ bool tail_keys(const AttnQ8Args &a, Aux *aux, unsigned char *sK, int SK, int g,
                                        int nq, int t, int &met, volatile uint32_t *abort,
                                        WorkspaceHeader *hdr)
@@ -743,32 +743,21 @@ __device__ __noinline__ bool tail_keys(const AttnQ8Args &a, Aux *aux, unsigned c
     tv = top_of(tv);
     const bool bad_k = tk >= 0x7F80u, bad = bad_k || tv >= 0x7F80u;
     const uint32_t wk = __ballot_sync(0xffffffffu, bad_k), wb = __ballot_sync(0xffffffffu, bad);
-    const uint32_t wtop = __reduce_max_sync(0xffffffffu, bad ? 0u : tk);
-    if (lane == 0) {
-        bar->top[w] = wtop;
-        mbar_arrive(smem_addr(&bar->conv));
-    }
-    if (!warp_wait(smem_addr(&bar->conv), met++ & 1, abort, hdr))
-        return false;
+    const int e = bad_k ? 0 : split_exp(tk);
     if (!warp_wait(smem_addr(&bar->tail_slots[t & (kTileRing - 1)]), (t >> 4) & 1, abort, hdr))
         return false;
     // Tile t - 4's notes are read until now at the latest.  These two K slots are
     // free: with at most five, QK of tile t - 2 is complete, and it waited until
-    // tile t - 4's S was read, by warp 0 too, which reads bad_k before it says so.
-    // bad of t - 4 has its last reader before PV of that tile, and this warp waited
-    // for PV of a later one.
+    // tile t - 4's S was read, by warp 0 too, which reads them before it says so.
+    // The softmax reads them before PV of that tile, and this warp waited for PV of
+    // a later one.
     static_assert(kMaxStages <= 5, "a later QK than tile t - 4's successor in its S slot");
     if (lane == 0) {
         bar->bad_k[t & 3][w] = wk;
         bar->bad[t & 3][w] = wb;
     }
-    volatile uint32_t *top = bar->top;
-    const int e = split_exp(max(top[w & 2], top[(w & 2) + 1]));
-    if (tid == 0) {
-        aux->scale_of[t & (kTileRing - 1)][0].x = two_to(e);
-        aux->scale_of[t & (kTileRing - 1)][1].x = two_to(split_exp(max(top[2], top[3])));
-    }
-    const int e0 = bar->entry_of[t & (kTileRing - 1)];
+    aux->key_exp[t & 3][tid] = (uint8_t)(e + 127);
+    const int e0 = bar->entry_of[t & 3];
     unsigned char *khi = sK + (e0 % SK) * kRawBytes, *klo = sK + ((e0 + 1) % SK) * kRawBytes;
     const float f = two_to(-e);
 #pragma unroll 2
@@ -917,7 +906,7 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
             mbar_init(smem_addr(&bar->info[i]), 1);
             mbar_init(smem_addr(&bar->tail_slots[i]), 1);
         }
-        for (int i = 0; i < 3; ++i) {
+        for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&bar->s_full[i]), 1);
             mbar_init(smem_addr(&bar->s_free[i]), NB == 1 ? act0 + rs : (i == 0 ? act0 : act1 + rs));
             mbar_init(smem_addr(&bar->sm_done[i]), act0 + act1);
@@ -988,7 +977,7 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                         tma_load_3d_hint(smem_addr(sK + s * kRawBytes), &tmap_k, 0, tile * kTileN, g, fb, pol);
                         k_tma = ke;
                     } else if (part == 1) {
-                        bar->entry_of[at] = ke - 1;
+                        bar->entry_of[t & 3] = ke - 1;
                         mbar_arrive(smem_addr(&bar->tail_slots[at]));
                     }
                 }
@@ -1127,14 +1116,23 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                         break;   // uniform: nothing of the context from here on
                     uint32_t rr[32];
                     tmem_ld16x256_x8(tmem + kSCol + 128 * slot + 64 * h, rr);
-                    if (mine) {
+                    float *dst = dst_row + pos0 + 64 * h + c0;
+                    if (mine && !q8) {
+                        // a tail tile: the keys have a scale each
+                        const unsigned long long nan = bar->bad_k[t & 3][2 * h] |
+                                                       ((unsigned long long)bar->bad_k[t & 3][2 * h + 1] << 32);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            const int p = 8 * (k >> 1) + c0 + (k & 1);
+                            const float f = rsc * two_to(aux->key_exp[t & 3][64 * h + p] - 127);
+                            if (p < lh)
+                                dst[8 * (k >> 1) + (k & 1)] =
+                                    (nan >> p) & 1ull ? __uint_as_float(0x7FC00000u)
+                                                      : __uint_as_float(rr[4 * (k >> 1) + (k & 1)]) * f;
+                        }
+                    } else if (mine) {
                         const float f = rsc * aux->scale_of[t & (kTileRing - 1)][h].x;
-                        float *dst = dst_row + pos0 + 64 * h + c0;
-                        unsigned long long nan = 0ull;
-                        if (!q8)
-                            nan = bar->bad_k[t & 3][2 * h] |
-                                  ((unsigned long long)bar->bad_k[t & 3][2 * h + 1] << 32);
-                        if (vec && lh >= 64 && nan == 0ull) {
+                        if (vec && lh >= 64) {
 #pragma unroll
                             for (int j = 0; j < 8; ++j)
                                 *reinterpret_cast<float2 *>(dst + 8 * j) =
@@ -1145,9 +1143,7 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                             for (int k = 0; k < 16; ++k) {
                                 const int p = 8 * (k >> 1) + c0 + (k & 1);
                                 if (p < lh)
-                                    dst[8 * (k >> 1) + (k & 1)] =
-                                        (nan >> p) & 1ull ? __uint_as_float(0x7FC00000u)
-                                                          : __uint_as_float(rr[4 * (k >> 1) + (k & 1)]) * f;
+                                    dst[8 * (k >> 1) + (k & 1)] = __uint_as_float(rr[4 * (k >> 1) + (k & 1)]) * f;
                             }
                         }
                     }
@@ -1486,6 +1482,23 @@ attn_q8_t128_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     // tail tile) come the tree's, of which a row sees its path
                     const bool tail = left > kTailMark / 2;
                     const int d = tail ? left - kTailMark : left;
+                    if (tail) {
+                        // the keys have a scale each: the scores in full, before the
+                        // masks (a query row that is none has a NaN for its scale)
+                        const uint8_t *ke = aux->key_exp[t & 3] + 64 * h + 32 * odd + c0;
+#pragma unroll
+                        for (int w = 0; w < J; ++w) {
+                            const uint32_t two = *reinterpret_cast<const uint16_t *>(ke + 8 * w);
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const float f = __uint_as_float(((two >> (8 * i)) & 0xFFu) << 23);
+                                r[4 * w + i] = __float_as_uint(__uint_as_float(r[4 * w + i]) * fmaxf(rsA * f, 0.f));
+                                r[4 * w + 2 + i] =
+                                    __float_as_uint(__uint_as_float(r[4 * w + 2 + i]) * fmaxf(rsB * f, 0.f));
+                            }
+                        }
+                        cA = cB = 1.f;
+                    }
                     const unsigned long long wA = row_vis(tail ? ancA : 0ull, d);
                     const unsigned long long wB = row_vis(tail ? ancB : 0ull, d);
 #pragma unroll

@@ -1,5 +1,6 @@
 """The 8-bit cache's attention on the GPU, beyond the plain forms' sizes: the same
-call twice, long tails with keys that are no numbers."""
+call twice, tail rows of very different sizes, long tails with keys that are no
+numbers."""
 import math
 
 import numpy as np
@@ -59,6 +60,89 @@ def test_the_same_call_gives_the_same_bits(hq, hkv, d, n_q8, n_tail, t, root):
         assert not root or torch.equal(rs, first[1]), rep
     assert L.workspace_status(ws) == 0
     torch.cuda.synchronize()
+
+
+# ------------------------------------------------- tail rows far apart in size
+def near(q, k, v, n_ctx, parent, scale):
+    """(out, bound) as P8.attention, with every score's error taken at its own
+    position: eta_j = (sum of its magnitudes) * per + 2^-18, so that a position
+    without weight does not widen the bound.  Weights w_j e^(+-eta_j) move the
+    result by at most sum w_j (e^eta_j - e^-eta_j) |v_j - out| / sum w_j e^-eta_j."""
+    t, hq, d = q.shape
+    g = hq // k.shape[0]
+    per = (d + 8) * 2.0 ** -23 + 2.0 ** -20
+    vis = P8.sees(parent)
+    out = torch.empty(t, hq, d, dtype=torch.float64)
+    bound = torch.empty_like(out)
+    for h in range(hq):
+        kh, vh, qd = k[h // g], v[h // g], q[:, h].cpu().double()
+        for i in range(t):
+            at = torch.cat([torch.arange(n_ctx), n_ctx + vis[i].nonzero()[:, 0]])
+            x = kh[at] @ qd[i] * scale
+            eta = kh[at].abs() @ qd[i].abs() * abs(scale) * per + 2.0 ** -18
+            x = x - torch.logsumexp(x, 0)
+            w, more, less = x.exp(), (x + eta).exp(), (x - eta).exp()
+            o = w @ vh[at]
+            off = (vh[at] - o).abs()
+            move = torch.maximum(w @ vh[at].abs(), w @ off)
+            out[i, h] = o
+            bound[i, h] = (2.0 ** -8 * (move + o.abs()) * (1 + 2.0 ** -7) +
+                           (more - less) @ off / less.sum() + 1e-30)
+    return out, bound
+
+
+KERNELS = [(8, 2, 64, 128), (16, 4, 128, 2176), (148, 74, 128, 640)]   # general, general, tcgen05
+
+
+@pytest.mark.parametrize("hq,hkv,d,n_q8", KERNELS)
+@pytest.mark.parametrize("size", [1e5, 1e30])
+def test_a_large_unseen_key_changes_nothing(hq, hkv, d, n_q8, size):
+    """Finite keys and values of a branch that a node does not see."""
+    t, n_tail = 13, 30
+    c = P8.cache_inputs(90, hkv, d, n_q8, n_tail, t)
+    q, parent, scale = P8.bf16(np.random.default_rng(91), t, hq * d).reshape(t, hq, d), P8.parents("bfs", t), d ** -0.5
+    c["k_tail"][:, n_tail + 2] *= size
+    c["k_tail"][:, n_tail + 12, 5] = -size
+    c["v_tail"][:, n_tail + 12] *= size
+    cache = L.KvCacheQ8(**{k: x.cuda() for k, x in c.items()}, n_q8=n_q8, n_tail=n_tail)
+    rs = torch.empty(hq, n_q8 + n_tail, device="cuda")
+    out = L.tree_verify_attn_q8(q.cuda(), cache, parent, root_scores_out=rs).double().cpu()
+    k, v = (P8.cache_rows(c, n, n_q8, 0, n_tail + t) for n in "kv")
+    vis = P8.sees(parent)
+    free = ~(vis[:, 2] | vis[:, 12])
+    assert bool(free.any()) and not bool(free.all())
+    want, bound = near(q, k, v, n_q8 + n_tail, parent, scale)
+    assert bool(((out - want).abs() <= bound)[free].all()), float(((out - want).abs() / bound)[free].max())
+    _, _, wr, br = P8.attention(q[:1], k[:, :n_q8 + n_tail + 1], v[:, :n_q8 + n_tail + 1], n_q8 + n_tail, [-1], scale)
+    assert bool(((rs.double().cpu() - wr).abs() <= br).all())
+
+
+@pytest.mark.parametrize("hq,hkv,d,n_q8", KERNELS + [(74, 74, 128, 0)])
+@pytest.mark.parametrize("power", [20, 60])
+def test_tail_keys_of_very_different_sizes(hq, hkv, d, n_q8, power):
+    """Context rows in the tail from 2^-power to 2^power; the large ones point
+    away from every query, the root's scores are right at each."""
+    t, n_tail = 4, 330
+    c = P8.cache_inputs(92, hkv, d, n_q8, n_tail, t)
+    rng = np.random.default_rng(93)
+    q = P8.bf16(rng, t, hq * d).reshape(t, hq, d)
+    q[:] = q[:1, :1]
+    away = -(q[0, 0].double() / q[0, 0].double().norm())
+    size = torch.from_numpy(rng.integers(-power, power + 1, (hkv, n_tail, 1)).astype(np.float64))
+    rows = c["k_tail"][:, :n_tail].double()
+    rows = torch.where(size > 0, rows.norm(dim=-1, keepdim=True) * away, rows) * 2.0 ** size
+    c["k_tail"][:, :n_tail] = rows.to(torch.bfloat16)
+    cache = L.KvCacheQ8(**{k: x.cuda() for k, x in c.items()}, n_q8=n_q8, n_tail=n_tail)
+    rs = torch.empty(hq, n_q8 + n_tail, device="cuda")
+    parent = P8.parents("chain", t)
+    out = L.tree_verify_attn_q8(q.cuda(), cache, parent, root_scores_out=rs).double().cpu()
+    k, v = (P8.cache_rows(c, n, n_q8, 0, n_tail + t) for n in "kv")
+    want, bound = near(q, k, v, n_q8 + n_tail, parent, d ** -0.5)
+    assert bool(((out - want).abs() <= bound).all()), float(((out - want).abs() / bound).max())
+    _, _, wr, br = P8.attention(q[:1], k[:, :n_q8 + n_tail + 1], v[:, :n_q8 + n_tail + 1],
+                                n_q8 + n_tail, [-1], d ** -0.5)
+    err = (rs.double().cpu() - wr).abs()
+    assert bool((err <= br).all()), float((err / br).max())
 
 
 # --------------------------------------------------- values that are no numbers
