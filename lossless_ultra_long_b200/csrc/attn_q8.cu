@@ -20,9 +20,9 @@
 // of the bf16 tail (context, then the tree).  cp.async brings the bytes into
 // a three-stage ring; a block's codes are turned into bf16 rows in a work
 // tile, a tail tile is used where it lies.  Only tail tiles evaluate masks.
-// A tail position whose K or V row holds an infinity or a NaN is kept out of
-// the products (0 * NaN would reach rows that do not see it) and turns the
-// rows that do see it into NaN.
+// A tail row of K or of V that holds an infinity or a NaN is kept out of its
+// product (0 * NaN would reach rows that do not see it) and turns the rows that do
+// see its position into NaN.
 #include <math.h>
 
 #include "attn_q8.cuh"
@@ -301,7 +301,7 @@ attn_q8_kernel(AttnQ8Args a, TreeMasks masks, int tiles_per_split, int n_split, 
             }
             ks = smem_u32(work);
         } else {
-            // rows with an infinity or a NaN leave the products
+            // rows with an infinity or a NaN leave their product
             if (threadIdx.x == 0)
                 odd_rows = odd_keys = 0ull;
             __syncthreads();
@@ -319,9 +319,10 @@ attn_q8_kernel(AttnQ8Args a, TreeMasks masks, int tiles_per_split, int n_split, 
             odd = odd_rows;
             odd_k = odd_keys;
             if (odd) {
+                // (a key whose value is no number still has its score)
                 for (int c = threadIdx.x; c < kTile * D / 4; c += nthreads) {
                     const int which = c / (kTile * D / 8), ch = c % (kTile * D / 8);
-                    if ((odd >> (ch / (D / 8))) & 1ull)
+                    if (((which ? odd : odd_k) >> (ch / (D / 8))) & 1ull)
                         *reinterpret_cast<uint4 *>(raw + which * TB + 16 * ch) =
                             make_uint4(0u, 0u, 0u, 0u);
                 }

@@ -717,8 +717,9 @@ __device__ __forceinline__ void combine_row(const AttnQ8Args &a, const TreeMasks
 
 // The keys of tail tile t into its two K slots, by the converters' 128 threads,
 // a row each: scaled to at most 448 by a power of two (noted in key_exp), split
-// into e4m3 and e5m2 codes; notes the rows with an infinity or a NaN (and zeroes
-// them).  False when a wait ran out.
+// into e4m3 and e5m2 codes; notes the rows with an infinity or a NaN, and zeroes
+// the keys among them (a key whose value is no number still has its score).  False
+// when a wait ran out.
 __device__ __noinline__ bool tail_keys(const AttnQ8Args &a, Aux *aux, unsigned char *sK, int SK, int g,
                                        int nq, int t, int &met, volatile uint32_t *abort,
                                        WorkspaceHeader *hdr)
@@ -763,7 +764,7 @@ __device__ __noinline__ bool tail_keys(const AttnQ8Args &a, Aux *aux, unsigned c
 #pragma unroll 2
     for (int c = 0; c < kD / 16; ++c) {   // 16 codes a step
         uint4 hi = make_uint4(0u, 0u, 0u, 0u), lo = hi;
-        if (have && !bad) {
+        if (have && !bad_k) {
             uint2 h0, l0, h1, l1;
             split_16b(__ldg(kr + 2 * c), f, h0, l0);
             split_16b(__ldg(kr + 2 * c + 1), f, h1, l1);

@@ -1,5 +1,5 @@
 """The 8-bit cache's attention on the GPU, beyond the plain forms' sizes: the same
-call twice, tail rows of very different sizes, long tails with keys that are no
+call twice, tail rows of very different sizes, rows that hold no
 numbers."""
 import math
 
@@ -146,6 +146,34 @@ def test_tail_keys_of_very_different_sizes(hq, hkv, d, n_q8, power):
 
 
 # --------------------------------------------------- values that are no numbers
+@pytest.mark.parametrize("hq,hkv,d,n_q8", KERNELS + [(74, 74, 128, 0)])
+@pytest.mark.parametrize("what", [math.inf, math.nan])
+def test_root_scores_do_not_depend_on_values(hq, hkv, d, n_q8, what):
+    """A row of V that is no number makes the outputs NaN, not a score; a row
+    of K its own score."""
+    t, n_tail = 5, 150
+    c = P8.cache_inputs(94, hkv, d, n_q8, n_tail, t)
+    q, parent = P8.bf16(np.random.default_rng(95), t, hq * d).reshape(t, hq, d), P8.parents("bfs", t)
+    c["v_tail"][:, 7, 3] = what
+    c["v_tail"][:, 140, d - 1] = -what
+    c["v_tail"][0, n_tail + 3, 0] = what
+    c["k_tail"][hkv - 1, 99, 1] = what
+    cache = L.KvCacheQ8(**{k: x.cuda() for k, x in c.items()}, n_q8=n_q8, n_tail=n_tail)
+    rs = torch.zeros(hq, n_q8 + n_tail, device="cuda")
+    out = L.tree_verify_attn_q8(q.cuda(), cache, parent, root_scores_out=rs)
+    assert bool(torch.isnan(out).all())
+    k = P8.cache_rows(c, "k", n_q8, 0, n_tail + t)
+    bad = n_q8 + 99
+    k[hkv - 1, bad] = 0.0
+    _, _, wr, br = P8.attention(q[:1], k[:, :n_q8 + n_tail + 1], torch.zeros_like(k[:, :n_q8 + n_tail + 1]),
+                                n_q8 + n_tail, [-1], d ** -0.5)
+    got = rs.double().cpu()
+    last = slice(hq - hq // hkv, hq)
+    assert bool(torch.isnan(got[last, bad]).all())
+    got[last, bad] = 0.0
+    assert bool(((got - wr).abs() <= br).all()), float(((got - wr).abs() / br).max())
+
+
 @pytest.mark.parametrize("hq,hkv,n_tail,t", [(74, 74, 2500, 3), (592, 74, 2000, 12), (592, 74, 1900, 16),
                                              (296, 74, 1500, 40)])
 def test_many_tail_tiles_with_keys_that_are_no_numbers(hq, hkv, n_tail, t):
