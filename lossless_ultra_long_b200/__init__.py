@@ -238,10 +238,25 @@ def _raise(rc, where):
         raise TsError(rc, where)
 
 
-def new_workspace(nbytes: int, device=None) -> torch.Tensor:
-    """A zero-filled uint8 device buffer (torch allocations are 512-byte aligned)."""
+# A call's own buffers are made on the stream that it runs on: a workspace's
+# zeros are there before the kernel reads them, and memory that is freed when
+# the call returns goes to what this stream runs next, not to another's work.
+def new_workspace(nbytes: int, device=None, stream=None) -> torch.Tensor:
+    """A zero-filled uint8 device buffer (torch allocations are 512-byte
+    aligned), made on ``stream`` (None: the current one), behind which a call
+    on another stream has to be ordered."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return new_workspace(nbytes, device)
     return torch.zeros(max(int(nbytes), 256), dtype=torch.uint8,
                        device=device if device is not None else "cuda")
+
+
+def _empty(shape, dtype, device, stream):
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=dtype, device=device)
+    return torch.empty(shape, dtype=dtype, device=device)
 
 
 # ----------------------------------------------------------- attention
@@ -269,10 +284,10 @@ def tree_verify_attn(q, k_cache, v_cache, n_ctx: int, parent, out=None, workspac
     if v_cache.shape != k_cache.shape or d2 != d:
         raise ValueError("k_cache / v_cache / q shapes disagree")
     if out is None:
-        out = torch.empty((t, hq, d), dtype=torch.float32, device=dev)
+        out = _empty((t, hq, d), torch.float32, dev, stream)
     _check_dev("out", out, torch.float32, dev)
     if workspace is None:
-        workspace = new_workspace(tree_verify_attn_workspace_size(hq, hkv, d, n_ctx, t), dev)
+        workspace = new_workspace(tree_verify_attn_workspace_size(hq, hkv, d, n_ctx, t), dev, stream)
     par, par_p = _host_i32(parent)
     if len(par) != t:
         raise ValueError("parent must have one entry per tree node")
@@ -316,13 +331,13 @@ def kv_importance_select(q_last, k_cache, v_cache, n_ctx: int, n_sink: int, budg
     hkv, cap, d2 = k_cache.shape
     n_keep = min(n_ctx, n_sink + budget)
     if k_partial is None:
-        k_partial = torch.empty((hkv, n_keep, d), dtype=torch.bfloat16, device=dev)
+        k_partial = _empty((hkv, n_keep, d), torch.bfloat16, dev, stream)
     if v_partial is None:
-        v_partial = torch.empty_like(k_partial)
+        v_partial = _empty(k_partial.shape, _BF16, dev, stream)
     if idx_out is None:
-        idx_out = torch.empty((hkv, n_keep), dtype=torch.int32, device=dev)
+        idx_out = _empty((hkv, n_keep), torch.int32, dev, stream)
     if want_scores and scores_out is None:
-        scores_out = torch.empty((hkv, n_ctx), dtype=torch.float32, device=dev)
+        scores_out = _empty((hkv, n_ctx), torch.float32, dev, stream)
     for name, t, dt in (("k_partial", k_partial, torch.bfloat16),
                         ("v_partial", v_partial, torch.bfloat16),
                         ("idx_out", idx_out, torch.int32)):
@@ -330,7 +345,7 @@ def kv_importance_select(q_last, k_cache, v_cache, n_ctx: int, n_sink: int, budg
     if scores_out is not None:
         _check_dev("scores_out", scores_out, torch.float32, dev)
     if workspace is None:
-        workspace = new_workspace(kv_importance_select_workspace_size(hq, hkv, d, n_ctx), dev)
+        workspace = new_workspace(kv_importance_select_workspace_size(hq, hkv, d, n_ctx), dev, stream)
     scale = float(d) ** -0.5 if softmax_scale is None else float(softmax_scale)
     rc = _lib().ts_kv_importance_select(
         _ptr(q_last), _ptr(k_cache), _ptr(v_cache), cap, hq, hkv, d, int(n_ctx), int(n_sink),
@@ -362,13 +377,13 @@ def kv_select_from_scores(root_scores, k_cache, v_cache, n_ctx: int, n_sink: int
     hkv, cap, d = k_cache.shape
     n_keep = min(n_ctx, n_sink + budget)
     if k_partial is None:
-        k_partial = torch.empty((hkv, n_keep, d), dtype=torch.bfloat16, device=dev)
+        k_partial = _empty((hkv, n_keep, d), torch.bfloat16, dev, stream)
     if v_partial is None:
-        v_partial = torch.empty_like(k_partial)
+        v_partial = _empty(k_partial.shape, _BF16, dev, stream)
     if idx_out is None:
-        idx_out = torch.empty((hkv, n_keep), dtype=torch.int32, device=dev)
+        idx_out = _empty((hkv, n_keep), torch.int32, dev, stream)
     if want_scores and scores_out is None:
-        scores_out = torch.empty((hkv, n_ctx), dtype=torch.float32, device=dev)
+        scores_out = _empty((hkv, n_ctx), torch.float32, dev, stream)
     for name, t, dt in (("k_partial", k_partial, torch.bfloat16),
                         ("v_partial", v_partial, torch.bfloat16),
                         ("idx_out", idx_out, torch.int32)):
@@ -376,7 +391,7 @@ def kv_select_from_scores(root_scores, k_cache, v_cache, n_ctx: int, n_sink: int
     if scores_out is not None:
         _check_dev("scores_out", scores_out, torch.float32, dev)
     if workspace is None:
-        workspace = new_workspace(kv_select_from_scores_workspace_size(hq, hkv, int(n_ctx)), dev)
+        workspace = new_workspace(kv_select_from_scores_workspace_size(hq, hkv, int(n_ctx)), dev, stream)
     rc = _lib().ts_kv_select_from_scores(
         _ptr(root_scores), _ptr(k_cache), _ptr(v_cache), cap, hq, hkv, d, int(n_ctx),
         int(n_sink), int(budget), _ptr(scores_out), _ptr(idx_out), _ptr(k_partial),
@@ -412,14 +427,14 @@ def penalize_accept(logits, window, penalty: float, parent, tree_tokens, argmax_
     else:
         wlen, wptr = 0, None
     if accept_out is None:
-        accept_out = torch.empty(2 + t, dtype=torch.int32, device=dev)
+        accept_out = _empty(2 + t, torch.int32, dev, stream)
     if want_argmax and argmax_out is None:
-        argmax_out = torch.empty(t, dtype=torch.int32, device=dev)
+        argmax_out = _empty(t, torch.int32, dev, stream)
     _check_dev("accept_out", accept_out, torch.int32, dev)
     if argmax_out is not None:
         _check_dev("argmax_out", argmax_out, torch.int32, dev)
     if workspace is None:
-        workspace = new_workspace(penalize_accept_workspace_size(t, vocab), dev)
+        workspace = new_workspace(penalize_accept_workspace_size(t, vocab), dev, stream)
     par, par_p = _host_i32(parent)
     if len(par) != t:
         raise ValueError("parent must have one entry per tree node")
@@ -464,14 +479,14 @@ def penalize_sample_accept(logits, gumbel, temperature: float, window, penalty: 
     else:
         wlen, wptr = 0, None
     if accept_out is None:
-        accept_out = torch.empty(2 + t, dtype=torch.int32, device=dev)
+        accept_out = _empty(2 + t, torch.int32, dev, stream)
     if want_target and target_out is None:
-        target_out = torch.empty(t, dtype=torch.int32, device=dev)
+        target_out = _empty(t, torch.int32, dev, stream)
     _check_dev("accept_out", accept_out, torch.int32, dev)
     if target_out is not None:
         _check_dev("target_out", target_out, torch.int32, dev)
     if workspace is None:
-        workspace = new_workspace(penalize_accept_workspace_size(t, vocab), dev)
+        workspace = new_workspace(penalize_accept_workspace_size(t, vocab), dev, stream)
     par, par_p = _host_i32(parent)
     if len(par) != t:
         raise ValueError("parent must have one entry per tree node")
@@ -496,7 +511,7 @@ def kv_commit_path(k_cache, v_cache, n_ctx: int, n_tree: int, accept, workspace=
     if v_cache.shape != k_cache.shape:
         raise ValueError("k_cache / v_cache shapes disagree")
     if workspace is None:
-        workspace = new_workspace(256, dev)
+        workspace = new_workspace(256, dev, stream)
     rc = _lib().ts_kv_commit_path(_ptr(k_cache), _ptr(v_cache), cap, hkv, d, int(n_ctx),
                                   int(n_tree), _ptr(accept), _ptr(workspace),
                                   _ws_bytes(workspace, dev), _stream(stream))
@@ -566,7 +581,7 @@ def rope_append(q, k, v, k_cache, v_cache, row0: int, pos0: int, inv_freq, paren
     if q is not None:
         qs, hq = _check_rows("q", q, None, d, dev), q.shape[1]
         if q_out is None:
-            q_out = torch.empty((n, hq, d), dtype=_BF16, device=dev)
+            q_out = _empty((n, hq, d), _BF16, dev, stream)
         _check_dev("q_out", q_out, _BF16, dev)
         if q_out.shape != q.shape:
             raise ValueError("q_out must have q's shape")
@@ -702,7 +717,7 @@ class KvCacheQ8:
         _check_dev("accept", accept, _I32, self.device)
         dev = _call_device("k_tail", self.k_tail)
         if workspace is None:
-            workspace = new_workspace(256, dev)
+            workspace = new_workspace(256, dev, stream)
         hkv, cap, d = self.k_tail.shape
         if self.tail_row0 + self.n_tail + int(n_tree) > cap:
             raise ValueError("the tree's rows do not lie in the tail")
@@ -765,7 +780,7 @@ def tree_verify_attn_q8(q, cache: KvCacheQ8, parent, out=None, workspace=None,
     if d != st.head_dim:
         raise ValueError("q and the cache must have the same head_dim")
     if out is None:
-        out = torch.empty((t, hq, d), dtype=_BF16, device=dev)
+        out = _empty((t, hq, d), _BF16, dev, stream)
     _check_dev("out", out, _BF16, dev)
     if out.shape != q.shape:
         raise ValueError("out must have q's shape")
@@ -775,7 +790,7 @@ def tree_verify_attn_q8(q, cache: KvCacheQ8, parent, out=None, workspace=None,
             raise ValueError("root_scores_out must be [Hq, n_ctx]")
     if workspace is None:
         workspace = new_workspace(tree_verify_attn_q8_workspace_size(
-            hq, st.n_heads_kv, d, st.n_q8, st.n_tail, t), dev)
+            hq, st.n_heads_kv, d, st.n_q8, st.n_tail, t), dev, stream)
     par, par_p = _parent_arg(parent, t)
     scale = float(d) ** -0.5 if softmax_scale is None else float(softmax_scale)
     rc = _lib().ts_tree_verify_attn_q8(
@@ -785,12 +800,12 @@ def tree_verify_attn_q8(q, cache: KvCacheQ8, parent, out=None, workspace=None,
     return out
 
 
-def _q8_partials(cache, n_keep, k_partial, v_partial, dev):
+def _q8_partials(cache, n_keep, k_partial, v_partial, dev, stream):
     hkv, _, d = cache.k8.shape
     if k_partial is None:
-        k_partial = torch.empty((hkv, n_keep, d), dtype=_BF16, device=dev)
+        k_partial = _empty((hkv, n_keep, d), _BF16, dev, stream)
     if v_partial is None:
-        v_partial = torch.empty_like(k_partial)
+        v_partial = _empty(k_partial.shape, _BF16, dev, stream)
     _check_dev("k_partial", k_partial, _BF16, dev)
     _check_dev("v_partial", v_partial, _BF16, dev)
     if (k_partial.dim() != 3 or k_partial.shape[0] != hkv or k_partial.shape[2] != d or
@@ -807,9 +822,9 @@ def kv_gather_q8(cache: KvCacheQ8, idx, k_partial=None, v_partial=None, workspac
     _check_dev("idx", idx, _I32, dev)
     if idx.dim() != 2 or idx.shape[0] != st.n_heads_kv:
         raise ValueError("idx must be [Hkv, n_keep]")
-    k_partial, v_partial = _q8_partials(cache, idx.shape[1], k_partial, v_partial, dev)
+    k_partial, v_partial = _q8_partials(cache, idx.shape[1], k_partial, v_partial, dev, stream)
     if workspace is None:
-        workspace = new_workspace(256, dev)
+        workspace = new_workspace(256, dev, stream)
     _raise(_lib().ts_kv_gather_q8(
         ctypes.byref(st), _ptr(idx), idx.shape[1], _ptr(k_partial), _ptr(v_partial),
         k_partial.shape[1], _ptr(workspace), _ws_bytes(workspace, dev), _stream(stream, dev)),
@@ -833,20 +848,20 @@ def kv_select_from_scores_q8(root_scores, cache: KvCacheQ8, n_sink: int, budget:
     if root_scores.shape[1] != n_ctx:
         raise ValueError("root_scores must be [Hq, n_ctx]")
     n_keep = min(n_ctx, int(n_sink) + int(budget))
-    k_partial, v_partial = _q8_partials(cache, n_keep, k_partial, v_partial, dev)
+    k_partial, v_partial = _q8_partials(cache, n_keep, k_partial, v_partial, dev, stream)
     if idx_out is None:
-        idx_out = torch.empty((hkv, n_keep), dtype=_I32, device=dev)
+        idx_out = _empty((hkv, n_keep), _I32, dev, stream)
     _check_dev("idx_out", idx_out, _I32, dev)
     if idx_out.numel() != hkv * n_keep:
         raise ValueError("idx_out must be [Hkv, n_keep]")
     if want_scores and scores_out is None:
-        scores_out = torch.empty((hkv, n_ctx), dtype=torch.float32, device=dev)
+        scores_out = _empty((hkv, n_ctx), torch.float32, dev, stream)
     if scores_out is not None:
         _check_dev("scores_out", scores_out, torch.float32, dev)
         if scores_out.numel() != hkv * n_ctx:
             raise ValueError("scores_out must be [Hkv, n_ctx]")
     if workspace is None:
-        workspace = new_workspace(kv_select_from_scores_workspace_size(hq, hkv, n_ctx), dev)
+        workspace = new_workspace(kv_select_from_scores_workspace_size(hq, hkv, n_ctx), dev, stream)
     _raise(_lib().ts_kv_select_from_scores_q8(
         _ptr(root_scores), ctypes.byref(st), hq, int(n_sink), int(budget), _ptr(scores_out),
         _ptr(idx_out), _ptr(k_partial), _ptr(v_partial), k_partial.shape[1], _ptr(workspace),
@@ -864,7 +879,7 @@ def selftest_bounded_wait(workspace=None, stream=None):
     on a barrier nothing completes; about a second later TS_ERR_TIMEOUT is
     in the workspace's status word.  Returns the workspace."""
     if workspace is None:
-        workspace = new_workspace(256)
+        workspace = new_workspace(256, stream=stream)
     nbytes = _ws_bytes(workspace, _call_device("workspace", workspace))
     _raise(_lib().ts_selftest_bounded_wait(_ptr(workspace), nbytes, _stream(stream)),
            "ts_selftest_bounded_wait")
