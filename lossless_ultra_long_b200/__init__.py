@@ -10,6 +10,7 @@ call raises.
 from __future__ import annotations
 
 import array
+import contextlib
 import ctypes
 import os
 
@@ -672,9 +673,9 @@ class KvCacheQ8:
     @classmethod
     def empty(cls, n_heads_kv: int, head_dim: int, capacity: int, tail_rows: int = 256,
               device=None):
-        """An empty cache for ``capacity`` 8-bit rows (rounded up to 64).  The
-        tail takes a step's tree behind up to 63 rows (128 rows), or a
-        prompt's chunk."""
+        """An empty cache for ``capacity`` 8-bit rows (rounded up to 64), made on
+        the current stream.  The tail takes a step's tree, or a prompt's chunk,
+        behind the up to 63 rows that :meth:`fold` leaves."""
         device = "cuda" if device is None else device
         cap = -(-int(capacity) // TS_Q8_BLOCK) * TS_Q8_BLOCK
 
@@ -730,9 +731,8 @@ class KvCacheQ8:
         self.n_tail += int(n_accepted) + 1
 
     def fold(self, stream=None) -> int:
-        """Turns the tail's full blocks into 8 bits and, where the tail's end
-        is near, moves the rows that are left to its start.  Returns the rows
-        folded."""
+        """Turns the tail's full blocks into 8 bits and moves the rows that are
+        left (fewer than 64) to its start.  Returns the rows folded."""
         rows = self.n_tail // TS_Q8_BLOCK * TS_Q8_BLOCK
         if rows:
             kv_quantize_q8(self.k_tail, self.v_tail, self.tail_row0, rows, self.k8, self.v8,
@@ -740,13 +740,13 @@ class KvCacheQ8:
             self.n_q8 += rows
             self.n_tail -= rows
             self.tail_row0 += rows
-        # fewer than 64 rows are left; those before them are done with
-        if (self.tail_row0 and self.tail_row0 >= self.n_tail and
-                self.k_tail.shape[1] - self.tail_row0 < 3 * TS_Q8_BLOCK):
-            cur = torch.cuda.current_stream() if stream is None else stream
-            with torch.cuda.stream(cur):
-                for t in (self.k_tail, self.v_tail):
-                    t[:, :self.n_tail].copy_(t[:, self.tail_row0:self.tail_row0 + self.n_tail])
+        if self.tail_row0:
+            _call_device("k_tail", self.k_tail)
+            n, at = self.n_tail, self.tail_row0
+            with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+                for t in (self.k_tail, self.v_tail) if n else ():
+                    left = t[:, at:at + n]
+                    t[:, :n].copy_(left if at >= n else left.clone())
             self.tail_row0 = 0
         return rows
 
