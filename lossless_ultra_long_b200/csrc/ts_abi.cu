@@ -431,7 +431,9 @@ int ts_kv_quantize_q8(const void *k, const void *v, int64_t src_cap, int n_heads
                       int64_t src_row0, int n_rows, void *k8, void *v8, uint8_t *k_scale,
                       uint8_t *v_scale, int64_t q8_cap, int64_t dst_row, void *stream)
 {
-    if (!k || !v || !k8 || !v8 || !k_scale || !v_scale || n_heads_kv < 1 || n_heads_kv > 1024)
+    // (an empty call's buffers may have no address)
+    if ((n_rows > 0 && (!k || !v || !k8 || !v8 || !k_scale || !v_scale)) || n_heads_kv < 1 ||
+        n_heads_kv > 1024)
         return TS_ERR_INVALID_ARG;
     if (n_rows < 0 || n_rows % TS_Q8_BLOCK || dst_row < 0 || dst_row % TS_Q8_BLOCK ||
         q8_cap < 0 || q8_cap % TS_Q8_BLOCK || src_row0 < 0)
@@ -558,7 +560,7 @@ int ts_kv_gather_q8(const ts_q8_cache *cache, const int32_t *idx, int n_keep, vo
     const int st = q8_cache_check(cache, 0, &a.c);
     if (st != TS_OK)
         return st;
-    if (!idx || !k_partial || !v_partial || n_keep < 0 || partial_cap < n_keep ||
+    if ((n_keep > 0 && (!idx || !k_partial || !v_partial)) || n_keep < 0 || partial_cap < n_keep ||
         !aligned(idx, 4) || !aligned(k_partial, 16) || !aligned(v_partial, 16))
         return TS_ERR_INVALID_ARG;
     if (!workspace_ok(workspace, workspace_bytes, ts::kHeaderBytes))
@@ -630,8 +632,9 @@ int ts_rope_append(const void *q, int64_t q_stride, const void *k, int64_t k_str
                    int rot_dim, int interleaved, float mscale, void *q_out, void *k_cache,
                    void *v_cache, int64_t kv_cap, int64_t row0, void *stream)
 {
-    if (!k || !v || !k_cache || !v_cache || n_heads_kv < 1 || n_heads_kv > 1024 ||
-        n_heads_q < 0 || n_heads_q > 1024 || (n_heads_q > 0 && (!q || !q_out)))
+    if (n_heads_kv < 1 || n_heads_kv > 1024 || n_heads_q < 0 || n_heads_q > 1024)
+        return TS_ERR_INVALID_ARG;
+    if (n_tok > 0 && (!k || !v || !k_cache || !v_cache || (n_heads_q > 0 && (!q || !q_out))))
         return TS_ERR_INVALID_ARG;
     if (n_tok < 0 || pos0 < 0 || row0 < 0 || kv_cap < n_tok || row0 > kv_cap - n_tok ||
         !isfinite(mscale))

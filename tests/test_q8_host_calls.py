@@ -1,0 +1,72 @@
+"""Calls of the 8-bit cache's operators that a machine without a GPU can decide:
+those without rows, through the C ABI and through the binding.  As in
+test_binding_host.py host tensors stand in for device tensors."""
+import ctypes
+import types
+
+import pytest
+import torch
+
+import lossless_ultra_long_b200 as L
+from test_binding_host import on_dev, workspace, zeros
+
+STREAM = types.SimpleNamespace(cuda_stream=0)
+D, HKV, HQ = 64, 2, 8
+no_gpu = pytest.mark.skipif(torch.cuda.is_available(), reason="host-memory stand-ins are for machines without a GPU")
+
+
+@pytest.fixture(autouse=True)
+def _current_device_zero(monkeypatch):
+    from lossless_ultra_long_b200 import build
+    build.build()
+    if not torch.cuda.is_available():
+        monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+        monkeypatch.setattr(L, "_raw_stream", lambda index: 0)
+
+
+def bf16(*shape):
+    return zeros(shape, torch.bfloat16)
+
+
+def cache(n_q8=64, n_tail=5, cap=128, tail=100):
+    k8, v8 = (on_dev(torch.zeros(HKV, cap, D, dtype=torch.uint8).view(torch.float8_e4m3fn)) for _ in "kv")
+    scales = (zeros((HKV, cap // 64), torch.uint8) for _ in "kv")
+    return L.KvCacheQ8(k8, v8, *scales, bf16(HKV, tail, D), bf16(HKV, tail, D), n_q8=n_q8, n_tail=n_tail)
+
+
+# ------------------------------------------------------------------ without rows
+def test_empty_calls_need_no_addresses():
+    lib = L.library()
+    assert lib.ts_kv_quantize_q8(None, None, 0, 2, 64, 0, 0, None, None, None, None, 0, 0, None) == 0
+    st = L._Q8Cache(0, 0, 0, 0, 0, 0, 0, 0, 0, 2, 64, 0, 0)
+    assert lib.ts_kv_gather_q8(ctypes.byref(st), None, 0, None, None, 0, 1 << 20, 256, None) == 0
+    for parent in (None, 1 << 20):
+        assert lib.ts_rope_append(None, 512, None, 128, None, 128, 8, 2, 64, 0, parent, 0, None, 0, 0, 1.0,
+                                  None, None, None, 0, 0, None) == 0
+    # what an empty call says is still checked
+    assert lib.ts_kv_quantize_q8(None, None, 0, 2, 64, 1, 0, None, None, None, None, 0, 0, None) == 1
+    assert lib.ts_kv_quantize_q8(None, None, 0, 2, 96, 0, 0, None, None, None, None, 0, 0, None) == 2
+    assert lib.ts_rope_append(None, 512, None, 128, None, 128, 8, 2, 64, 0, None, 0, None, 0, 0, 1.0,
+                              None, None, None, 10, 11, None) == 1
+    assert lib.ts_kv_gather_q8(ctypes.byref(st), None, 0, None, None, 0, None, 256, None) == 3
+    # and one row needs them
+    assert lib.ts_rope_append(None, 512, None, 128, None, 128, 8, 2, 64, 1, None, 0, None, 0, 0, 1.0,
+                              None, None, None, 10, 0, None) == 1
+    assert lib.ts_kv_gather_q8(ctypes.byref(st), None, 1, None, None, 1, 1 << 20, 256, None) == 1
+
+
+@no_gpu
+def test_empty_calls_of_the_binding():
+    kc, vc = bf16(HKV, 9, D), bf16(HKV, 9, D)
+    q, k, v = bf16(0, HQ, D), bf16(0, HKV, D), bf16(0, HKV, D)
+    ws = dict(q_out=bf16(0, HQ, D), stream=STREAM)
+    for parent in (None, []):
+        assert L.rope_append(q, k, v, kc, vc, 9, 3, zeros(D // 2), parent=parent, **ws).shape == (0, HQ, D)
+    c = cache()
+    assert c.append(q, k, v, zeros(D // 2), **ws).shape == (0, HQ, D) and c.n_tail == 5
+    kp, vp = L.kv_gather_q8(c, zeros((HKV, 0), torch.int32), k_partial=bf16(HKV, 0, D),
+                            v_partial=bf16(HKV, 0, D), workspace=workspace(256), stream=STREAM)
+    assert kp.shape == vp.shape == (HKV, 0, D)
+    none = cache(n_q8=0, n_tail=0, cap=0, tail=0)
+    L.kv_quantize_q8(none.k_tail, none.v_tail, 0, 0, none.k8, none.v8, none.k_scale, none.v_scale, 0, stream=STREAM)
+    assert none.fold(stream=STREAM) == 0
