@@ -716,6 +716,8 @@ class KvCacheQ8:
         if not 0 <= int(n_accepted) < int(n_tree):
             raise ValueError("n_accepted must lie in [0, n_tree)")
         _check_dev("accept", accept, _I32, self.device)
+        if accept.numel() < 2 + int(n_tree):     # the kernel goes by the length it finds there
+            raise ValueError("accept must hold 2 + n_tree entries")
         dev = _call_device("k_tail", self.k_tail)
         if workspace is None:
             workspace = new_workspace(256, dev, stream)

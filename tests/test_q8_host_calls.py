@@ -70,3 +70,16 @@ def test_empty_calls_of_the_binding():
     none = cache(n_q8=0, n_tail=0, cap=0, tail=0)
     L.kv_quantize_q8(none.k_tail, none.v_tail, 0, 0, none.k8, none.v8, none.k_scale, none.v_scale, 0, stream=STREAM)
     assert none.fold(stream=STREAM) == 0
+
+
+# ------------------------------------------------------------- what a call would misread
+@no_gpu
+def test_a_short_acceptance_result_is_refused():
+    """The kernel reads up to 2 + n_tree entries."""
+    c = cache(n_tail=5, tail=100)
+    for n in (0, 2, 14):
+        with pytest.raises(ValueError, match="entries"):
+            c.commit(zeros(n, torch.int32), 13, 0, workspace=workspace(256), stream=STREAM)
+    with pytest.raises(L.TsError) as e:          # enough of them: accepted, there is no device
+        c.commit(zeros(15, torch.int32), 13, 0, workspace=workspace(256), stream=STREAM)
+    assert e.value.status == 4
