@@ -227,10 +227,16 @@ def _parent_arg(parent, n):
     import numpy as np
     if isinstance(parent, torch.Tensor):
         parent = parent.cpu().numpy()
-    arr = (parent if isinstance(parent, np.ndarray) and parent.dtype == np.int32 and
-           parent.flags.c_contiguous else np.array(parent, dtype=np.int32))
+    arr = np.asarray(parent)
     if arr.shape != (n,):
         raise ValueError("parent must have one entry per tree node")
+    if arr.dtype != np.int32:
+        with np.errstate(invalid="ignore"):
+            ints = arr.astype(np.int32)
+        if not (ints == arr).all():
+            raise ValueError("parent must hold 32-bit integers")
+        arr = ints
+    arr = np.ascontiguousarray(arr)
     return arr, arr.__array_interface__["data"][0]
 
 

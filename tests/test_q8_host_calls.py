@@ -2,8 +2,10 @@
 those without rows, through the C ABI and through the binding.  As in
 test_binding_host.py host tensors stand in for device tensors."""
 import ctypes
+import math
 import types
 
+import numpy as np
 import pytest
 import torch
 
@@ -83,3 +85,23 @@ def test_a_short_acceptance_result_is_refused():
     with pytest.raises(L.TsError) as e:          # enough of them: accepted, there is no device
         c.commit(zeros(15, torch.int32), 13, 0, workspace=workspace(256), stream=STREAM)
     assert e.value.status == 4
+
+
+@pytest.mark.parametrize("parent", [
+    np.array([-1, 0, 2 ** 32]), np.array([-1, 2 ** 32 - 1, 0]), [-1, 0, 0.5], np.array([-1.0, 0.0, 1.5]),
+    (-1, 0, math.nan), torch.tensor([-1, 0, 2 ** 33 + 1]), np.array([2 ** 32 - 1, 0, 0], dtype=np.uint32),
+    [-1, 0, 1 << 70], [-1, None, 0], "abc", np.array([[-1, 0, 0]]), [-1, [0], 0],
+], ids=str)
+def test_a_tree_that_is_not_32_bit_integers_is_refused(parent):
+    """(2^32 would be node 0 in 32 bits, 1.5 node 1)"""
+    with pytest.raises((ValueError, TypeError, OverflowError)):
+        L._parent_arg(parent, 3)
+
+
+def test_a_tree_in_other_types_and_strides():
+    wide = np.array([[-1, 7], [0, 7], [1, 7]])
+    for parent in (wide[:, 0], wide.astype(np.int32)[:, 0], np.array([-1.0, 0.0, 1.0]), torch.tensor([-1, 0, 1]).to(
+            torch.int16), np.array([-1, 0, 1], dtype=">i4"), [np.int64(-1), 0, True]):
+        keep, address = L._parent_arg(parent, 3)
+        assert list((ctypes.c_int32 * 3).from_address(address)) == [-1, 0, 1]
+        del keep
