@@ -214,6 +214,14 @@ def _host_i32(a):
     return arr, arr.ctypes.data_as(ctypes.c_void_p)
 
 
+def _int(name, x, bits=32):
+    """x as the C ABI's signed integer (ctypes would cut what lies outside)."""
+    x = int(x)
+    if not -1 << bits - 1 <= x < 1 << bits - 1:
+        raise ValueError(f"{name} must be a signed {bits}-bit integer")
+    return x
+
+
 def _parent_arg(parent, n):
     """(keep-alive, address) of a host int32 parent array of n entries."""
     if type(parent) is list:
@@ -600,9 +608,9 @@ def rope_append(q, k, v, k_cache, v_cache, row0: int, pos0: int, inv_freq, paren
         rot = 2 * inv_freq.numel()
     par, par_p = (None, None) if parent is None else _parent_arg(parent, n)
     _raise(_lib().ts_rope_append(
-        _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, hq, hkv, d, n, par_p, int(pos0),
+        _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, hq, hkv, d, n, par_p, _int("pos0", pos0, 64),
         _ptr(inv_freq) if rot else None, rot, int(bool(interleaved)), float(mscale),
-        _ptr(q_out) if hq else None, _ptr(k_cache), _ptr(v_cache), cap, int(row0),
+        _ptr(q_out) if hq else None, _ptr(k_cache), _ptr(v_cache), cap, _int("row0", row0, 64),
         _stream(stream, dev)), "ts_rope_append")
     return q_out
 
@@ -631,9 +639,10 @@ def kv_quantize_q8(k, v, row0: int, n_rows: int, k8, v8, k_scale, v_scale, dst_r
     if k.dim() != 3 or v.shape != k.shape or k.shape[0] != k8.shape[0] or k.shape[2] != k8.shape[2]:
         raise ValueError("k / v / k8 / v8 shapes disagree")
     hkv, cap, d = k.shape
-    _raise(_lib().ts_kv_quantize_q8(_ptr(k), _ptr(v), cap, hkv, d, int(row0), int(n_rows), _ptr(k8),
-                                    _ptr(v8), _ptr(k_scale), _ptr(v_scale), k8.shape[1],
-                                    int(dst_row), _stream(stream, dev)), "ts_kv_quantize_q8")
+    _raise(_lib().ts_kv_quantize_q8(
+        _ptr(k), _ptr(v), cap, hkv, d, _int("row0", row0, 64), _int("n_rows", n_rows), _ptr(k8), _ptr(v8),
+        _ptr(k_scale), _ptr(v_scale), k8.shape[1], _int("dst_row", dst_row, 64), _stream(stream, dev)),
+        "ts_kv_quantize_q8")
     return k8, v8, k_scale, v_scale
 
 
@@ -855,7 +864,8 @@ def kv_select_from_scores_q8(root_scores, cache: KvCacheQ8, n_sink: int, budget:
     hq, n_ctx, hkv = root_scores.shape[0], cache.n_ctx, st.n_heads_kv
     if root_scores.shape[1] != n_ctx:
         raise ValueError("root_scores must be [Hq, n_ctx]")
-    n_keep = min(n_ctx, int(n_sink) + int(budget))
+    n_sink, budget = _int("n_sink", n_sink), _int("budget", budget)
+    n_keep = min(n_ctx, n_sink + budget)
     k_partial, v_partial = _q8_partials(cache, n_keep, k_partial, v_partial, dev, stream)
     if idx_out is None:
         idx_out = _empty((hkv, n_keep), _I32, dev, stream)
@@ -871,7 +881,7 @@ def kv_select_from_scores_q8(root_scores, cache: KvCacheQ8, n_sink: int, budget:
     if workspace is None:
         workspace = new_workspace(kv_select_from_scores_workspace_size(hq, hkv, n_ctx), dev, stream)
     _raise(_lib().ts_kv_select_from_scores_q8(
-        _ptr(root_scores), ctypes.byref(st), hq, int(n_sink), int(budget), _ptr(scores_out),
+        _ptr(root_scores), ctypes.byref(st), hq, n_sink, budget, _ptr(scores_out),
         _ptr(idx_out), _ptr(k_partial), _ptr(v_partial), k_partial.shape[1], _ptr(workspace),
         _ws_bytes(workspace, dev), _stream(stream, dev)), "ts_kv_select_from_scores_q8")
     return idx_out, k_partial, v_partial, scores_out

@@ -636,8 +636,8 @@ int ts_rope_append(const void *q, int64_t q_stride, const void *k, int64_t k_str
         return TS_ERR_INVALID_ARG;
     if (n_tok > 0 && (!k || !v || !k_cache || !v_cache || (n_heads_q > 0 && (!q || !q_out))))
         return TS_ERR_INVALID_ARG;
-    if (n_tok < 0 || pos0 < 0 || row0 < 0 || kv_cap < n_tok || row0 > kv_cap - n_tok ||
-        !isfinite(mscale))
+    if (n_tok < 0 || pos0 < 0 || pos0 > INT64_MAX - n_tok || row0 < 0 || kv_cap < n_tok ||
+        row0 > kv_cap - n_tok || !isfinite(mscale))
         return TS_ERR_INVALID_ARG;
     if (parent && n_tok > 0 && !tree_ok(parent, n_tok))
         return TS_ERR_INVALID_ARG;

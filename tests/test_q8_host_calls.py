@@ -105,3 +105,41 @@ def test_a_tree_in_other_types_and_strides():
         keep, address = L._parent_arg(parent, 3)
         assert list((ctypes.c_int32 * 3).from_address(address)) == [-1, 0, 1]
         del keep
+
+
+@no_gpu
+@pytest.mark.parametrize("name,at", [("pos0", 2 ** 64 + 5), ("row0", 2 ** 64), ("n_rows", 2 ** 32 + 64),
+                                     ("from", 2 ** 64), ("dst", 2 ** 64), ("n_sink", 2 ** 32 + 4),
+                                     ("budget", 2 ** 32 + 60), ("budget", 2 ** 63)])
+def test_integers_past_the_c_types_are_refused(name, at):
+    """(cut to their low bits these would be valid calls)"""
+    c, f = cache(n_q8=64, n_tail=5), {"pos0": 5, "row0": 0, "n_rows": 64, "from": 0, "dst": 0, "n_sink": 4, "budget": 60}
+
+    def rope():
+        L.rope_append(bf16(4, HQ, D), bf16(4, HKV, D), bf16(4, HKV, D), c.k_tail, c.v_tail, f["row0"], f["pos0"],
+                      zeros(D // 2), q_out=bf16(4, HQ, D), stream=STREAM)
+
+    def quantize():
+        L.kv_quantize_q8(c.k_tail, c.v_tail, f["from"], f["n_rows"], c.k8, c.v8, c.k_scale, c.v_scale, f["dst"],
+                         stream=STREAM)
+
+    def select():
+        L.kv_select_from_scores_q8(zeros((HQ, 69)), c, f["n_sink"], f["budget"], k_partial=bf16(HKV, 69, D),
+                                   v_partial=bf16(HKV, 69, D), idx_out=zeros((HKV, f["keep"]), torch.int32),
+                                   workspace=workspace(), stream=STREAM)
+
+    call = {"pos0": rope, "row0": rope, "n_sink": select, "budget": select}.get(name, quantize)
+    f["keep"] = 64
+    with pytest.raises(L.TsError) as e:          # accepted as it is, there is no device
+        call()
+    assert e.value.status == 4
+    f[name], f["keep"] = at, 69
+    with pytest.raises(ValueError, match="bit integer"):
+        call()
+
+
+def test_positions_past_64_bits_are_refused():
+    lib, A = L.library(), 1 << 20
+    for n_tok, pos0 in ((1, 2 ** 63 - 1), (4, 2 ** 63 - 4)):
+        assert lib.ts_rope_append(A, 512, A, 128, A, 128, 8, 2, 64, n_tok, None, pos0, A, 64, 0, 1.0, 2 * A, A, A,
+                                  10, 0, None) == 1
