@@ -1,6 +1,6 @@
-"""The 8-bit cache's attention on the GPU, beyond the plain forms' sizes: the same
-call twice, tail rows of very different sizes, rows that hold no
-numbers."""
+"""The 8-bit cache's attention on the GPU: the same call twice, tail rows of very
+different sizes, rows that hold no numbers, blocks of zeros; the rotation of long
+prompts."""
 import math
 
 import numpy as np
@@ -198,3 +198,87 @@ def test_many_tail_tiles_with_keys_that_are_no_numbers(hq, hkv, n_tail, t):
         assert torch.equal(torch.isnan(got), mask)
         assert bool(((got - want).abs() <= bound)[~mask].all())
         assert bool(torch.isnan(out).all())
+
+
+# ------------------------------------------------------- one large element in a row
+@pytest.mark.parametrize("hq,hkv,d,n_q8", KERNELS)
+@pytest.mark.parametrize("power", [6, 12, 20])
+def test_small_elements_beside_a_large_one(hq, hkv, d, n_q8, power):
+    """Queries with one element 2^power times the others, where every key has a zero,
+    and tail keys with another where every query has one.  Down to 2^-14 of the
+    largest the others count in full, a smaller one may be off by 2^-21 of it."""
+    t, n_tail = 5, 70
+    c = P8.cache_inputs(98, hkv, d, n_q8, n_tail, t)
+    rng = np.random.default_rng(99)
+    q = P8.bf16(rng, t, hq * d).reshape(t, hq, d)
+    x = c["k8"].view(torch.uint8)
+    x[:, :, 3] = 0
+    x[:, :, 9] = 0
+    c["k_tail"][:, :, 3] = 0.0
+    c["k_tail"][:, :, 9] = 2.0 ** power
+    q[..., 3] = 2.0 ** power
+    q[..., 9] = 0.0
+    cache = L.KvCacheQ8(**{k: y.cuda() for k, y in c.items()}, n_q8=n_q8, n_tail=n_tail)
+    n, parent, scale = n_q8 + n_tail, P8.parents("chain", t), d ** -0.5
+    rs = torch.empty(hq, n, device="cuda")
+    L.tree_verify_attn_q8(q.cuda(), cache, parent, root_scores_out=rs)
+    k = P8.cache_rows(c, "k", n_q8, 0, n_tail)
+    g = hq // hkv
+    q0 = q[0].double().reshape(hkv, g, d)
+    want = torch.einsum("hgd,hnd->hgn", q0, k).reshape(hq, n) * scale / math.log(2)
+    mag = torch.einsum("hgd,hnd->hgn", q0.abs(), k.abs()).reshape(hq, n)
+    # (an element is split without loss from 2^-6 of the scaled row on, whose largest is
+    # at most 448 and lies above 224: at least 2^-14 of it)
+    far = 2.0 ** -21 * (q0.abs().amax(-1)[..., None] * k.abs().sum(-1)[:, None] +
+                        q0.abs().sum(-1)[..., None] * k.abs().amax(-1)[:, None]).reshape(hq, n)
+    bound = (mag * ((d + 8) * 2.0 ** -23 + 2.0 ** -20) + (far if power > 6 else 0.0)) * scale / math.log(2) + 1e-30
+    err = (rs.double().cpu() - want).abs()
+    assert bool((err <= bound).all()), float((err / bound).max())
+
+
+# ----------------------------------------------------------- values near nothing
+def test_weights_over_blocks_of_zeros_count():
+    """2^20 positions whose values are zeros (the least scale), each with a
+    weight 2^-26.1 of the one position that has a value: together 1.4 % of the sum."""
+    d, n = 128, 1 << 20
+    zeros = torch.zeros(1, n, d, dtype=torch.uint8).view(torch.float8_e4m3fn)
+    byte = torch.full((1, n // 64), 27, dtype=torch.uint8)
+    k_tail, v_tail = torch.zeros(1, 1, d), torch.ones(1, 1, d)
+    q = torch.zeros(1, 1, d)
+    q[..., 0] = 1.0
+    k_tail[..., 0] = 26.125
+    c = dict(k8=zeros, v8=zeros.clone(), k_scale=byte, v_scale=byte.clone(),
+             k_tail=k_tail.to(torch.bfloat16), v_tail=v_tail.to(torch.bfloat16))
+    cache = L.KvCacheQ8(**{k: x.cuda() for k, x in c.items()}, n_q8=n, n_tail=0)
+    out = L.tree_verify_attn_q8(q.to(torch.bfloat16).cuda(), cache, [-1], softmax_scale=math.log(2))
+    want = 1.0 / (1.0 + n * 2.0 ** -26.125)
+    # its one rounding, the weights' (each way) and the sum of 2^20 terms in 32 bits
+    assert float((out.double().cpu() - want).abs().max()) <= (2.0 ** -8 + 2.0 ** -8 * (1 - want)) * want + 2.0 ** -12
+
+
+# ------------------------------------------------------------ rotation of long prompts
+@pytest.mark.parametrize("hq,hkv,d,rot,inter,n", [
+    (8, 2, 128, 128, False, 2303), (8, 2, 128, 128, True, 8190), (4, 2, 64, 64, False, 8190),
+    (4, 2, 64, 32, True, 2303), (5, 1, 128, 64, False, 4801), (3, 3, 64, 20, False, 2303),
+    (0, 2, 128, 96, True, 8190),
+])
+def test_rope_append_of_long_prompts(hq, hkv, d, rot, inter, n):
+    """Runs of several tokens per CTA, the last one short."""
+    rng = np.random.default_rng(n + rot)
+    fused = P8.bf16(rng, n, (hq + 2 * hkv) * d).reshape(n, hq + 2 * hkv, d)
+    q, k, v = fused.cuda().split([hq, hkv, hkv], 1)
+    freq, m = L.rope_inv_freq(rot, 500000.0, "wavelength", 8.0, 1.0, 4.0, 8192.0)
+    cap, row0, pos0 = n + 5, 2, 24571
+    kc, vc = (torch.full((hkv, cap, d), 3.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    got = L.rope_append(q if hq else None, k, v, kc, vc, row0, pos0, freq.cuda(), interleaved=inter, mscale=m)
+    cq, ck, cv = fused.split([hq, hkv, hkv], 1)
+    for x, y in ((cq, got), (ck, kc[:, row0:row0 + n].transpose(0, 1))):
+        if x.shape[1] == 0:
+            continue
+        want = P8.rotate(x, range(pos0, pos0 + n), freq, inter, m)
+        bound = 2.0 ** -8 * want.abs() + P8.rotate_bound(x, freq, inter, m)
+        assert bool(((y.cpu().double() - want).abs() <= bound).all())
+        assert torch.equal(y[..., rot:].cpu(), x[..., rot:])
+    assert torch.equal(vc[:, row0:row0 + n].cpu(), cv.transpose(0, 1))
+    for x in (kc, vc):
+        assert bool((x[:, :row0] == 3.0).all()) and bool((x[:, row0 + n:] == 3.0).all())
