@@ -214,12 +214,8 @@ def _host_i32(a):
     return arr, arr.ctypes.data_as(ctypes.c_void_p)
 
 
-def _int(name, x, bits=32):
-    """x as the C ABI's signed integer (ctypes would cut what lies outside)."""
-    x = int(x)
-    if not -1 << bits - 1 <= x < 1 << bits - 1:
-        raise ValueError(f"{name} must be a signed {bits}-bit integer")
-    return x
+# one past the C ABI's integers (ctypes would cut what lies outside)
+_C_INT, _C_INT64 = 1 << 31, 1 << 63
 
 
 def _parent_arg(parent, n):
@@ -607,10 +603,13 @@ def rope_append(q, k, v, k_cache, v_cache, row0: int, pos0: int, inv_freq, paren
         _check_dev("inv_freq", inv_freq, torch.float32, dev)
         rot = 2 * inv_freq.numel()
     par, par_p = (None, None) if parent is None else _parent_arg(parent, n)
+    row0, pos0 = int(row0), int(pos0)
+    if not (-_C_INT64 <= row0 < _C_INT64 and -_C_INT64 <= pos0 < _C_INT64):
+        raise ValueError("row0 and pos0 must be signed 64-bit integers")
     _raise(_lib().ts_rope_append(
-        _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, hq, hkv, d, n, par_p, _int("pos0", pos0, 64),
+        _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, hq, hkv, d, n, par_p, pos0,
         _ptr(inv_freq) if rot else None, rot, int(bool(interleaved)), float(mscale),
-        _ptr(q_out) if hq else None, _ptr(k_cache), _ptr(v_cache), cap, _int("row0", row0, 64),
+        _ptr(q_out) if hq else None, _ptr(k_cache), _ptr(v_cache), cap, row0,
         _stream(stream, dev)), "ts_rope_append")
     return q_out
 
@@ -639,10 +638,12 @@ def kv_quantize_q8(k, v, row0: int, n_rows: int, k8, v8, k_scale, v_scale, dst_r
     if k.dim() != 3 or v.shape != k.shape or k.shape[0] != k8.shape[0] or k.shape[2] != k8.shape[2]:
         raise ValueError("k / v / k8 / v8 shapes disagree")
     hkv, cap, d = k.shape
+    row0, n_rows, dst_row = int(row0), int(n_rows), int(dst_row)
+    if not (-_C_INT64 <= row0 < _C_INT64 and -_C_INT <= n_rows < _C_INT and -_C_INT64 <= dst_row < _C_INT64):
+        raise ValueError("row0 and dst_row must be signed 64-bit integers, n_rows a 32-bit integer")
     _raise(_lib().ts_kv_quantize_q8(
-        _ptr(k), _ptr(v), cap, hkv, d, _int("row0", row0, 64), _int("n_rows", n_rows), _ptr(k8), _ptr(v8),
-        _ptr(k_scale), _ptr(v_scale), k8.shape[1], _int("dst_row", dst_row, 64), _stream(stream, dev)),
-        "ts_kv_quantize_q8")
+        _ptr(k), _ptr(v), cap, hkv, d, row0, n_rows, _ptr(k8), _ptr(v8), _ptr(k_scale), _ptr(v_scale),
+        k8.shape[1], dst_row, _stream(stream, dev)), "ts_kv_quantize_q8")
     return k8, v8, k_scale, v_scale
 
 
@@ -864,7 +865,9 @@ def kv_select_from_scores_q8(root_scores, cache: KvCacheQ8, n_sink: int, budget:
     hq, n_ctx, hkv = root_scores.shape[0], cache.n_ctx, st.n_heads_kv
     if root_scores.shape[1] != n_ctx:
         raise ValueError("root_scores must be [Hq, n_ctx]")
-    n_sink, budget = _int("n_sink", n_sink), _int("budget", budget)
+    n_sink, budget = int(n_sink), int(budget)
+    if not (-_C_INT <= n_sink < _C_INT and -_C_INT <= budget < _C_INT):
+        raise ValueError("n_sink and budget must be signed 32-bit integers")
     n_keep = min(n_ctx, n_sink + budget)
     k_partial, v_partial = _q8_partials(cache, n_keep, k_partial, v_partial, dev, stream)
     if idx_out is None:
