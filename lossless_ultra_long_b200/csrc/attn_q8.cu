@@ -13,7 +13,7 @@
 //
 // Bound: short contexts, where a call is a chain of latencies (the launch, one
 // or two tiles, the combine): 8 heads of 64 over 2, 13 nodes, 2048 positions
-// 8.8 us; one node, 212 positions 6.5 us.
+// 8.6 us; one node, 212 positions 6.2 to 8 us.
 //
 // Work split: grid (splits, Hkv, row blocks).  A CTA streams a contiguous
 // range of tiles: a tile is one 64-row block of the 8-bit cache or 64 rows
@@ -34,8 +34,8 @@ constexpr int kTile = kQ8Block;
 constexpr int kStages = 3;
 constexpr int kMaxWarps = 12;    // 192 query rows per CTA
 // Contexts of at most so many tiles are one split: two tiles in turn cost less
-// than two splits and their combine.  Four tiles (212 positions, D = 64) are
-// 6.5 us as four splits with their combine and 10.2 us as one split.
+// than the meeting of two splits.  Four tiles (212 positions, D = 64) are
+// 6.2 us as four splits with their combine and 10.2 us as one split.
 constexpr int kOneSplit = 2;
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p)
@@ -174,16 +174,19 @@ __device__ __forceinline__ void write_row(__nv_bfloat16 *out, int row, const flo
 
 template <int D>
 __global__ void __launch_bounds__(kMaxWarps * 32, 1)
-attn_q8_kernel(AttnQ8Args a, TreeMasks masks, int tiles_per_split, int n_split)
+attn_q8_kernel(AttnQ8Args a, TreeMasks masks, int tiles_per_split, int n_split, int meet)
 {
     extern __shared__ __align__(128) unsigned char smem[];
     // tail tile: rows with a value that is no number, and those of K among them
     __shared__ unsigned long long odd_rows, odd_keys;
+    __shared__ uint32_t gave_up;
     constexpr int TB = Shape<D>::kTileBytes;
     const Q8Cache &kc = a.c;
 
-    if (threadIdx.x == 0)
+    if (threadIdx.x == 0) {
+        gave_up = 0u;
         sm100::launch_dependents();
+    }
     sm100::grid_dependency_wait();   // what the previous kernel wrote
     const int split = blockIdx.x, g = blockIdx.y;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -466,13 +469,40 @@ attn_q8_kernel(AttnQ8Args a, TreeMasks masks, int tiles_per_split, int n_split)
                     make_float2(m_run[hi], l_run[hi]);
         }
     }
+    if (!meet)
+        return;
+
+    // ---- few splits and rows (a cooperative launch): once every split of
+    // these rows has arrived, each folds every n_split-th row
+    WorkspaceHeader *hdr = reinterpret_cast<WorkspaceHeader *>(a.workspace);
+    int32_t *ctr = reinterpret_cast<int32_t *>(reinterpret_cast<char *>(a.workspace) + kHeaderBytes) +
+                   4 * (g * gridDim.z + blockIdx.z);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        __threadfence();   // the partials before the arrival
+        atomicAdd(&ctr[1], 1);
+        wait_count_bounded(&ctr[1], n_split, &gave_up, hdr);
+    }
+    __syncthreads();
+    const int row0 = blockIdx.z * nthreads / 2, row1 = min(R, row0 + nthreads / 2);
+    if (!*(volatile uint32_t *)&gave_up) {
+        for (int r = row0 + split + warp * n_split; r < row1; r += (nthreads / 32) * n_split) {
+            const int row = (r / G) * a.n_heads_q + g * G + r % G;
+            float acc[D / 32] = {}, L = 0.f;
+            add_splits<D>(ws_o, ws_ml, row, rows_all, 0, 1, n_split,
+                          row_max(ws_ml, row, rows_all, n_split), acc, L);
+            write_row<D>(a.out, row, acc, L);
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x == 0 && atomicAdd(&ctr[2], 1) == n_split - 1) {
+        atomicExch(&ctr[1], 0);
+        atomicExch(&ctr[2], 0);
+    }
 }
 
-// The combine (a dependent launch: it starts while the splits run), `per_row`
-// warps to a row.  A launch of its own also where few splits fold few rows: 8 heads
-// of 64 over 2, one node, 212 positions 6.5 us against 7.6 where the splits wait for
-// one another and fold their rows themselves in one cooperative launch; eager calls
-// take the host's 10 us either way.
+// The combine as a launch of its own (dependent: it starts while the splits
+// run), `per_row` warps to a row.
 template <int D>
 __global__ void __launch_bounds__(256)
 attn_q8_combine_kernel(const float *__restrict__ ws_o, const float *__restrict__ ws_ml,
@@ -508,6 +538,7 @@ attn_q8_combine_kernel(const float *__restrict__ ws_o, const float *__restrict__
 
 struct SplitPlan {
     int warps, row_blocks, n_split, tiles_per_split;
+    bool meet;   // the splits combine their rows themselves
 };
 
 SplitPlan make_plan(int n_heads_q, int n_heads_kv, int n_q8, int n_tail, int n_tree, int num_sms)
@@ -524,6 +555,13 @@ SplitPlan make_plan(int n_heads_q, int n_heads_kv, int n_q8, int n_tail, int n_t
         want = 1;
     p.tiles_per_split = (n_tiles + want - 1) / want;
     p.n_split = (n_tiles + p.tiles_per_split - 1) / p.tiles_per_split;
+    // One launch, without a combine of its own, where a warp has no more than
+    // one row to fold, of no more splits than it loads at once: 8 heads of 64
+    // over 2, T = 1, 212 positions 7.7 us a call against 9.6 (the host's time
+    // of two launches); T = 13 there, four rows a warp, 13.4 against 10.9.
+    const int warps = p.warps < 4 ? 4 : p.warps;
+    p.meet = p.n_split > 1 && p.n_split <= kB && R <= p.n_split * warps * p.row_blocks &&
+             n_heads_kv * p.row_blocks <= kQ8MaxSets;
     return p;
 }
 
@@ -546,10 +584,27 @@ cudaError_t launch_d(const AttnQ8Args &a, const TreeMasks &masks, const SplitPla
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess)
         return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.n_split, a.n_heads_kv, p.row_blocks);
     // at least 4 warps: they also turn the codes into bf16
-    e = launch_pdl(attn_q8_kernel<D>, dim3(p.n_split, a.n_heads_kv, p.row_blocks),
-                   dim3((p.warps < 4 ? 4 : p.warps) * 32), smem, stream, a, masks, p.tiles_per_split, p.n_split);
-    if (e != cudaSuccess || p.n_split == 1)
+    cfg.blockDim = dim3((p.warps < 4 ? 4 : p.warps) * 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    // cooperative where the splits wait for one another (at most one CTA per SM)
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeCooperative;
+    at[1].val.cooperative = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = p.meet ? 2 : 1;
+    e = cudaLaunchKernelEx(&cfg, attn_q8_kernel<D>, a, masks, p.tiles_per_split, p.n_split, (int)p.meet);
+    if (e == cudaSuccess)
+        e = cudaGetLastError();
+    if (e != cudaSuccess)
+        return e;
+    count_launches(1);
+    if (p.meet || p.n_split == 1)
         return e;
     const int rows_all = a.n_tree * a.n_heads_q;
     const float *ws_o = reinterpret_cast<const float *>(
