@@ -13,7 +13,7 @@
 //
 // Bound: short contexts, where a call is a chain of latencies (the launch, one
 // or two tiles, the combine): 8 heads of 64 over 2, 13 nodes, 2048 positions
-// 8.6 us; one node, 212 positions 6.2 to 8 us.
+// 9.0 us; one node, 212 positions 7.6 us.
 //
 // Work split: grid (splits, Hkv, row blocks).  A CTA streams a contiguous
 // range of tiles: a tile is one 64-row block of the 8-bit cache or 64 rows
@@ -35,7 +35,7 @@ constexpr int kStages = 3;
 constexpr int kMaxWarps = 12;    // 192 query rows per CTA
 // Contexts of at most so many tiles are one split: two tiles in turn cost less
 // than the meeting of two splits.  Four tiles (212 positions, D = 64) are
-// 6.2 us as four splits with their combine and 10.2 us as one split.
+// 6.5 us as four splits with their combine and 10.2 us as one split.
 constexpr int kOneSplit = 2;
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p)
@@ -541,7 +541,7 @@ struct SplitPlan {
     bool meet;   // the splits combine their rows themselves
 };
 
-SplitPlan make_plan(int n_heads_q, int n_heads_kv, int n_q8, int n_tail, int n_tree, int num_sms)
+SplitPlan make_plan(int n_heads_q, int n_heads_kv, int head_dim, int n_q8, int n_tail, int n_tree, int num_sms)
 {
     SplitPlan p;
     const int R = (n_heads_q / n_heads_kv) * n_tree;
@@ -555,12 +555,15 @@ SplitPlan make_plan(int n_heads_q, int n_heads_kv, int n_q8, int n_tail, int n_t
         want = 1;
     p.tiles_per_split = (n_tiles + want - 1) / want;
     p.n_split = (n_tiles + p.tiles_per_split - 1) / p.tiles_per_split;
-    // One launch, without a combine of its own, where a warp has no more than
-    // one row to fold, of no more splits than it loads at once: 8 heads of 64
-    // over 2, T = 1, 212 positions 7.7 us a call against 9.6 (the host's time
-    // of two launches); T = 13 there, four rows a warp, 13.4 against 10.9.
+    // One launch, without a combine of its own, for heads of 64 where a warp has no
+    // more than one row to fold, of no more splits than it loads at once: it spares
+    // the host a launch.  8 heads of 64 over 2, T = 1, 212 positions, one launch
+    // against two: a loop of calls 9.2 to 10.2 us against 10.4 to 10.6, but one call
+    // waited for 22 against 21 and the GPU's time 7.6 against 6.5 (the cooperative
+    // launch and the splits' meeting).  T = 13 there, four rows a warp, 14.5 against
+    // 10.0 in a loop; heads of 128, 4 over 4, 265 positions, 12.3 against 10.5.
     const int warps = p.warps < 4 ? 4 : p.warps;
-    p.meet = p.n_split > 1 && p.n_split <= kB && R <= p.n_split * warps * p.row_blocks &&
+    p.meet = head_dim == 64 && p.n_split > 1 && p.n_split <= kB && R <= p.n_split * warps * p.row_blocks &&
              n_heads_kv * p.row_blocks <= kQ8MaxSets;
     return p;
 }
@@ -569,10 +572,10 @@ SplitPlan make_plan(int n_heads_q, int n_heads_kv, int n_q8, int n_tail, int n_t
 // tiles a split takes in turn, from a short start; the other's start (TMEM,
 // barriers, the tail's keys, the meeting of the splits) costs 13 us or more
 // whatever the length.  Heads of 128, this kernel against the other: up to two
-// tiles in turn, 32 heads over 8 at 2048 positions T = 1 14.0 and 15.9 us,
-// T = 40 20.8 and 22.7; 8 over 1 at 16K T = 1 17.4 and 20.6; three, 32 over 8
-// at 2.5K T = 40 24.8 and 24.7, 32 over 32 at 768 T = 1 17.0 and 16.3, 8 over 1
-// at 12K T = 40 26.7 and 24.4.
+// tiles in turn, 32 heads over 8 at 2048 positions T = 1 14.1 and 16.7 us,
+// T = 40 21.0 and 23.4; 8 over 1 at 16K T = 1 17.1 and 22.7; three, 32 over 8
+// at 2.5K T = 40 25.0 and 23.5 (T = 1 15.3 and 17.0), 32 over 32 at 768 T = 1 19.6
+// and 16.5, 8 over 1 at 12K T = 40 27.2 and 23.3.
 bool long_enough(const SplitPlan &p) { return p.tiles_per_split > 2; }
 
 template <int D>
@@ -622,7 +625,7 @@ cudaError_t launch_d(const AttnQ8Args &a, const TreeMasks &masks, const SplitPla
 size_t attn_q8_workspace_bytes(int n_heads_q, int n_heads_kv, int head_dim, int n_q8, int n_tail,
                                int n_tree, int num_sms)
 {
-    const SplitPlan p = make_plan(n_heads_q, n_heads_kv, n_q8, n_tail, n_tree, num_sms);
+    const SplitPlan p = make_plan(n_heads_q, n_heads_kv, head_dim, n_q8, n_tail, n_tree, num_sms);
     size_t bytes = kHeaderBytes + kQ8SyncBytes +
                    align_up((size_t)p.n_split * n_tree * n_heads_q * (head_dim + 2) * sizeof(float), 256);
     // large enough for whichever kernel the launch picks
@@ -637,7 +640,7 @@ size_t attn_q8_workspace_bytes(int n_heads_q, int n_heads_kv, int head_dim, int 
 cudaError_t attn_q8_launch(const AttnQ8Args &a, const TreeMasks &masks, int num_sms,
                            cudaStream_t stream)
 {
-    const SplitPlan p = make_plan(a.n_heads_q, a.n_heads_kv, a.c.n_q8, a.c.n_tail, a.n_tree, num_sms);
+    const SplitPlan p = make_plan(a.n_heads_q, a.n_heads_kv, a.head_dim, a.c.n_q8, a.c.n_tail, a.n_tree, num_sms);
     // the tcgen05 kernel needs scores that grow with the products, and leaves
     // root scores for groups of up to 8 heads
     if (long_enough(p) && a.scale_log2 > 0.f && (!a.root_scores || a.n_heads_q / a.n_heads_kv <= 8) &&
