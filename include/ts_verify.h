@@ -461,12 +461,22 @@ TS_API int ts_kv_quantize_q8(const void *k, const void *v, int64_t src_cap, int 
  *  root_scores_out  device fp32 [Hq, n_q8 + n_tail], or NULL.
  *  workspace    device, >= ts_tree_verify_attn_q8_workspace_size(...) bytes;
  *               its counters lie where other entry points keep scratch, so
- *               it serves this one alone.
+ *               it serves this one alone (calls of any shapes, one after the
+ *               other).
  * The result is formed in 32 bits before its rounding: weights times values
  * of V past 2^60 may overflow.
  * Other arguments as for ts_tree_verify_attn.  A position that a row does
  * not see does not affect it, whatever its K and V hold; a row that sees a
- * key or value row with an infinity or a NaN comes out as NaN.
+ * key or value row with an infinity or a NaN comes out as NaN.  A root score
+ * depends on its key alone.
+ *
+ * The same call on the same device gives the same bits, outputs and scores.
+ * How the weights are rounded depends on the kernel that the sizes choose: two
+ * bf16 parts, or, with head_dim 128 and long contexts, one, off the exact
+ * result by up to 2^-8 of sum_j w_j |v_j - out| before the result's own
+ * rounding.  There the queries and the tail's keys enter as two 8-bit parts,
+ * without loss for elements down to 2^-14 of their row's largest; smaller ones
+ * may be off by 2^-21 of that largest.
  */
 TS_API size_t ts_tree_verify_attn_q8_workspace_size(int n_heads_q, int n_heads_kv, int head_dim,
                                                     int n_q8, int n_tail, int n_tree);
@@ -552,7 +562,9 @@ TS_API int ts_rope_append(const void *q, int64_t q_stride, const void *k, int64_
  *                      0.1 ln(factor) + 1 for a factor above 1;
  *                      params {factor, ctx, fast, slow}
  * (YaRN: Peng et al., "YaRN: Efficient Context Window Extension of Large
- * Language Models", section 3.)  All params > 0, base > 1.
+ * Language Models"; the ramp of its section 3 is linear in the turns that a
+ * frequency makes, the one here, which models in use follow, in the pair's index.)
+ * All params > 0, base > 1.
  */
 #define TS_ROPE_PLAIN 0
 #define TS_ROPE_LINEAR 1

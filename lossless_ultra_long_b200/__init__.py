@@ -789,7 +789,8 @@ def tree_verify_attn_q8(q, cache: KvCacheQ8, parent, out=None, workspace=None,
     """Tree-masked attention over an 8-bit cache (``ts_tree_verify_attn_q8``);
     the tree's rows lie in the tail behind the context.  q: bf16 [T, Hq, D];
     returns bf16 [T, Hq, D].  ``root_scores_out``: fp32 [Hq, n_ctx], as for
-    :func:`tree_verify_attn`."""
+    :func:`tree_verify_attn`.  A workspace that is kept serves this function
+    alone: it has to come back as the last call of it left it."""
     _check_dev("q", q, _BF16)
     dev, st = _call_cache(cache)
     if q.device != dev:

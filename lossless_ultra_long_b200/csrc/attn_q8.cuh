@@ -69,8 +69,8 @@ cudaError_t attn_q8_t128_launch(const AttnQ8Args &a, const TreeMasks &masks, int
                                 cudaStream_t stream);
 
 // Both attention kernels' workspaces: header, this region (four counters per
-// set of splits that meet, zero between calls, so that one workspace serves
-// calls of any shape), then scratch.
+// set of splits that meet, the tcgen05 kernel's; zero between calls, so that one
+// workspace serves calls of any shape), then scratch.
 constexpr size_t kQ8SyncBytes = 4096;
 constexpr int kQ8MaxSets = (int)kQ8SyncBytes / 16;
 

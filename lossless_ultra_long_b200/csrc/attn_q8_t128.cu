@@ -51,11 +51,11 @@
 //
 // What bounds it, at 102400 positions (8 KV heads, 210 MB: 32 us of HBM time):
 // up to 16 query rows a head 51 us, the conversion of V the largest part (8 us
-// without it) and shared memory, of which a tile moves some 150 KB; 52 rows 58
-// us; 160 rows 96 us, the exponentials and the order of the tiles' steps (two
+// without it) and shared memory, of which a tile moves some 150 KB; 52 rows 57
+// us; 160 rows 95 us, the exponentials and the order of the tiles' steps (two
 // query blocks leave room for one bf16 V tile).  32 KV heads of 4 rows (839 MB)
-// 190 us, on the 128 SMs that 32 heads divide into.  Under calls without a pause
-// the clock falls to 1.65 GHz at the power limit (57, 110 and 222 us).
+// 186 us, on the 128 SMs that 32 heads divide into.  Under calls without a pause
+// the clock falls to 1.65 GHz at the power limit (59, 111 and 223 us).
 //
 // Every wait is bounded (about a second): on expiry the kernel records
 // TS_ERR_TIMEOUT in the workspace status word, all roles leave their loops,
@@ -90,8 +90,8 @@ constexpr int kTmemCols = 512;
 constexpr int kQ1Bytes = 2 * kBlockM * kD;   // Q of block 1 in shared memory: hi, lo
 constexpr float kMaxRowSum = 9.223372036854775808e18f;   // 2^63
 // 8-bit tiles that the others stream while a split makes its tail tile ready.
-// 102400 positions of 8 heads, 1, 4, 6 of them: one query row a head 56.0, 53.0,
-// 51.3 us, 40 nodes 103, 97.8, 97.7 us (run-time hand-out: 51.9 and 96.1)
+// 102400 positions of 8 heads, 3, 4, 5, 6 of them: one query row a head 54.0, 52.8,
+// 52.1, 51.0 us, 40 nodes 97.1, 95.5, 95.8, 95.1
 constexpr int kTailCost = 6;
 constexpr int kTailWarps = 4;                // warps 16-19, which also turn the tail tiles
 constexpr size_t kSmemLimit = 232448;        // dynamic shared memory per CTA
