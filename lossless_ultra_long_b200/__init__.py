@@ -249,6 +249,14 @@ def _raise(rc, where):
         raise TsError(rc, where)
 
 
+def _on(stream):
+    """The context of a stream, which need not be torch's own kind: any object with
+    its handle, as the calls take."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
+    return torch.cuda.stream(stream)
+
+
 # A call's own buffers are made on the stream that it runs on: a workspace's
 # zeros are there before the kernel reads them, and memory that is freed when
 # the call returns goes to what this stream runs next, not to another's work.
@@ -257,7 +265,7 @@ def new_workspace(nbytes: int, device=None, stream=None) -> torch.Tensor:
     aligned), made on ``stream`` (None: the current one), behind which a call
     on another stream has to be ordered."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream):
             return new_workspace(nbytes, device)
     return torch.zeros(max(int(nbytes), 256), dtype=torch.uint8,
                        device=device if device is not None else "cuda")
@@ -265,7 +273,7 @@ def new_workspace(nbytes: int, device=None, stream=None) -> torch.Tensor:
 
 def _empty(shape, dtype, device, stream):
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream):
             return torch.empty(shape, dtype=dtype, device=device)
     return torch.empty(shape, dtype=dtype, device=device)
 
@@ -761,7 +769,7 @@ class KvCacheQ8:
         if self.tail_row0:
             _call_device("k_tail", self.k_tail)
             n, at = self.n_tail, self.tail_row0
-            with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+            with contextlib.nullcontext() if stream is None else _on(stream):
                 for t in (self.k_tail, self.v_tail) if n else ():
                     left = t[:, at:at + n]
                     t[:, :n].copy_(left if at >= n else left.clone())

@@ -83,6 +83,7 @@ def test_a_call_makes_its_buffers_on_its_stream(monkeypatch, name, given):
 
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle: STREAM)
     monkeypatch.setattr(L, "_raw_stream", lambda index: 0)
     call = CALLS[name]
     for n, f in (("zeros", device_buffer), ("empty", device_buffer), ("empty_like", like)):

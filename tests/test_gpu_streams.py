@@ -1,5 +1,7 @@
 """Calls on a stream of their own, with nothing but their inputs given, while the
 current stream is busy: their outputs and workspaces are not that stream's."""
+import types
+
 import pytest
 import torch
 
@@ -80,3 +82,16 @@ def test_a_call_on_its_own_stream(data, name):
             assert float((x - y.cpu()).abs().max()) <= 2e-4
         else:
             assert torch.equal(x, y.cpu())
+
+
+def test_a_stream_that_is_only_a_handle(data):
+    """Any object with a stream's handle serves, the default stream's 0 among them."""
+    data["tree"] = P8.parents("bfs", T)
+    s = torch.cuda.Stream()
+    want = L.tree_verify_attn_q8(data["q"], data["cache"], data["tree"])
+    torch.cuda.synchronize()
+    for handle in (s.cuda_stream, 0):
+        out = L.tree_verify_attn_q8(data["q"], data["cache"], data["tree"],
+                                    stream=types.SimpleNamespace(cuda_stream=handle))
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
