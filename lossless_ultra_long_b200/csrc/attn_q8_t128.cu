@@ -591,6 +591,12 @@ __device__ __noinline__ void tile_exact(const AttnQ8Args &a, unsigned long long 
                 continue;
             const int64_t at = (int64_t)g * kc.tail_cap + r0 + i;
             const uint2 kb = *reinterpret_cast<const uint2 *>(kc.k_tail + at * kD + 4 * lane);
+            const uint2 vb = *reinterpret_cast<const uint2 *>(kc.v_tail + at * kD + 4 * lane);
+            // a key or a value that is no number, anywhere in its row
+            if (__any_sync(0xffffffffu, top_of(top_word(make_uint4(kb.x, kb.y, vb.x, vb.y))) >= 0x7F80u)) {
+                l = __uint_as_float(0x7FC00000u);
+                continue;
+            }
             k0 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&kb.x));
             k1 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&kb.y));
             v = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(kc.v_tail + at * kD + dv));

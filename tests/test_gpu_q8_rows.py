@@ -174,6 +174,35 @@ def test_root_scores_do_not_depend_on_values(hq, hkv, d, n_q8, what):
     assert bool(((got - wr).abs() <= br).all()), float(((got - wr).abs() / br).max())
 
 
+@pytest.mark.parametrize("hq,hkv,d,n_q8,n_tail", [(8, 2, 64, 2048, 9), (74, 74, 128, 4096, 9), (740, 37, 128, 2048, 9),
+                                                  (600, 20, 128, 6144, 9)])
+@pytest.mark.parametrize("what", [-math.inf, math.nan])
+def test_a_row_that_sees_no_number_is_nan_where_scores_rise(hq, hkv, d, n_q8, n_tail, what):
+    """Scores that outgrow a split's reference (its rows are computed again) beside
+    one element of a branch's value, or key, that is no number."""
+    t, rise = 5, 200.0
+    q = P8.bf16(np.random.default_rng(85), t, hq * d).reshape(t, hq, d)
+    q[:] = q[:1, :1]
+    dirn = q[0, 0].double() / q[0, 0].double().norm()
+    ramp = torch.linspace(0, 1, n_q8, dtype=torch.float64) * rise * math.sqrt(d) / float(q[0, 0].double().norm())
+    parent = [-1, 0, 0, 1, 2]
+    vis = P8.sees(parent)
+    for flip in (False, True):
+        c = P8.cache_inputs(86, hkv, d, n_q8, n_tail, t)
+        rows = (ramp.flip(0) if flip else ramp)[None, :, None] * dirn
+        codes, byte = P8.quantize(rows.expand(hkv, n_q8, d).to(torch.bfloat16))
+        c["k8"], c["k_scale"] = codes.float().to(torch.float8_e4m3fn), byte
+        k, v = (P8.cache_rows(c, x, n_q8, 0, n_tail + t) for x in "kv")
+        want, bound, _, _ = P8.attention(q, k, v, n_q8 + n_tail, parent, d ** -0.5)
+        c["v_tail"][:, n_tail + 2, 7] = what
+        c["k_tail"][:, n_tail + 3, d - 2] = what
+        cache = L.KvCacheQ8(**{x: y.cuda() for x, y in c.items()}, n_q8=n_q8, n_tail=n_tail)
+        out = L.tree_verify_attn_q8(q.cuda(), cache, parent).double().cpu()
+        hit = vis[:, 2] | vis[:, 3]
+        assert bool(torch.isnan(out[hit]).all()), flip
+        assert bool(((out - want).abs() <= bound)[~hit].all()), flip
+
+
 @pytest.mark.parametrize("hq,hkv,n_tail,t", [(74, 74, 2500, 3), (592, 74, 2000, 12), (592, 74, 1900, 16),
                                              (296, 74, 1500, 40)])
 def test_many_tail_tiles_with_keys_that_are_no_numbers(hq, hkv, n_tail, t):
