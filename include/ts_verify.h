@@ -457,7 +457,8 @@ TS_API int ts_kv_quantize_q8(const void *k, const void *v, int64_t src_cap, int 
  *  q            device bf16 [n_tree, Hq, D].
  *  cache        HOST struct, read before the call returns;
  *               tail_row0 + n_tail + n_tree <= tail_cap.
- *  out          device bf16 [n_tree, Hq, D], written entirely.
+ *  out          device bf16 [n_tree, Hq, D], written entirely; not
+ *               overlapping q.
  *  root_scores_out  device fp32 [Hq, n_q8 + n_tail], or NULL.
  *  workspace    device, >= ts_tree_verify_attn_q8_workspace_size(...) bytes;
  *               its counters lie where other entry points keep scratch, so

@@ -21,8 +21,9 @@
 // products: the converter warps scale its keys, each row by a power of two of its
 // own (no row takes another's bits, whatever its size), split them like the
 // queries into an e4m3 and an e5m2 tile (two K slots, four products), and copy V;
-// the scores take the keys' scales where the masks are evaluated.  Rows with an infinity or a NaN are zeroed there and noted;
-// a query row that sees one gets a NaN sum.
+// the scores take the keys' scales where the masks are evaluated.  Rows with an
+// infinity or a NaN are zeroed there and noted; a query row that sees one gets a NaN
+// sum.
 //
 // Softmax layout, reference maximum (fixed at a row's first tile), partials, and
 // the combine by the splits themselves follow the bf16 kernel in attn_t128.cu;
@@ -137,8 +138,8 @@ struct Aux {
     Bars bar;
     // per tile and half, posted with tile_of: K's scale (1 on a tail tile), V's
     // as an exponent, V's inverse, and (as an int) how many of the half's positions
-    // are context, kTailMark added on a tail tile, or kEndMark.  A block that is NaN, in K or V, has a NaN exponent and
-    // inverse: its weights and sums are NaN.
+    // are context, kTailMark added on a tail tile, or kEndMark.  A block that is
+    // NaN, in K or V, has a NaN exponent and inverse: its weights and sums are NaN.
     float4 scale_of[kTileRing][2];
     unsigned long long anc[TS_MAX_TREE];
     float2 ml[2][64];               // (m, l) of each group's rows, to be merged
@@ -510,10 +511,10 @@ struct Q8Sync {
 // Which split streams which tile of a head, by counting alone.  The nt tail tiles
 // come first, one per split and round; the `busy` splits of the last such round are
 // kTailCost 8-bit tiles behind the others (the tail's keys are split and its masks
-// evaluated), so the others take so many rounds ahead of them.  The rest
-// goes round all splits, what is left of the last round to the last ones.  Tiles
-// are taken from the end of the cache backwards.  Every split has a tile as long as
-// there are no more splits than tiles.
+// evaluated), so the others take so many rounds ahead of them.  The rest goes round
+// all splits, what is left of the last round to the last ones.  Tiles are taken from
+// the end of the cache backwards.  Every split has a tile as long as there are no
+// more splits than tiles.
 struct HandOut {
     int n_split, nq, n_tiles, tail_rounds, busy, ahead, full, left;
     __device__ __forceinline__ HandOut(int n_split_, int nq_, int n_tiles_) : n_split(n_split_), nq(nq_), n_tiles(n_tiles_)

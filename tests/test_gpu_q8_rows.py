@@ -229,6 +229,49 @@ def test_many_tail_tiles_with_keys_that_are_no_numbers(hq, hkv, n_tail, t):
         assert bool(torch.isnan(out).all())
 
 
+@pytest.mark.parametrize("hq,hkv,d,n_q8", KERNELS)
+@pytest.mark.parametrize("which", ["k_scale", "v_scale"])
+def test_root_scores_of_a_block_that_is_no_number(hq, hkv, d, n_q8, which):
+    """A block of K has NaN for its scores, a block of V its keys' own."""
+    n_tail, t = 9, 4
+    c = P8.cache_inputs(87, hkv, d, n_q8, n_tail, t)
+    q = P8.bf16(np.random.default_rng(88), t, hq * d).reshape(t, hq, d)
+    k = P8.cache_rows(c, "k", n_q8, 0, n_tail)
+    c[which][1, 1] = 255
+    cache = L.KvCacheQ8(**{x: y.cuda() for x, y in c.items()}, n_q8=n_q8, n_tail=n_tail)
+    rs = torch.zeros(hq, n_q8 + n_tail, device="cuda")
+    L.tree_verify_attn_q8(q.cuda(), cache, P8.parents("chain", t), root_scores_out=rs)
+    got = rs.double().cpu().reshape(hkv, hq // hkv, -1)
+    nan = torch.zeros_like(got, dtype=torch.bool)
+    nan[1, :, 64:128] = which == "k_scale"
+    assert torch.equal(torch.isnan(got), nan)
+    kk = torch.cat([k, torch.zeros(hkv, 1, d, dtype=torch.float64)], 1)
+    _, _, wr, br = P8.attention(q[:1], kk, torch.zeros_like(kk), n_q8 + n_tail, [-1], d ** -0.5)
+    err = (got - wr.reshape(got.shape)).abs()
+    assert bool((err <= br.reshape(got.shape))[~nan].all())
+
+
+@pytest.mark.parametrize("hq,hkv,d,n_q8", KERNELS)
+@pytest.mark.parametrize("what", [math.inf, math.nan])
+def test_a_query_that_is_no_number_reaches_its_own_row(hq, hkv, d, n_q8, what):
+    n_tail, t = 9, 5
+    c = P8.cache_inputs(89, hkv, d, n_q8, n_tail, t)
+    q = P8.bf16(np.random.default_rng(84), t, hq * d).reshape(t, hq, d)
+    k, v = (P8.cache_rows(c, x, n_q8, 0, n_tail + t) for x in "kv")
+    parent = P8.parents("bfs", t)
+    want, bound, wr, br = P8.attention(q, k, v, n_q8 + n_tail, parent, d ** -0.5)
+    q[0, 1, 5], q[3, hq - 1, d - 1] = what, what
+    cache = L.KvCacheQ8(**{x: y.cuda() for x, y in c.items()}, n_q8=n_q8, n_tail=n_tail)
+    rs = torch.zeros(hq, n_q8 + n_tail, device="cuda")
+    out = L.tree_verify_attn_q8(q.cuda(), cache, parent, root_scores_out=rs).double().cpu()
+    hit = torch.zeros(t, hq, dtype=torch.bool)
+    hit[0, 1] = hit[3, hq - 1] = True
+    assert bool(torch.isnan(out[hit]).all())
+    assert bool(((out - want).abs() <= bound)[~hit].all())
+    rest = [h for h in range(hq) if h != 1]
+    assert bool(((rs.double().cpu() - wr).abs() <= br)[rest].all())
+
+
 # ------------------------------------------------------- one large element in a row
 @pytest.mark.parametrize("hq,hkv,d,n_q8", KERNELS)
 @pytest.mark.parametrize("power", [6, 12, 20])
@@ -311,3 +354,26 @@ def test_rope_append_of_long_prompts(hq, hkv, d, rot, inter, n):
     assert torch.equal(vc[:, row0:row0 + n].cpu(), cv.transpose(0, 1))
     for x in (kc, vc):
         assert bool((x[:, :row0] == 3.0).all()) and bool((x[:, row0 + n:] == 3.0).all())
+
+
+# ------------------------------------------------------------ captured calls
+def test_graphs_that_share_a_workspace_and_one_that_makes_its_own():
+    """Two captured calls of different shapes on one workspace, replayed in turn, and
+    one whose workspace and output were made while it was captured."""
+    shapes = [(16, 4, 128, 8128, 40, 13), (8, 2, 64, 192, 20, 1), (160, 40, 128, 1024, 20, 40)]
+    ws = L.new_workspace(max(L.tree_verify_attn_q8_workspace_size(*s) for s in shapes))
+    jobs = []
+    for i, shape in enumerate(shapes):
+        q, cache, parent = random_call(7 + i, *shape)
+        eager = L.tree_verify_attn_q8(q, cache, parent)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = L.tree_verify_attn_q8(q, cache, parent, workspace=ws if i < 2 else None)
+        jobs.append((graph, out, eager, cache, q))
+    for _ in range(5):
+        for graph, out, _, _, _ in jobs:
+            out.zero_()
+            graph.replay()
+        for _, out, eager, _, _ in jobs:
+            assert torch.equal(out, eager)
+    assert L.workspace_status(ws) == 0
